@@ -472,6 +472,115 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
                          akv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * A chunk of new tokens over the active cache (paper review page section 4
+ * serving flow: a history that is cached is extended by its new message; an
+ * agent's tool response is a chunk of some hundred tokens).  The four calls
+ * below run one after the other on a stream:
+ *
+ *   akv_qk_norm_append   the chunk's q, k, v rows made ready: q normalised and
+ *                        rotated, k and v in their pool slots;
+ *   akv_chunk_attention  out and log-sum-exp of every row over its request's
+ *                        list, which ends with the chunk's own slots;
+ *   akv_attention_mass   the weight those rows put on each entry of the list,
+ *                        added to what it had;
+ *   akv_evict_by_mass    each list cut to a budget, lowest mass first: the new
+ *                        list for the next decode or chunk, and the slots
+ *                        that became free.
+ *
+ * Common to the last three: lists are those of the decode calls (kv_indptr
+ * [B+1], kv_indices, device int32, keys in the pool already rotated).  q_indptr
+ * (device int32 [B+1], ascending): request b's chunk is rows q_indptr[b] ..
+ * q_indptr[b+1]-1 of the row tensors, of n_rows rows in all; rows that belong
+ * to no request are neither read nor written.  Row i of a chunk of m rows sees
+ * the first n - m + i + 1 of the list's n entries (none if that is not
+ * positive).  max_q, max_kv: host, upper bounds on the chunks' and lists'
+ * lengths; longer ones are cut to them.  A pool index outside [0, S) reads
+ * pool row 0.  All index data stays on the device, so the calls can be
+ * captured in a CUDA graph and replayed with other lengths within the bounds.
+ * Limits: B <= 65535, max_kv <= 2^30, Hq <= 65535, and grids within CUDA's
+ * limits (AKV_ERR_UNSUPPORTED otherwise). */
+
+/* Row preparation.  For token i < n and head row x of q (Hq rows) or k (Hkv):
+ *   y = x / sqrt(mean(x^2) + eps) * weight   with AKV_NORM_Q / AKV_NORM_K
+ *                                            (weight NULL = ones), else x;
+ *   z = R(pos[i]) y                          with AKV_ROPE_Q / AKV_ROPE_K.
+ * q_out[i] = z of q; k_pool[slot[i]] = z of k; v_pool[slot[i]] = v[i].
+ * q, k, v: device, token i at i * {q,k,v}_stride elements, its heads
+ * contiguous (Hq * D, Hkv * D elements), so that they may be column blocks of
+ * one projection; strides are at least the row's length.  q_out [n, Hq, D]
+ * contiguous; it may be q itself if q is contiguous.  q_weight, k_weight:
+ * device fp32 [D].  pos, slot: device int32 [n]; slots must be distinct.  A
+ * token whose slot is outside [0, S) is padding: nothing of it is read or
+ * written.  Pointers and row strides must be multiples of 16 bytes
+ * (AKV_ERR_INVALID).  For akv_decode_attention, which rotates the query
+ * itself, leave AKV_ROPE_Q out; for the raw-key pool of
+ * akv_decode_attention_rope leave out AKV_ROPE_K too. */
+enum { AKV_NORM_Q = 1, AKV_NORM_K = 2, AKV_ROPE_Q = 4, AKV_ROPE_K = 8 };
+akv_status akv_qk_norm_append(const akv_shape *shape, int32_t n, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const float *q_weight, const float *k_weight, float eps,
+                              int32_t flags, const int32_t *pos, const int32_t *slot, int32_t S,
+                              void *q_out, void *k_pool, void *v_pool, akv_stream_t stream);
+
+/* Chunk attention.  q [n_rows, Hq, D]: rotated rows, as akv_qk_norm_append
+ * leaves them.  out [n_rows, Hq, D]; lse: device fp32 [n_rows, Hq] or NULL,
+ * log(sum_j exp(s_j)) of the scaled scores.  A row that sees nothing gets
+ * zeros, and -inf.  k_pool, v_pool [S, Hkv, D].  Values in hidden entries
+ * (NaN, infinities) do not reach a row.  workspace: device, 256-byte
+ * aligned, akv_chunk_workspace() bytes for the same arguments (0: may be
+ * NULL): split-KV partials.  bf16: the weights are rounded to bf16 for the
+ * P x V product; their sum and the scores are fp32. */
+size_t akv_chunk_workspace(const akv_shape *shape, int32_t B, int32_t n_rows, int32_t max_q,
+                           int32_t max_kv);
+akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t *q_indptr,
+                               int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                               const void *v_pool, int32_t S, const int32_t *kv_indptr,
+                               const int32_t *kv_indices, int32_t max_kv, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, akv_stream_t stream);
+
+/* Attention mass.  For list entry j < n of request b:
+ *   mass_out[b * mass_stride + j] = decay * mass_in[b * mass_stride + j]
+ *     + sum over the chunk's rows i that see j, and heads h, of
+ *       exp(s_ihj - lse[i][h]),
+ * the first term only for entries older than the chunk (j < n - m: the
+ * chunk's own start at zero) and only if mass_in is given.  A row's position
+ * in the list, not its slot, carries its mass, so slots shared by several
+ * requests have one mass in each.  mass_in may be NULL or mass_out.
+ * mass_stride >= max_kv.  Entries from n on are left as they are.  lse: device
+ * fp32 [n_rows, Hq] from akv_chunk_attention; a row with -inf counts nothing.
+ * workspace: as above, akv_attention_mass_workspace() bytes. */
+size_t akv_attention_mass_workspace(const akv_shape *shape, int32_t B, int32_t n_rows,
+                                    int32_t max_q, int32_t max_kv);
+akv_status akv_attention_mass(const akv_shape *shape, int32_t B, const int32_t *q_indptr,
+                              int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                              int32_t S, const int32_t *kv_indptr, const int32_t *kv_indices,
+                              int32_t max_kv, const float *lse, float decay, const float *mass_in,
+                              float *mass_out, int64_t mass_stride, void *workspace,
+                              size_t workspace_bytes, akv_stream_t stream);
+
+/* Eviction by mass: drop(P) of section 3.3 with P chosen by weight.  Request
+ * b keeps min(max(keep[b], 0), n) entries: those of the largest mass, ties to
+ * the lowest list position.  The first n_first and last n_recent entries of a
+ * list count as +inf, a NaN mass as -inf.  Outputs, in list order:
+ *   out_indptr [B+1], out_indices, out_pos   the kept lists (kv_pos and
+ *       out_pos: both given or both NULL), for the next decode or chunk, or
+ *       for akv_repos_rotate (src_idx = out_indices, pos_from = out_pos);
+ *   out_mass [B][out_stride]                 the kept entries' masses;
+ *   dropped_indptr [B+1], dropped            the slots that left each list.
+ * All device.  keep: device int32 [B].  out_capacity: entries that out_indices
+ * and out_pos hold, dropped_capacity: those of dropped (the length of
+ * kv_indices always suffices); out_stride: masses that a row of out_mass
+ * holds.  What would go past them is not written; the index pointers count it
+ * all the same.  Outputs must not overlap inputs. */
+akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_pos, int32_t max_kv, const float *mass,
+                             int64_t mass_stride, const int32_t *keep, int32_t n_first,
+                             int32_t n_recent, int32_t *out_indptr, int32_t *out_indices,
+                             int32_t *out_pos, float *out_mass, int64_t out_stride,
+                             int64_t out_capacity, int32_t *dropped_indptr, int32_t *dropped,
+                             int64_t dropped_capacity, akv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Decoder layers of a single-prefill restoration (paper review page section
  * 4.2, Appendix A.1.1, Figure 10): attention is cut into segments, every
  * other layer op (projections, FFN) runs once over the whole batched

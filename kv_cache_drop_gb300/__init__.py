@@ -23,6 +23,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libakv.so")
 
 AKV_F32, AKV_BF16 = 0, 1
+# akv_qk_norm_append flags
+AKV_NORM_Q, AKV_NORM_K, AKV_ROPE_Q, AKV_ROPE_K = 1, 2, 4, 8
 _STATUS = {0: "AKV_OK", 1: "AKV_ERR_INVALID", 2: "AKV_ERR_CUDA", 3: "AKV_ERR_WORKSPACE",
            4: "AKV_ERR_UNSUPPORTED", 5: "AKV_ERR_DEVICE"}
 
@@ -174,6 +176,28 @@ _SIGS = {
                                            ctypes.POINTER(LayerWeights), ctypes.c_int32,
                                            ctypes.c_int32, ctypes.c_float] +
                             [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "akv_qk_norm_append": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
+                           [ctypes.c_void_p, ctypes.c_int64] * 3 + [ctypes.c_void_p] * 2 +
+                           [ctypes.c_float, ctypes.c_int32] + [ctypes.c_void_p] * 2 +
+                           [ctypes.c_int32] + [ctypes.c_void_p] * 4),
+    "akv_chunk_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] + [ctypes.c_int32] * 4),
+    "akv_chunk_attention": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32,
+                                           ctypes.c_void_p] + [ctypes.c_int32] * 2 +
+                            [ctypes.c_void_p] * 3 + [ctypes.c_int32] + [ctypes.c_void_p] * 2 +
+                            [ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                            [ctypes.c_size_t, ctypes.c_void_p]),
+    "akv_attention_mass_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] +
+                                     [ctypes.c_int32] * 4),
+    "akv_attention_mass": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32,
+                                          ctypes.c_void_p] + [ctypes.c_int32] * 2 +
+                           [ctypes.c_void_p] * 2 + [ctypes.c_int32] + [ctypes.c_void_p] * 2 +
+                           [ctypes.c_int32, ctypes.c_void_p, ctypes.c_float] +
+                           [ctypes.c_void_p] * 2 + [ctypes.c_int64, ctypes.c_void_p,
+                                                    ctypes.c_size_t, ctypes.c_void_p]),
+    "akv_evict_by_mass": (ctypes.c_int, [ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                          [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
+                          [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 4 + [ctypes.c_int64] * 2 +
+                          [ctypes.c_void_p] * 2 + [ctypes.c_int64, ctypes.c_void_p]),
     "akv_append_kv": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
                       [ctypes.c_void_p] * 6 + [ctypes.c_void_p]),
 }
@@ -545,6 +569,134 @@ def akv_decode_static_scratch_bytes() -> int:
 def akv_append_kv(shp: Shape, n: int, k_new, v_new, pos, slot, k_pool, v_pool, stream=None):
     _check(lib().akv_append_kv(ctypes.byref(shp), n, _dev(k_new), _dev(v_new), _dev(pos),
                                _dev(slot), _dev(k_pool), _dev(v_pool), _stream(stream)))
+
+
+def _typed(name: str, t, dtype, device, shape=None, rows: bool = False):
+    """Address of a tensor argument of the chunk calls: on `device`, of
+    `dtype`, contiguous (rows: only its inner dimensions), and of the given
+    shape (None: any extent).  None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, need {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {shape}")
+    if not (t.is_contiguous() or (rows and t.numel() and t[0].is_contiguous())):
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _run_on(stream):
+    """(device, raw stream) that a call without tensors' own choice uses: the
+    given stream, or the current one; its device must be the current one."""
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    if s.device_index != torch.cuda.current_device():
+        raise ValueError(f"the stream is on cuda:{s.device_index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return s.device, s.cuda_stream
+
+
+def _torch_dtype(shp: Shape):
+    import torch
+    return torch.bfloat16 if shp.dtype == AKV_BF16 else torch.float32
+
+
+def akv_qk_norm_append(shp: Shape, n: int, q, k, v, pos, slot, k_pool, v_pool, q_out,
+                       q_weight=None, k_weight=None, eps: float = 1e-6,
+                       flags: int = AKV_NORM_Q | AKV_NORM_K | AKV_ROPE_Q | AKV_ROPE_K,
+                       stream=None):
+    """Per-head norm and rotation of a chunk's q and k rows, k and v into
+    their pool slots.  q, k, v [n, heads, D] may be column blocks of one
+    projection (any stride between tokens); slots outside the pool mark
+    padding rows."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, D = _torch_dtype(shp), shp.D
+    args = [(_typed(x, t, dt, dev, (n, h, D), rows=True), t.stride(0) if n > 1 else h * D)
+            for x, t, h in (("q", q, shp.Hq), ("k", k, shp.Hkv), ("v", v, shp.Hkv))]
+    S = k_pool.shape[0]
+    _check(lib().akv_qk_norm_append(
+        ctypes.byref(shp), n, *args[0], *args[1], *args[2],
+        _typed("q_weight", q_weight, torch.float32, dev, (D,)),
+        _typed("k_weight", k_weight, torch.float32, dev, (D,)), eps, flags,
+        _typed("pos", pos, torch.int32, dev, (n,)), _typed("slot", slot, torch.int32, dev, (n,)),
+        S, _typed("q_out", q_out, dt, dev, (n, shp.Hq, D)),
+        _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
+        _typed("v_pool", v_pool, dt, dev, (S, shp.Hkv, D)), st))
+
+
+def akv_chunk_workspace(shp: Shape, B: int, n_rows: int, max_q: int, max_kv: int) -> int:
+    return lib().akv_chunk_workspace(ctypes.byref(shp), B, n_rows, max_q, max_kv)
+
+
+def akv_chunk_attention(shp: Shape, B: int, q_indptr, q, k_pool, v_pool, kv_indptr, kv_indices,
+                        max_q: int, max_kv: int, out, lse, workspace, stream=None):
+    """Attention of each request's chunk of new rows over its list, which ends
+    with the chunk's own slots; lse may be None."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, D, n, S = _torch_dtype(shp), shp.D, q.shape[0], k_pool.shape[0]
+    _check(lib().akv_chunk_attention(
+        ctypes.byref(shp), B, _typed("q_indptr", q_indptr, torch.int32, dev, (B + 1,)), n, max_q,
+        _typed("q", q, dt, dev, (n, shp.Hq, D)), _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
+        _typed("v_pool", v_pool, dt, dev, (S, shp.Hkv, D)), S,
+        _typed("kv_indptr", kv_indptr, torch.int32, dev, (B + 1,)),
+        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), max_kv,
+        _typed("out", out, dt, dev, (n, shp.Hq, D)),
+        _typed("lse", lse, torch.float32, dev, (n, shp.Hq)),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), st))
+
+
+def akv_attention_mass_workspace(shp: Shape, B: int, n_rows: int, max_q: int,
+                                 max_kv: int) -> int:
+    return lib().akv_attention_mass_workspace(ctypes.byref(shp), B, n_rows, max_q, max_kv)
+
+
+def akv_attention_mass(shp: Shape, B: int, q_indptr, q, k_pool, kv_indptr, kv_indices, max_q: int,
+                       max_kv: int, lse, decay: float, mass_in, mass_out, workspace, stream=None):
+    """mass_out [B, >= max_kv] = decay * mass_in (None: zero) plus the weight
+    the chunk's rows put on each list entry; lse from akv_chunk_attention."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, D, n, S = _torch_dtype(shp), shp.D, q.shape[0], k_pool.shape[0]
+    _check(lib().akv_attention_mass(
+        ctypes.byref(shp), B, _typed("q_indptr", q_indptr, torch.int32, dev, (B + 1,)), n, max_q,
+        _typed("q", q, dt, dev, (n, shp.Hq, D)), _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
+        S, _typed("kv_indptr", kv_indptr, torch.int32, dev, (B + 1,)),
+        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), max_kv,
+        _typed("lse", lse, torch.float32, dev, (n, shp.Hq)), decay,
+        _typed("mass_in", mass_in, torch.float32, dev, tuple(mass_out.shape)),
+        _typed("mass_out", mass_out, torch.float32, dev, (B, None)), mass_out.shape[1],
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), st))
+
+
+def akv_evict_by_mass(B: int, kv_indptr, kv_indices, kv_pos, max_kv: int, mass, keep,
+                      n_first: int, n_recent: int, out_indptr, out_indices, out_pos, out_mass,
+                      dropped_indptr, dropped, stream=None):
+    """Each list cut to keep[b] entries, lowest mass first out (mass and
+    out_mass [B, stride]); kv_pos and out_pos may both be None."""
+    import torch
+    dev, st = _run_on(stream)
+    i32, f32 = torch.int32, torch.float32
+    cap = out_indices.shape[0]
+    _check(lib().akv_evict_by_mass(
+        B, _typed("kv_indptr", kv_indptr, i32, dev, (B + 1,)),
+        _typed("kv_indices", kv_indices, i32, dev, (None,)),
+        _typed("kv_pos", kv_pos, i32, dev, tuple(kv_indices.shape)), max_kv,
+        _typed("mass", mass, f32, dev, (B, None)), mass.shape[1],
+        _typed("keep", keep, i32, dev, (B,)), n_first, n_recent,
+        _typed("out_indptr", out_indptr, i32, dev, (B + 1,)),
+        _typed("out_indices", out_indices, i32, dev, (None,)),
+        _typed("out_pos", out_pos, i32, dev, (cap,)),
+        _typed("out_mass", out_mass, f32, dev, (B, None)), out_mass.shape[1], cap,
+        _typed("dropped_indptr", dropped_indptr, i32, dev, (B + 1,)),
+        _typed("dropped", dropped, i32, dev, (None,)), dropped.shape[0], st))
 
 
 def to_device(arr: np.ndarray, dtype: str, device="cuda"):

@@ -214,4 +214,31 @@ cudaError_t launch_decode_static(int dtype, int B, int Hq, int Hkv, const void *
                                  const int32_t *indptr, const int32_t *indices, int max_kv,
                                  void *out, const RopeTheta &th, cudaStream_t s);
 
+// A chunk of new tokens over the pool: row preparation (qk_norm.cu), attention
+// (chunk.cu), attention mass (mass.cu), eviction by mass (evict.cu).
+cudaError_t launch_qk_norm_append(int dtype, int Hq, int Hkv, int n, const void *q, int64_t qs,
+                                  const void *k, int64_t ks, const void *v, int64_t vs,
+                                  const float *qw, const float *kw, float eps, int flags,
+                                  const int32_t *pos, const int32_t *slot, int S, void *q_out,
+                                  void *kp, void *vp, const RopeTheta &th, cudaStream_t s);
+// CTAs along the first grid axis of the chunk attention (its limit is 2^31 - 1)
+int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv);
+size_t chunk_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv);
+cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
+                         const int32_t *q_indptr, int max_q, const void *q, const void *k,
+                         const void *v, const int32_t *kv_indptr, const int32_t *kv_indices,
+                         int max_kv, void *out, float *lse, void *ws, cudaStream_t s);
+size_t mass_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv);
+cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
+                        const int32_t *q_indptr, int max_q, const void *q, const void *k,
+                        const int32_t *kv_indptr, const int32_t *kv_indices, int max_kv,
+                        const float *lse, float decay, const float *in, float *out, int64_t stride,
+                        void *ws, cudaStream_t s);
+cudaError_t launch_evict(int B, const int32_t *indptr, const int32_t *indices, const int32_t *pos,
+                         int max_kv, const float *mass, int64_t stride, const int32_t *keep,
+                         int n_first, int n_recent, int32_t *out_indptr, int32_t *out_indices,
+                         int32_t *out_pos, float *out_mass, int64_t out_stride,
+                         int64_t out_cap, int32_t *dropped_indptr, int32_t *dropped,
+                         int64_t dropped_cap, cudaStream_t s);
+
 }  // namespace akv

@@ -1268,6 +1268,175 @@ akv_status akv_decode_check_indices(int32_t B, const int32_t *kv_indptr, const i
 }
 
 // ------------------------------------------------------------------------
+// A chunk of new tokens over the pool
+// ------------------------------------------------------------------------
+
+namespace {
+constexpr int32_t kMaxList = 1 << 30;
+
+bool misaligned(const void *p) { return (uintptr_t)p % 16 != 0; }
+
+// what akv_chunk_attention and akv_attention_mass check alike
+akv_status check_chunk(const akv_shape *shape, int32_t B, int32_t n_rows, int32_t max_q, int32_t S,
+                       int32_t max_kv) {
+  if (akv_status st = check_shape(shape)) return st;
+  if (B < 0 || n_rows < 0 || max_q < 0 || max_kv < 0 || S < 0)
+    return fail(AKV_ERR_INVALID, "negative size");
+  if (B > 65535 || shape->Hq > 65535)
+    return fail(AKV_ERR_UNSUPPORTED, "chunk calls support B <= 65535 and Hq <= 65535");
+  if (max_kv > kMaxList)
+    return fail(AKV_ERR_UNSUPPORTED, "chunk calls support max_kv <= %d", kMaxList);
+  if (max_kv > 0 && S == 0) return fail(AKV_ERR_INVALID, "lists over an empty pool (S = 0)");
+  return AKV_OK;
+}
+
+akv_status check_scratch(const char *what, void *ws, size_t have, size_t need) {
+  if (need && (!ws || (uintptr_t)ws % 256 || have < need))
+    return fail(AKV_ERR_WORKSPACE, "%s workspace: need %zu aligned bytes", what, need);
+  return AKV_OK;
+}
+
+bool chunk_sizes_ok(const akv_shape *s, int32_t B, int32_t n_rows, int32_t max_q, int32_t max_kv) {
+  return s && s->Hq > 0 && s->Hkv > 0 && s->Hq % s->Hkv == 0 && B > 0 && n_rows >= 0 &&
+         max_q >= 0 && max_kv >= 0 && max_kv <= kMaxList;
+}
+}  // namespace
+
+akv_status akv_qk_norm_append(const akv_shape *shape, int32_t n, const void *q, int64_t q_stride,
+                              const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const float *q_weight, const float *k_weight, float eps,
+                              int32_t flags, const int32_t *pos, const int32_t *slot, int32_t S,
+                              void *q_out, void *k_pool, void *v_pool, akv_stream_t stream) {
+  AKV_ENTRY("akv_qk_norm_append");
+  if (akv_status st = check_shape(shape)) return st;
+  if (n < 0 || S < 0) return fail(AKV_ERR_INVALID, "negative size");
+  if (flags & ~(AKV_NORM_Q | AKV_NORM_K | AKV_ROPE_Q | AKV_ROPE_K))
+    return fail(AKV_ERR_INVALID, "unknown flags 0x%x", (unsigned)flags);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(AKV_ERR_INVALID, "eps must be finite and >= 0");
+  if (n == 0) return AKV_OK;
+  if (!q || !k || !v || !slot || !q_out || !k_pool || !v_pool ||
+      ((flags & (AKV_ROPE_Q | AKV_ROPE_K)) && !pos))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  const int64_t q_row = (int64_t)shape->Hq * shape->D, k_row = (int64_t)shape->Hkv * shape->D;
+  if (q_stride < q_row || k_stride < k_row || v_stride < k_row)
+    return fail(AKV_ERR_INVALID, "row strides must be at least the rows' lengths (%lld, %lld)",
+                (long long)q_row, (long long)k_row);
+  const int64_t per16 = 16 / (int64_t)esize(shape->dtype);
+  if (q_stride % per16 || k_stride % per16 || v_stride % per16 || misaligned(q) ||
+      misaligned(k) || misaligned(v) || misaligned(q_out) || misaligned(k_pool) ||
+      misaligned(v_pool))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  if (q == q_out && q_stride != q_row)
+    return fail(AKV_ERR_INVALID, "in place (q_out == q) needs contiguous q");
+  RopeTheta th;
+  rope_theta(shape->rope_base, &th);
+  cudaError_t e = launch_qk_norm_append(shape->dtype, shape->Hq, shape->Hkv, n, q, q_stride, k,
+                                        k_stride, v, v_stride, q_weight, k_weight, eps, flags, pos,
+                                        slot, S, q_out, k_pool, v_pool, th, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "row preparation");
+  return AKV_OK;
+}
+
+size_t akv_chunk_workspace(const akv_shape *shape, int32_t B, int32_t n_rows, int32_t max_q,
+                           int32_t max_kv) {
+  if (!chunk_sizes_ok(shape, B, n_rows, max_q, max_kv)) return 0;
+  return chunk_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, max_q, max_kv);
+}
+
+akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t *q_indptr,
+                               int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                               const void *v_pool, int32_t S, const int32_t *kv_indptr,
+                               const int32_t *kv_indices, int32_t max_kv, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, akv_stream_t stream) {
+  AKV_ENTRY("akv_chunk_attention");
+  if (akv_status st = check_chunk(shape, B, n_rows, max_q, S, max_kv)) return st;
+  if (B == 0 || n_rows == 0 || max_q == 0) return AKV_OK;
+  if (!q_indptr || !q || !kv_indptr || !out ||
+      (max_kv > 0 && (!k_pool || !v_pool || !kv_indices)))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if (misaligned(q) || misaligned(k_pool) || misaligned(v_pool) || misaligned(out))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  if (chunk_grid_x(shape->dtype, B, shape->Hq, shape->Hkv, max_q, max_kv) > INT32_MAX ||
+      (int64_t)n_rows * shape->Hq > (int64_t)INT32_MAX * 8)
+    return fail(AKV_ERR_UNSUPPORTED, "chunk attention: %d rows of %d heads exceed a grid", max_q,
+                shape->Hq);
+  const size_t need =
+      chunk_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, max_q, max_kv);
+  if (akv_status st = check_scratch("chunk attention", workspace, workspace_bytes, need)) return st;
+  cudaError_t e = launch_chunk(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, S, q_indptr, max_q, q,
+                               k_pool, v_pool, kv_indptr, kv_indices, max_kv, out, lse, workspace,
+                               (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention");
+  return AKV_OK;
+}
+
+size_t akv_attention_mass_workspace(const akv_shape *shape, int32_t B, int32_t n_rows,
+                                    int32_t max_q, int32_t max_kv) {
+  if (!chunk_sizes_ok(shape, B, n_rows, max_q, max_kv)) return 0;
+  return mass_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, max_q, max_kv);
+}
+
+akv_status akv_attention_mass(const akv_shape *shape, int32_t B, const int32_t *q_indptr,
+                              int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                              int32_t S, const int32_t *kv_indptr, const int32_t *kv_indices,
+                              int32_t max_kv, const float *lse, float decay, const float *mass_in,
+                              float *mass_out, int64_t mass_stride, void *workspace,
+                              size_t workspace_bytes, akv_stream_t stream) {
+  AKV_ENTRY("akv_attention_mass");
+  if (akv_status st = check_chunk(shape, B, n_rows, max_q, S, max_kv)) return st;
+  if (!std::isfinite(decay)) return fail(AKV_ERR_INVALID, "decay must be finite");
+  if (mass_stride < max_kv) return fail(AKV_ERR_INVALID, "mass_stride %lld < max_kv %d",
+                                        (long long)mass_stride, max_kv);
+  if (B == 0 || max_kv == 0) return AKV_OK;
+  if (!q_indptr || !kv_indptr || !k_pool || !kv_indices || !mass_out ||
+      (n_rows > 0 && max_q > 0 && (!q || !lse)))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if (misaligned(q) || misaligned(k_pool))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  const size_t need =
+      mass_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, max_q, max_kv);
+  if (akv_status st = check_scratch("attention mass", workspace, workspace_bytes, need)) return st;
+  cudaError_t e = launch_mass(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, S, q_indptr, max_q, q,
+                              k_pool, kv_indptr, kv_indices, max_kv, lse, decay, mass_in, mass_out,
+                              mass_stride, workspace, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention mass");
+  return AKV_OK;
+}
+
+akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t *kv_indices,
+                             const int32_t *kv_pos, int32_t max_kv, const float *mass,
+                             int64_t mass_stride, const int32_t *keep, int32_t n_first,
+                             int32_t n_recent, int32_t *out_indptr, int32_t *out_indices,
+                             int32_t *out_pos, float *out_mass, int64_t out_stride,
+                             int64_t out_capacity, int32_t *dropped_indptr, int32_t *dropped,
+                             int64_t dropped_capacity, akv_stream_t stream) {
+  AKV_ENTRY("akv_evict_by_mass");
+  if (B < 0 || max_kv < 0 || n_first < 0 || n_recent < 0)
+    return fail(AKV_ERR_INVALID, "negative size");
+  if (B > 65535) return fail(AKV_ERR_UNSUPPORTED, "eviction supports B <= 65535");
+  if (max_kv > kMaxList)
+    return fail(AKV_ERR_UNSUPPORTED, "eviction supports max_kv <= %d", kMaxList);
+  if (mass_stride < max_kv) return fail(AKV_ERR_INVALID, "mass_stride %lld < max_kv %d",
+                                        (long long)mass_stride, max_kv);
+  if (out_stride < 0 || out_capacity < 0 || dropped_capacity < 0)
+    return fail(AKV_ERR_INVALID, "negative size");
+  if (B == 0) return AKV_OK;
+  if (!kv_indptr || !keep || !out_indptr || !dropped_indptr ||
+      (max_kv > 0 && (!kv_indices || !mass || !out_indices || !out_mass || !dropped)))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if (max_kv > 0 && (kv_pos == nullptr) != (out_pos == nullptr))
+    return fail(AKV_ERR_INVALID, "kv_pos and out_pos are given together or not at all");
+  if (max_kv > 0 && mass == out_mass)
+    return fail(AKV_ERR_INVALID, "out_mass must not be mass");
+  cudaError_t e = launch_evict(B, kv_indptr, kv_indices, kv_pos, max_kv, mass, mass_stride, keep,
+                               n_first, n_recent, out_indptr, out_indices, out_pos, out_mass,
+                               out_stride, out_capacity, dropped_indptr, dropped,
+                               dropped_capacity, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "eviction by mass");
+  return AKV_OK;
+}
+
+// ------------------------------------------------------------------------
 // Decoder layers around the segment attention
 // ------------------------------------------------------------------------
 

@@ -1,0 +1,102 @@
+// Shared by the kernels over a chunk of new tokens and a page-size-1 pool
+// (chunk.cu, mass.cu): the batch, a request's view of it, and the 64 x 64
+// score tile on the CUDA cores.
+//
+// Rows.  The query rows of KV head g are packed (token, head of the group):
+// packed row r of request b is token i = r / grp of its chunk and query head
+// g * grp + r % grp, so that one K/V tile serves every row that reads it.
+// Row i of a chunk of m tokens sees the list entries j < n - m + i + 1.
+#pragma once
+
+#include "common.cuh"
+
+namespace akv {
+
+struct ChunkBatch {
+  int B, Hq, Hkv, n_rows, S, max_q, max_kv;
+  const int32_t *q_indptr, *kv_indptr, *kv_indices;
+  const void *q, *k, *v;
+};
+
+struct ChunkReq {
+  int q0, m;    // first row of the chunk in q, its tokens
+  int beg, n;   // first list entry, entries
+  __device__ __forceinline__ int limit(int i) const {  // entries that token i sees
+    return min(n, max(0, n - m + i + 1));
+  }
+};
+
+// Lengths are held to the bounds the call was given, so that no index can
+// leave the buffers whatever the index arrays hold.
+__device__ __forceinline__ ChunkReq chunk_req(const ChunkBatch &a, int b) {
+  ChunkReq r;
+  r.q0 = max(0, a.q_indptr[b]);
+  r.m = max(0, min(min(a.q_indptr[b + 1], a.n_rows) - r.q0, a.max_q));
+  r.beg = a.kv_indptr[b];
+  r.n = min(max(a.kv_indptr[b + 1] - r.beg, 0), a.max_kv);
+  return r;
+}
+
+// pool row of list entry j; an index outside the pool reads its first row
+__device__ __forceinline__ int64_t chunk_slot(const ChunkBatch &a, const ChunkReq &r, int j) {
+  const int s = __ldg(a.kv_indices + (int64_t)r.beg + j);
+  return (unsigned)s < (unsigned)a.S ? s : 0;
+}
+
+// ---- 64 x 64 score tile on the CUDA cores, 256 threads, 4 x 4 per thread ----
+// Thread (ty, tx) = (tid / 16, tid % 16) holds rows 4 ty .. + 3 and keys (or
+// value columns) 4 tx .. + 3.  Q and K are staged transposed ([d][row]) so
+// that both operands of a step are one 16-byte shared load.
+constexpr int kSimt = 64;
+constexpr int kSimtPad = kSimt + 4;
+constexpr int kSimtThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void simt_stage_t(float (*dst)[kSimtPad], int row, int part,
+                                             const T *src) {
+  constexpr int E = Chunk<T>::kElems;
+#pragma unroll
+  for (int c = 0; c < 16 / E; ++c) {
+    float f[E];
+    if (src) chunk_to_f32<T>(__ldg(reinterpret_cast<const uint4 *>(src + part * 16) + c), f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[part * 16 + c * E + e][row] = src ? f[e] : 0.f;
+  }
+}
+
+// packed rows r0.. of KV head g (rows past the chunk: zeros)
+template <typename T>
+__device__ __forceinline__ void simt_load_q(float (*dst)[kSimtPad], const ChunkBatch &a,
+                                            const ChunkReq &rq, int g, int r0) {
+  const int grp = a.Hq / a.Hkv, row = threadIdx.x % kSimt, r = r0 + row;
+  const T *src = nullptr;
+  if (r < rq.m * grp)
+    src = (const T *)a.q + ((int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp) * kD;
+  simt_stage_t<T>(dst, row, threadIdx.x / kSimt, src);
+}
+
+// keys j0.. of KV head g (entries from `end` on: zeros)
+template <typename T>
+__device__ __forceinline__ void simt_load_k(float (*dst)[kSimtPad], const ChunkBatch &a,
+                                            const ChunkReq &rq, int g, int j0, int end) {
+  const int row = threadIdx.x % kSimt, j = j0 + row;
+  const T *src =
+      j < end ? (const T *)a.k + (chunk_slot(a, rq, j) * a.Hkv + g) * kD : nullptr;
+  simt_stage_t<T>(dst, row, threadIdx.x / kSimt, src);
+}
+
+__device__ __forceinline__ void simt_mma(const float (*x)[kSimtPad], const float (*y)[kSimtPad],
+                                         int ty, int tx, float (*acc)[4]) {
+#pragma unroll 16
+  for (int d = 0; d < kSimt; ++d) {
+    const float4 u = *reinterpret_cast<const float4 *>(&x[d][4 * ty]);
+    const float4 w = *reinterpret_cast<const float4 *>(&y[d][4 * tx]);
+    const float uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[p][q] = fmaf(uu[p], ww[q], acc[p][q]);
+  }
+}
+
+}  // namespace akv
