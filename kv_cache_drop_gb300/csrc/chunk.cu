@@ -20,6 +20,7 @@ struct ChunkParts {
   float *o;
   int ns, chunk;
 };
+constexpr int kMaxSplit = 1024;  // the merge keeps one weight per split in shared memory
 
 template <typename T>
 __device__ __forceinline__ void store4(T *dst, const float *x);
@@ -145,16 +146,19 @@ __global__ void __launch_bounds__(kSimtThreads)
   }
 }
 
-// Joins the splits of a row by their log-sum-exp: a warp per (row, head), two
-// output columns per lane.
-constexpr int kMergeWarps = 8;
+// Joins the splits of a row by their log-sum-exp: a CTA per (row, head), eight
+// groups of 16 threads each summing every eighth split's output row (16 bytes
+// per load).  Launched as a programmatic dependent of the attention kernel.
+constexpr int kMergeThreads = 128;
 template <typename T>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+__global__ void __launch_bounds__(kMergeThreads)
     chunk_merge_kernel(const ChunkBatch a, T *out, float *lse, const ChunkParts part) {
-  const int64_t w = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  __shared__ float wgt[kMaxSplit];
+  __shared__ float4 red[8][kD / 4];
+  __shared__ float tot[kMergeThreads / 32], top[kMergeThreads / 32];
+  const int64_t w = blockIdx.x;
   const int t = (int)(w / a.Hq);
-  if (t >= a.n_rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int lo = 0, hi = a.B;  // the request that holds row t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -164,37 +168,708 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const int i = t - rq.q0;
   if (i < 0 || i >= rq.m) return;  // no request's row: left as it is
   const int used = (rq.limit(i) + part.chunk - 1) / part.chunk;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const float2 *ml = part.ml + w * part.ns;
   float M = -INFINITY;
-  for (int s = lane; s < used; s += 32) M = fmaxf(M, ml[s].x);
+  for (int s = threadIdx.x; s < used; s += kMergeThreads) {
+    const float m = __ldcg(&ml[s].x);
+    wgt[s] = m;
+    M = fmaxf(M, m);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) top[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
   const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, x0 = 0.f, x1 = 0.f;
-  for (int s0 = 0; s0 < used; s0 += 32) {
-    float f = 0.f;
-    if (s0 + lane < used) {
-      const float2 v = ml[s0 + lane];
-      f = exp2f(v.x - ref);
-      L += v.y * f;
-    }
-    const int cnt = min(32, used - s0);
-    for (int s = 0; s < cnt; ++s) {
-      const float fs = __shfl_sync(0xffffffffu, f, s);
-      const float2 v = reinterpret_cast<const float2 *>(part.o + (w * part.ns + s0 + s) * kD)[lane];
-      x0 = fmaf(v.x, fs, x0);
-      x1 = fmaf(v.y, fs, x1);
-    }
+  float L = 0.f;
+  for (int s = threadIdx.x; s < used; s += kMergeThreads) {
+    const float f = exp2f(wgt[s] - ref);
+    wgt[s] = f;
+    L = fmaf(__ldcg(&ml[s].y), f, L);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) tot[warp] = L;
+  __syncthreads();
+  L = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+  const int cg = threadIdx.x & 15, sg = threadIdx.x >> 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = sg; s < used; s += 8) {
+    const float4 v =
+        __ldcg(reinterpret_cast<const float4 *>(part.o + (w * part.ns + s) * kD) + cg);
+    const float f = wgt[s];
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  red[sg][cg] = acc;
+  __syncthreads();
   const bool none = used == 0;
-  const float y0 = none ? 0.f : x0 / L, y1 = none ? 0.f : x1 / L;
-  if constexpr (sizeof(T) == 4)
-    reinterpret_cast<float2 *>(out + w * kD)[lane] = make_float2(y0, y1);
-  else
-    reinterpret_cast<__nv_bfloat162 *>(out + w * kD)[lane] = __floats2bfloat162_rn(y0, y1);
-  if (lse && lane == 0) lse[w] = none ? -INFINITY : M * kLn2 + logf(L);
+  if (threadIdx.x < kD / 4) {
+    float y[4] = {};
+    for (int g = 0; g < 8; ++g) {
+      const float4 v = red[g][threadIdx.x];
+      y[0] += v.x;
+      y[1] += v.y;
+      y[2] += v.z;
+      y[3] += v.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = none ? 0.f : y[e] / L;
+    store4<T>(out + w * kD + 4 * threadIdx.x, y);
+  }
+  if (lse && threadIdx.x == 0) lse[w] = none ? -INFINITY : M * kLn2 + logf(L);
+}
+
+
+// ---------------------------------------------------------------------------
+// bf16, few rows (decode steps, short verification chunks): up to 16 kRT
+// packed rows per KV head.  CTA = key split x request, a warp per KV head (up
+// to eight heads a CTA), so that a key's heads are read together.  Keys and
+// values are gathered 16 rows at a time by 16-byte cp.async into an
+// XOR-swizzled tile, several tiles in flight; the packed rows are the rows of
+// m16n8k16 tiles: S = Q K^T with K as the B operand, P reused from the S
+// registers for P V.  Bound by the gather from HBM; tcgen05 would spend a
+// 128-row tile on 8 rows.
+// ---------------------------------------------------------------------------
+constexpr int kSKeys = 16;
+constexpr int kSTile = kSKeys * kD * 2;    // bytes of a K (or V) tile
+constexpr int kSHeads = 8;                 // warps (KV heads) per CTA at most
+constexpr int small_stages(int rt) { return rt == 1 ? 3 : 6; }
+constexpr float kScale = 0.125f * kLog2e;  // scores to log2 units
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// byte offset of (row, 16-byte chunk) in a [16][64] bf16 tile
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int kRT>
+__global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
+    chunk_small_kernel(const ChunkBatch a, __nv_bfloat16 *out, float *lse, const ChunkParts part) {
+  constexpr int kSt = small_stages(kRT);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int split = blockIdx.x, b = blockIdx.y, g = blockIdx.z * kSHeads + warp;
+  const ChunkReq rq = chunk_req(a, b);
+  const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
+  if (rows == 0 || g >= a.Hkv) return;
+  const int c0 = split * part.chunk, c1 = min(rq.limit(rq.m - 1), c0 + part.chunk);
+  if (part.ns > 1 && c0 >= c1) return;
+  const int nk = max(0, c1 - c0), n_tiles = (nk + kSKeys - 1) / kSKeys;
+  const uint32_t wsm = ptx::smem_addr(smem_raw) + warp * kSt * 2 * kSTile;
+  uint8_t *const wsm_g = smem_raw + warp * kSt * 2 * kSTile;
+
+  // pool row of key `lane` of tile t, loaded a tile ahead of its use
+  auto load_slot = [&](int t) {
+    const int k = t * kSKeys + lane;
+    return lane < kSKeys && k < nk ? (int)chunk_slot(a, rq, c0 + k) : 0;
+  };
+  const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + g * kD;
+  const __nv_bfloat16 *vp = (const __nv_bfloat16 *)a.v + g * kD;
+  auto issue = [&](int t, int slot) {
+    if (t < n_tiles) {
+      const uint32_t at = wsm + (t % kSt) * 2 * kSTile;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = (lane >> 3) + 4 * i, ch = lane & 7;
+        const int sl = __shfl_sync(0xffffffffu, slot, key);
+        const bool valid = t * kSKeys + key < nk;
+        const int64_t off = (int64_t)sl * a.Hkv * kD + ch * 8;
+        cp_async16(at + tile_at(key, ch), kp + off, valid);
+        cp_async16(at + kSTile + tile_at(key, ch), vp + off, valid);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  int slot_nx = load_slot(0);
+#pragma unroll
+  for (int t = 0; t < kSt - 1; ++t) {
+    const int sl = slot_nx;
+    slot_nx = load_slot(t + 1);
+    issue(t, sl);
+  }
+
+  // Q fragments and the rows' limits (relative to c0)
+  uint32_t qa[kRT][4][4];
+  int lim[kRT][2], lim_min = INT32_MAX;
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = rt * 16 + gid + 8 * hh;
+      const bool ok = r < rows;
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(
+          (const __nv_bfloat16 *)a.q +
+          ((int64_t)(rq.q0 + (ok ? r / grp : 0)) * a.Hq + g * grp + (ok ? r % grp : 0)) * kD);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        qa[rt][ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
+        qa[rt][ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
+      }
+      lim[rt][hh] = (ok ? rq.limit(r / grp) : 0) - c0;
+    }
+  lim_min = rq.limit(0) - c0;  // the first token sees the least
+
+  float o[kRT][8][4], m[kRT][2], l[kRT][2];
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
+    m[rt][0] = m[rt][1] = -INFINITY;
+    l[rt][0] = l[rt][1] = 0.f;
+  }
+
+  for (int it = 0; it < n_tiles; ++it) {
+    const int sl = slot_nx;
+    slot_nx = load_slot(it + kSt);
+    issue(it + kSt - 1, sl);
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kSt - 1) : "memory");
+    __syncwarp();
+    const uint32_t kt = wsm + (it % kSt) * 2 * kSTile, vt = kt + kSTile;
+    const int k0 = it * kSKeys;
+    const bool ragged = k0 + kSKeys > min(lim_min, nk);
+    float s[kRT][2][4];
+#pragma unroll
+    for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) s[rt][nb][0] = s[rt][nb][1] = s[rt][nb][2] = s[rt][nb][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      uint32_t kb[4];
+      const int mi = lane >> 3;
+      ldsm4(kt + tile_at((mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), kb);
+#pragma unroll
+      for (int rt = 0; rt < kRT; ++rt) {
+        mma16816(s[rt][0], qa[rt][ks], kb[0], kb[1]);
+        mma16816(s[rt][1], qa[rt][ks], kb[2], kb[3]);
+      }
+    }
+    if (ragged) {
+#pragma unroll
+      for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k0 + nb * 8 + 2 * tig + (e & 1) >= min(lim[rt][e >> 1], nk)) s[rt][nb][e] = -INFINITY;
+    }
+    uint32_t pa[kRT][4];
+#pragma unroll
+    for (int rt = 0; rt < kRT; ++rt) {
+      float alpha[2], ref[2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float mx = fmaxf(fmaxf(s[rt][0][2 * hh], s[rt][0][2 * hh + 1]),
+                         fmaxf(s[rt][1][2 * hh], s[rt][1][2 * hh + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[rt][hh], mx * kScale);
+        ref[hh] = mn == -INFINITY ? 0.f : mn;
+        alpha[hh] = ptx::ex2(m[rt][hh] - ref[hh]);
+        m[rt][hh] = mn;
+        l[rt][hh] *= alpha[hh];
+      }
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[rt][nb][e] = ptx::ex2(fmaf(s[rt][nb][e], kScale, -ref[e >> 1]));
+          l[rt][e >> 1] += s[rt][nb][e];
+        }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[rt][i][0] *= alpha[0];
+        o[rt][i][1] *= alpha[0];
+        o[rt][i][2] *= alpha[1];
+        o[rt][i][3] *= alpha[1];
+      }
+      // weights rounded to bf16 for the product; their sum l is not
+      pa[rt][0] = pack2(s[rt][0][0], s[rt][0][1]);
+      pa[rt][1] = pack2(s[rt][0][2], s[rt][0][3]);
+      pa[rt][2] = pack2(s[rt][1][0], s[rt][1][1]);
+      pa[rt][3] = pack2(s[rt][1][2], s[rt][1][3]);
+    }
+    if (ragged) {
+      // An infinity or NaN in a hidden entry's value would reach every row
+      // of the tile as 0 * inf: such values are added to the rows that see
+      // them and leave the tile.
+      uint4 *vg = reinterpret_cast<uint4 *>(wsm_g + (it % kSt) * 2 * kSTile + kSTile);
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = vg[lane + 32 * i];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= nonfinite_lo(w[e]) || nonfinite_hi(w[e]);
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+        for (int key = 0; key < kSKeys; ++key)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                reinterpret_cast<const uint8_t *>(vg) + tile_at(key, i) + 4 * tig);
+#pragma unroll
+            for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+                if (k0 + key < min(lim[rt][hh], nk)) {
+                  if (nonfinite_lo(w)) o[rt][i][2 * hh] += __uint_as_float(w << 16);
+                  if (nonfinite_hi(w)) o[rt][i][2 * hh + 1] += __uint_as_float(w & 0xffff0000u);
+                }
+          }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = vg[lane + 32 * i];
+          vg[lane + 32 * i] = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y),
+                                         finite_or_zero(x.z), finite_or_zero(x.w));
+        }
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int nb2 = 0; nb2 < 4; ++nb2) {
+      const int mi = lane >> 3;
+      uint32_t vb[4];
+      ldsm4_t(vt + tile_at((mi & 1) * 8 + (lane & 7), nb2 * 2 + (mi >> 1)), vb);
+#pragma unroll
+      for (int rt = 0; rt < kRT; ++rt) {
+        mma16816(o[rt][2 * nb2], pa[rt], vb[0], vb[1]);
+        mma16816(o[rt][2 * nb2 + 1], pa[rt], vb[2], vb[3]);
+      }
+    }
+    __syncwarp();  // the tile's readers are done before it is refilled
+  }
+  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+
+#pragma unroll
+  for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      float x = l[rt][hh];
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      const int r = rt * 16 + gid + 8 * hh;
+      if (r >= rows) continue;
+      const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
+      if (part.ns == 1) {
+        const bool none = lim[rt][hh] <= 0;
+        const float inv = none ? 0.f : 1.f / x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          reinterpret_cast<uint32_t *>(out + row * kD)[4 * i + tig] =
+              none ? 0u : pack2(o[rt][i][2 * hh] * inv, o[rt][i][2 * hh + 1] * inv);
+        if (lse && tig == 0) lse[row] = none ? -INFINITY : m[rt][hh] * kLn2 + logf(x);
+      } else {
+        const int64_t pi = row * part.ns + split;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          reinterpret_cast<float2 *>(part.o + pi * kD)[4 * i + tig] =
+              make_float2(o[rt][i][2 * hh], o[rt][i][2 * hh + 1]);
+        if (tig == 0) part.ml[pi] = make_float2(m[rt][hh], x);
+      }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// bf16, more rows: tcgen05.  CTA = kTiles tiles of 128 packed rows of one KV
+// head (both read the same K/V windows) x one key split.
+//   warps 4 i .. 4 i + 3  softmax of tile i (thread = packed row = TMEM lane)
+//   then the producer warp: 128-key K and V windows through a ring of stages,
+//        each lane gathering four pool rows of K and of V per window
+//   then the MMA warp: TMEM allocation, one thread issuing tcgen05.mma
+// TMEM columns: S_i [128 i, + 128), O_i [128 kTiles + 64 i, + 64), Q_i
+// [192 kTiles + 32 i, + 32).  Q_i (bf16 pairs) is the A operand of S_i = Q_i
+// K^T; P_i overwrites the first 64 columns of S_i as bf16 pairs and is the A
+// operand of O_i += P_i V.  bf16 throughout, because A and B of one MMA have
+// one type and the pool is bf16; the row sums are taken by the softmax
+// threads from the unrounded weights, so that the log-sum-exp is good to fp32.
+// Per window the MMA thread issues O_0 += P_0 V, S_0 of the next window, then
+// the same for tile 1: one tile's softmax runs beside the other's MMAs.  The
+// running maximum is raised (and O rescaled) only when it grows by 2^8.
+//
+// Hidden entries.  Windows from the first tile's limit on are masked per row.
+// There a weight of 0 would still turn a hidden infinity or NaN of V into
+// NaN, so the softmax threads look the V window over first, clear such values
+// and remember; a row that sees one adds it at the end.
+//
+// Every wait is bounded: one that runs out marks the CTA (later waits return
+// at the next poll) and the workspace's status word, and the CTA still frees
+// its TMEM.  The named barriers are reached equally often whatever the waits
+// return.
+// ---------------------------------------------------------------------------
+constexpr int kBarP = 3;         // hardware barriers kBarP + i (0 is __syncthreads)
+constexpr int kBarPCount = 192;  // a softmax group, the producer warp, the MMA warp
+constexpr float kRescale = 8.f;  // log2 units
+
+constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 6; }
+
+template <int kTiles>
+struct __align__(1024) TcSmem {
+  uint8_t k[tc_stages(kTiles)][kTcTileBytes];
+  uint8_t v[tc_stages(kTiles)][kTcTileBytes];
+  uint64_t bar_kv[tc_stages(kTiles)];
+  uint64_t bar_s[2], bar_done;
+  uint32_t tmem_base;
+  uint32_t gave_up;  // a wait of this CTA ran out
+  uint32_t odd;      // V windows held an infinity or NaN beside hidden entries
+};
+
+template <int kTiles>
+__global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const ChunkBatch a,
+                    __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, const ChunkParts part,
+                    uint32_t *status) {
+  constexpr int kSt = tc_stages(kTiles);
+  constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + 1;
+  constexpr int kThreads = kTiles * 128 + 64;
+  constexpr uint32_t kCols = kTiles == 1 ? 256 : 512;
+  constexpr uint32_t kColO = 128 * kTiles, kColQ = 192 * kTiles;
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem<kTiles> &sm = *reinterpret_cast<TcSmem<kTiles> *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
+  const int64_t r0 = (int64_t)(blockIdx.x / part.ns) * (kTiles * kTcRows);
+  const ChunkReq rq = chunk_req(a, b);
+  const int grp = a.Hq / a.Hkv;
+  const int64_t rows = (int64_t)rq.m * grp;
+  if (r0 >= rows) return;
+  const int64_t r1 = min(rows, r0 + kTiles * kTcRows);
+  const int c0 = split * part.chunk;
+  const int c1 = min(rq.limit((int)((r1 - 1) / grp)), c0 + part.chunk);
+  if (part.ns > 1 && c0 >= c1) return;  // the merge reads only splits with visible entries
+  const int n_win = c1 > c0 ? (c1 - c0 + kTcKeys - 1) / kTcKeys : 0;
+  // first window with an entry hidden from a row of this CTA (or past c1)
+  const int w_ragged = max(0, min(rq.limit((int)(r0 / grp)), c1) - c0) / kTcKeys;
+
+  // this thread's packed row
+  const int i = warp >> 2;
+  const int64_t r = r0 + threadIdx.x;
+  const bool valid = warp < kProdWarp && r < r1;
+  const int lim = valid ? rq.limit((int)(r / grp)) : 0;
+  const int64_t row = valid ? (int64_t)(rq.q0 + (int)(r / grp)) * a.Hq + g * grp + (int)(r % grp) : 0;
+  uint32_t qw[32];
+  if (warp < kProdWarp) {
+    const uint4 *src = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + row * kD);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      qw[4 * c] = x.x;
+      qw[4 * c + 1] = x.y;
+      qw[4 * c + 2] = x.z;
+      qw[4 * c + 3] = x.w;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSt; ++s) ptx::mbar_init(&sm.bar_kv[s], 1);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&sm.bar_s[s], 1);
+    ptx::mbar_init(&sm.bar_done, 1);
+    sm.gave_up = sm.odd = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) ptx::tmem_alloc(&sm.tmem_base, kCols);
+  if (warp == kProdWarp && lane == 0) {
+    ptx::tma_prefetch_desc(&tmK);
+    ptx::tma_prefetch_desc(&tmV);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const bool two = kTiles == 2 && r0 + kTcRows < r1;  // tile 1 has rows
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!ptx::mbar_wait_grid(bar, parity, &sm.gave_up, 1u, kTcWaitBudget))
+      atomicOr(status, kStatusWaitTimeout);
+  };
+
+  if (warp == kProdWarp) {
+    // Lane l gathers entries 4 l .. 4 l + 3 of a window; the next window's
+    // indices are loaded one window ahead.  A stage is refilled without a
+    // wait: generation n + 1 of the last tile's barrier completes only after
+    // its softmax has seen S(n), whose commit tracks P.V(n - 1), the last
+    // reader of that stage.
+    const uint32_t kd = ptx::smem_addr(sm.k[0]) + lane * 512, vd = ptx::smem_addr(sm.v[0]) + lane * 512;
+    const int x = g * kD;
+    auto slots = [&](int n) {
+      return n < n_win ? chunk_slots4(a, rq, c0 + n * kTcKeys + 4 * lane, c1) : make_int4(0, 0, 0, 0);
+    };
+    auto load = [&](int n, const int4 &s) {
+      const int st = n % kSt;
+      if (lane == 0) ptx::mbar_expect_tx(&sm.bar_kv[st], 2 * kTcTileBytes);
+      __syncwarp();
+      const uint32_t bar = ptx::smem_addr(&sm.bar_kv[st]);
+      tma_gather4(kd + st * kTcTileBytes, &tmK, bar, x, s);
+      tma_gather4(vd + st * kTcTileBytes, &tmV, bar, x, s);
+    };
+    int4 nx = slots(0);
+    int loaded = 0;
+    for (; loaded < n_win && loaded < kSt; ++loaded) {
+      const int4 cur = nx;
+      nx = slots(loaded + 1);
+      load(loaded, cur);
+    }
+    if (n_win > 0) wait(&sm.bar_kv[0], 0);
+    ptx::named_bar_sync(kBarP, kBarPCount);
+    if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+    for (int n = 0; n < n_win; ++n) {
+      if (n + 1 < n_win) wait(&sm.bar_kv[(n + 1) % kSt], ((n + 1) / kSt) & 1);
+      ptx::named_bar_sync(kBarP, kBarPCount);
+      if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+      if (n >= 1 && loaded < n_win) {
+        const int4 cur = nx;
+        nx = slots(loaded + 1);
+        load(loaded, cur);
+        ++loaded;
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
+    constexpr uint32_t idO = ptx::idesc_bf16(128, 64, true);
+    constexpr uint64_t kTileStep = kTcTileBytes >> 4;
+    const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0]));
+    const uint64_t dv = ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]));
+    const bool leader = lane == 0;
+    auto issue_s = [&](int t, int st) {
+      if (!leader) return;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        ptx::mma_f16_ts(tmem + 128 * t, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk,
+                        idS, kk > 0);
+      ptx::mma_commit(&sm.bar_s[t]);
+    };
+    auto issue_o = [&](int t, int st, bool acc) {
+      if (!leader) return;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        ptx::mma_f16_ts(tmem + kColO + 64 * t, tmem + 128 * t + 8 * kk, dv + st * kTileStep + 128 * kk,
+                        idO, (acc || kk > 0) ? 1u : 0u);
+    };
+    ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
+    if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+    ptx::tc_fence_after();
+    if (n_win > 0) {
+      issue_s(0, 0);
+      if (two) issue_s(1, 0);
+    }
+    for (int n = 0; n < n_win; ++n) {
+      const int st = n % kSt, st1 = (n + 1) % kSt;
+      ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
+      ptx::tc_fence_after();
+      issue_o(0, st, n > 0);
+      if (n + 1 < n_win) issue_s(0, st1);
+      if (kTiles == 2) {
+        ptx::named_bar_sync(kBarP + 1, kBarPCount);
+        ptx::tc_fence_after();
+        if (two) {
+          issue_o(1, st, n > 0);
+          if (n + 1 < n_win) issue_s(1, st1);
+        }
+      }
+    }
+    if (leader) ptx::mma_commit(&sm.bar_done);
+    wait(&sm.bar_done, 0);
+  } else if (i == 1 && !two) {
+    // no row in this tile: only the barriers
+    for (int n = 0; n <= n_win; ++n) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+    wait(&sm.bar_done, 0);
+  } else {
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + 64 * i;
+    ptx::tmem_st32(tmem + lane_base + kColQ + 32 * i, qw);
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    ptx::named_bar_sync(kBarP + i, kBarPCount);
+    const float2 scale2 = make_float2(kScale, kScale);
+    float m_run = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f);
+    for (int n = 0; n < n_win; ++n) {
+      wait(&sm.bar_s[i], n & 1);
+      ptx::tc_fence_after();
+      uint32_t sr[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+      if (n >= w_ragged) {
+        const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= seen) sr[c] = 0xff800000u;  // -inf
+      }
+      float mx8[8];
+#pragma unroll
+      for (int k8 = 0; k8 < 8; ++k8)
+        mx8[k8] = ptx::max3(__uint_as_float(sr[k8]), __uint_as_float(sr[8 + k8]),
+                            __uint_as_float(sr[16 + k8]));
+#pragma unroll
+      for (int c = 24; c + 16 <= 120; c += 16)
+#pragma unroll
+        for (int k8 = 0; k8 < 8; ++k8)
+          mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
+#pragma unroll
+      for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = fmaxf(mx8[k8], __uint_as_float(sr[120 + k8]));
+      const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
+                             fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+      const float m_new = fmaxf(m_run, mx * kScale);
+      const bool need = m_new > m_run + kRescale;
+      const bool any = __any_sync(0xffffffffu, need);
+      float alpha = 1.f;
+      if (need) {
+        alpha = ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
+        m_run = m_new;
+        l2.x *= alpha;
+        l2.y *= alpha;
+      }
+      const float mref = m_run == -INFINITY ? 0.f : m_run;
+      const float2 neg2 = make_float2(-mref, -mref);
+      // weights in fp32 (summed as they are), rounded to bf16 pairs: word k
+      // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
+#pragma unroll
+      for (int qtr = 0; qtr < 4; ++qtr) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int c = 2 * (16 * qtr + k);
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                      scale2, neg2);
+          const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+          l2 = __fadd2_rn(l2, p);
+          pw[k] = pack2(p.x, p.y);
+        }
+        ptx::tmem_st16(tS + 16 * qtr, pw);
+      }
+      if (n > 0 && any) {
+        // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
+#pragma unroll
+        for (int hlf = 0; hlf < 2; ++hlf) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + 32 * hlf, o);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence32(o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+          ptx::tmem_st32(tO + 32 * hlf, o);
+        }
+      }
+      if (n >= w_ragged) {
+        wait(&sm.bar_kv[n % kSt], (n / kSt) & 1);  // landed long ago: makes it visible here
+        uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
+        for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
+          const uint4 x = v4[c];
+          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
+                                     finite_or_zero(x.w));
+          if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+            *(volatile uint32_t *)&sm.odd = 1u;
+            __threadfence_block();
+            v4[c] = y;
+          }
+        }
+        ptx::fence_proxy_async_smem();  // before the tensor core reads the window
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      ptx::named_bar_sync(kBarP + i, kBarPCount);
+    }
+    wait(&sm.bar_done, 0);  // the last P.V
+    ptx::tc_fence_after();
+    uint32_t o[64];
+    if (n_win > 0) {
+      ptx::tmem_ld32(tO, o);
+      ptx::tmem_ld32(tO + 32, o + 32);
+      ptx::tmem_wait_ld();
+      ptx::reg_fence32(o);
+      ptx::reg_fence32(o + 32);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) o[c] = 0u;
+    }
+    if (*(volatile uint32_t *)&sm.odd && valid) {
+      for (int j = c0 + w_ragged * kTcKeys; j < min(lim, c1); ++j) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            (const __nv_bfloat16 *)a.v + (chunk_slot(a, rq, j) * a.Hkv + g) * kD);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = __ldg(src + c);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d = 8 * c + 2 * e;
+            if (nonfinite_lo(w[e]))
+              o[d] = __float_as_uint(__uint_as_float(o[d]) + __uint_as_float(w[e] << 16));
+            if (nonfinite_hi(w[e]))
+              o[d + 1] = __float_as_uint(__uint_as_float(o[d + 1]) + __uint_as_float(w[e] & 0xffff0000u));
+          }
+        }
+      }
+    }
+    const float l = l2.x + l2.y;
+    if (valid && part.ns == 1) {
+      const bool none = lim == 0;
+      const float inv = none ? 0.f : 1.f / l;
+      uint4 *dst = reinterpret_cast<uint4 *>(out + row * kD);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t w4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w4[e] = none ? 0u : pack2(__uint_as_float(o[8 * c + 2 * e]) * inv,
+                                    __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+        dst[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+      }
+      if (lse) lse[row] = none ? -INFINITY : m_run * kLn2 + logf(l);
+    } else if (valid) {
+      const int64_t pi = row * part.ns + split;
+      float4 *dst = reinterpret_cast<float4 *>(part.o + pi * kD);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                             __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+      part.ml[pi] = make_float2(m_run, l);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kCols);
+  }
 }
 
 int sm_count() {
@@ -204,33 +879,74 @@ int sm_count() {
   return sms;
 }
 
-// Splits of the key axis: a call whose row tiles alone give `waves` waves of
-// CTAs is not split; otherwise the lists are cut into chunks of at least
-// kMinSplit keys, as many as reach that.  The count depends on the host's
-// bounds only, so that a captured call replays for any lengths within them.
-constexpr int kMinSplit = 256;
-constexpr int kMaxSplit = 1024;
-int plan_splits(int64_t tiles, int max_kv, int64_t want, int *chunk) {
-  int64_t ns = tiles >= want || tiles <= 0 ? 1 : (want + tiles - 1) / tiles;
-  ns = std::min<int64_t>(std::min<int64_t>(ns, kMaxSplit), (max_kv + kMinSplit - 1) / kMinSplit);
-  ns = std::max<int64_t>(ns, 1);
-  *chunk = (int)(((int64_t)(max_kv + ns - 1) / ns + 127) / 128 * 128);
-  if (*chunk < 128) *chunk = 128;
-  return (int)std::max<int64_t>(1, ((int64_t)max_kv + *chunk - 1) / *chunk);
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+  static const EncodeTiled fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeTiled)f;
+  }();
+  return fn;
 }
 
-int64_t row_tiles(int Hq, int Hkv, int max_q, int tile) {
-  return ((int64_t)max_q * (Hq / Hkv) + tile - 1) / tile;
-}
-
+// Which kernel takes a call, and its cut of the work.  All of it follows from
+// the host's bounds, so that a captured call replays for any lengths within
+// them.
 struct ChunkPlan {
-  int ns, chunk;
+  int kind;       // 0 CUDA cores; 1, 2: mma.sync with that many 16-row tiles; 3, 4: tcgen05 with
+                  // one or two 128-row tiles
+  int ns, chunk;  // key splits and entries of each
   int64_t tiles;  // row tiles of one (request, KV head)
 };
+constexpr int kSimtKind = 0, kSmallKind = 1, kTcKind = 3;
+
+// Key splits: none if `ctas` (the unsplit grid) reaches `want`; otherwise
+// chunks of max_chunk entries halved until it does, but not below `least` --
+// and below that, down to `least_idle`, only while SMs would stay idle.
+void split_keys(ChunkPlan *p, int64_t ctas, int64_t want, int64_t resident, int max_kv,
+                int max_chunk, int least, int least_idle) {
+  const auto splits = [&](int c) { return std::max<int64_t>(1, ((int64_t)max_kv + c - 1) / c); };
+  p->ns = 1;
+  p->chunk = std::max(128, (int)(((int64_t)max_kv + 127) / 128 * 128));
+  if (ctas >= want) return;
+  int c = max_chunk;
+  while (c > least && ctas * splits(c) < want) c /= 2;
+  while (c > least_idle && ctas * splits(c) < resident) c /= 2;
+  while (splits(c) > kMaxSplit) c *= 2;
+  if (splits(c) == 1) return;
+  p->chunk = c;
+  p->ns = (int)splits(c);
+}
+
 ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   ChunkPlan p;
-  p.tiles = row_tiles(Hq, Hkv, max_q, kSimt);
-  p.ns = plan_splits(p.tiles * B * Hkv, max_kv, 4LL * sm_count(), &p.chunk);
+  const int sms = sm_count();
+  const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+  if (dtype == AKV_BF16 && rows <= 32) {
+    p.kind = rows <= 16 ? kSmallKind : kSmallKind + 1;
+    p.tiles = 1;
+    const int warps = std::min(Hkv, kSHeads), per_sm = p.kind == kSmallKind ? 16 / warps : 8 / warps;
+    const int64_t ctas = (int64_t)B * ((Hkv + kSHeads - 1) / kSHeads);
+    split_keys(&p, ctas, 8LL * per_sm * sms, (int64_t)per_sm * sms, max_kv, 4096, 1024, 128);
+  } else if (dtype == AKV_BF16) {
+    p.kind = rows <= kTcRows ? kTcKind : kTcKind + 1;
+    const int per_sm = p.kind == kTcKind ? 2 : 1, tile = p.kind == kTcKind ? kTcRows : 2 * kTcRows;
+    p.tiles = (rows + tile - 1) / tile;
+    split_keys(&p, p.tiles * B * Hkv, 4LL * per_sm * sms, (int64_t)per_sm * sms, max_kv, 16384, 2048,
+               512);
+  } else {
+    p.kind = kSimtKind;
+    p.tiles = (rows + kSimt - 1) / kSimt;
+    split_keys(&p, p.tiles * B * Hkv, 4LL * sms, 3LL * sms, max_kv, 4096, 512, 128);
+  }
   return p;
 }
 
@@ -248,16 +964,64 @@ cudaError_t launch_simt(const ChunkBatch &a, void *out, float *lse, const ChunkP
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+template <int kRT>
+cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                          cudaStream_t s) {
-  const int64_t warps = (int64_t)a.n_rows * a.Hq;
-  chunk_merge_kernel<T><<<(unsigned)((warps + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0,
-                          s>>>(a, (T *)out, lse, part);
+  const int warps = std::min(a.Hkv, kSHeads), smem = warps * small_stages(kRT) * 2 * kSTile;
+  cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel<kRT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_small_kernel<kRT><<<dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads), warps * 32, smem, s>>>(
+      a, (__nv_bfloat16 *)out, lse, part);
   return cudaGetLastError();
 }
 
+template <int kTiles>
+cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+                      int64_t tiles, uint32_t *status, cudaStream_t s) {
+  CUtensorMap mk, mv;
+  // without lists (max_kv = 0) there need be no pools: the maps are not used
+  const bool pools = a.max_kv > 0;
+  if (!make_gather_map(&mk, pools ? a.k : a.q, pools ? a.S : 1, a.Hkv) ||
+      !make_gather_map(&mv, pools ? a.v : a.q, pools ? a.S : 1, a.Hkv))
+    return cudaErrorInvalidValue;
+  const int smem = (int)sizeof(TcSmem<kTiles>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<kTiles>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  chunk_tc_kernel<kTiles><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kTiles * 128 + 64, smem, s>>>(
+      mk, mv, a, (__nv_bfloat16 *)out, lse, part, status);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+                         cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.n_rows * a.Hq));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T>, a, (T *)out, lse, part);
+}
+
 }  // namespace
+
+bool make_gather_map(CUtensorMap *m, const void *pool, int S, int Hkv) {
+  const EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)Hkv * kD, (cuuint64_t)S};
+  const cuuint64_t strides[1] = {(cuuint64_t)Hkv * kD * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)kD, 1};  // a gather's box is one row high
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
@@ -266,9 +1030,9 @@ int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
 
 size_t chunk_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
-  if (p.ns == 1) return 0;
+  if (p.ns == 1) return kTcStatusBytes;
   const size_t parts = (size_t)n_rows * Hq * p.ns;
-  return up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
+  return kTcStatusBytes + up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
 }
 
 cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
@@ -277,13 +1041,15 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                          int max_kv, void *out, float *lse, void *ws, cudaStream_t s) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
   const ChunkBatch a{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q, k, v};
-  ChunkParts part{nullptr, nullptr, p.ns, p.chunk};
-  if (p.ns > 1) {
-    part.ml = (float2 *)ws;
-    part.o = (float *)((char *)ws + up256((size_t)n_rows * Hq * p.ns * sizeof(float2)));
-  }
-  cudaError_t e = dtype == AKV_BF16 ? launch_simt<__nv_bfloat16>(a, out, lse, part, p.tiles, s)
-                                    : launch_simt<float>(a, out, lse, part, p.tiles, s);
+  char *const w = (char *)ws + kTcStatusBytes;
+  const ChunkParts part{(float2 *)w, (float *)(w + up256((size_t)n_rows * Hq * p.ns * sizeof(float2))),
+                        p.ns, p.chunk};
+  cudaError_t e;
+  if (p.kind == kTcKind) e = launch_tc<1>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
+  else if (p.kind == kTcKind + 1) e = launch_tc<2>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
+  else if (p.kind == kSmallKind) e = launch_small<1>(a, out, lse, part, s);
+  else if (p.kind == kSmallKind + 1) e = launch_small<2>(a, out, lse, part, s);
+  else e = launch_simt<float>(a, out, lse, part, p.tiles, s);
   if (e != cudaSuccess || p.ns == 1) return e;
   return dtype == AKV_BF16 ? launch_merge<__nv_bfloat16>(a, out, lse, part, s)
                            : launch_merge<float>(a, out, lse, part, s);

@@ -9,6 +9,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace akv {
 
@@ -41,6 +42,45 @@ __device__ __forceinline__ ChunkReq chunk_req(const ChunkBatch &a, int b) {
 __device__ __forceinline__ int64_t chunk_slot(const ChunkBatch &a, const ChunkReq &r, int j) {
   const int s = __ldg(a.kv_indices + (int64_t)r.beg + j);
   return (unsigned)s < (unsigned)a.S ? s : 0;
+}
+
+// ---- tensor cores: 128 packed rows x 128 keys ----
+constexpr int kTcRows = 128;
+constexpr int kTcKeys = 128;
+constexpr uint32_t kTcTileBytes = kTcKeys * kD * 2;      // one K or V window of a KV head
+constexpr long long kTcWaitBudget = 1000000000LL;        // SM clocks (about 0.5 s)
+constexpr size_t kTcStatusBytes = 256;                   // status word at the workspace's start
+
+// 2-D view [S][Hkv * 64] of a bf16 pool for gathers of four 64-column rows,
+// 128-byte swizzle.  False if the driver refuses it.
+bool make_gather_map(CUtensorMap *m, const void *pool, int S, int Hkv);
+
+// Four pool rows (64 columns from column x on) to 512 consecutive bytes of a
+// 128-byte-swizzled tile.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
+                                            const int4 &row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"((uint64_t)m), "r"(bar), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
+      : "memory");
+}
+
+// pool rows of list entries j .. j + 3 (entries from `end` on: row 0)
+__device__ __forceinline__ int4 chunk_slots4(const ChunkBatch &a, const ChunkReq &r, int j, int end) {
+  int s[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] = j + e < end ? (int)chunk_slot(a, r, j + e) : 0;
+  return make_int4(s[0], s[1], s[2], s[3]);
+}
+
+// A bf16 pair with an infinity or NaN in it.
+__device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool nonfinite_hi(uint32_t w) {
+  return (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  return (nonfinite_lo(w) ? 0u : w & 0xffffu) | (nonfinite_hi(w) ? 0u : w & 0xffff0000u);
 }
 
 // ---- 64 x 64 score tile on the CUDA cores, 256 threads, 4 x 4 per thread ----
