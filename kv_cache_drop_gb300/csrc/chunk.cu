@@ -7,6 +7,7 @@
 #include "chunk.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace akv {
 namespace {
@@ -508,7 +509,9 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
 // head (both read the same K/V windows) x one key split.
 //   warps 4 i .. 4 i + 3  softmax of tile i (thread = packed row = TMEM lane)
 //   then the producer warp: 128-key K and V windows through a ring of stages,
-//        each lane gathering four pool rows of K and of V per window
+//        gathered by 16-byte cp.async into the 128-byte-swizzled layout that
+//        the MMA reads.  (TMA gathers of four rows deliver one 128-byte row
+//        per 24 clocks: 353 TFLOP/s at 1,024 rows over 16,384 entries.)
 //   then the MMA warp: TMEM allocation, one thread issuing tcgen05.mma
 // TMEM columns: S_i [128 i, + 128), O_i [128 kTiles + 64 i, + 64), Q_i
 // [192 kTiles + 32 i, + 32).  Q_i (bf16 pairs) is the A operand of S_i = Q_i
@@ -540,7 +543,6 @@ template <int kTiles>
 struct __align__(1024) TcSmem {
   uint8_t k[tc_stages(kTiles)][kTcTileBytes];
   uint8_t v[tc_stages(kTiles)][kTcTileBytes];
-  uint64_t bar_kv[tc_stages(kTiles)];
   uint64_t bar_s[2], bar_done;
   uint32_t tmem_base;
   uint32_t gave_up;  // a wait of this CTA ran out
@@ -549,10 +551,8 @@ struct __align__(1024) TcSmem {
 
 template <int kTiles>
 __global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
-    chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const ChunkBatch a,
-                    __nv_bfloat16 *__restrict__ out, float *__restrict__ lse, const ChunkParts part,
-                    uint32_t *status) {
+    chunk_tc_kernel(const ChunkBatch a, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
+                    const ChunkParts part, uint32_t *status) {
   constexpr int kSt = tc_stages(kTiles);
   constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + 1;
   constexpr int kThreads = kTiles * 128 + 64;
@@ -597,17 +597,12 @@ __global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
     }
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSt; ++s) ptx::mbar_init(&sm.bar_kv[s], 1);
     for (int s = 0; s < 2; ++s) ptx::mbar_init(&sm.bar_s[s], 1);
     ptx::mbar_init(&sm.bar_done, 1);
     sm.gave_up = sm.odd = 0u;
     ptx::fence_barrier_init();
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(&sm.tmem_base, kCols);
-  if (warp == kProdWarp && lane == 0) {
-    ptx::tma_prefetch_desc(&tmK);
-    ptx::tma_prefetch_desc(&tmV);
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -619,45 +614,65 @@ __global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
   };
 
   if (warp == kProdWarp) {
-    // Lane l gathers entries 4 l .. 4 l + 3 of a window; the next window's
-    // indices are loaded one window ahead.  A stage is refilled without a
-    // wait: generation n + 1 of the last tile's barrier completes only after
-    // its softmax has seen S(n), whose commit tracks P.V(n - 1), the last
-    // reader of that stage.
-    const uint32_t kd = ptx::smem_addr(sm.k[0]) + lane * 512, vd = ptx::smem_addr(sm.v[0]) + lane * 512;
-    const int x = g * kD;
+    // A window is 128 rows of K and of V, 16 bytes per lane and copy: copy
+    // step s takes entries 4 s .. 4 s + 3, eight lanes each.  Lane l holds the
+    // pool rows of entries l, l + 32, l + 64, l + 96, loaded a window ahead.
+    // A stage is refilled without a wait: generation n + 1 of the last tile's
+    // barrier completes only after its softmax has seen S(n), whose commit
+    // tracks P.V(n - 1), the last reader of that stage.  Each window is one
+    // group of copies (empty past the end), so that "window n + 1 has landed"
+    // is a count of groups still in flight.
+    const int key0 = lane >> 3, ch = lane & 7;
+    const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kTcTileBytes;
+    const uint32_t sw0 = (ch ^ key0) << 4, sw1 = (ch ^ (key0 + 4)) << 4;  // even, odd steps
+    const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
+    const char *vg = (const char *)a.v + (g * kD + ch * 8) * 2;
+    const int64_t pitch = (int64_t)a.Hkv * kD * 2;
+    int nx[4];
     auto slots = [&](int n) {
-      return n < n_win ? chunk_slots4(a, rq, c0 + n * kTcKeys + 4 * lane, c1) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = c0 + n * kTcKeys + 32 * e + lane;
+        nx[e] = n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
+      }
     };
-    auto load = [&](int n, const int4 &s) {
-      const int st = n % kSt;
-      if (lane == 0) ptx::mbar_expect_tx(&sm.bar_kv[st], 2 * kTcTileBytes);
+    auto load = [&](int n) {  // window n from the indices at hand, then those of n + 1
+      int cur[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cur[e] = nx[e];
+      slots(n + 1);
+      if (n < n_win) {
+        const uint32_t at = (n % kSt) * kTcTileBytes;
+#pragma unroll
+        for (int s = 0; s < 32; ++s) {
+          const int sl = __shfl_sync(0xffffffffu, cur[s >> 3], 4 * (s & 7) + key0);
+          const int64_t off = max(sl, 0) * pitch;
+          const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
+          cp_async16(kd + to, kg + off, sl >= 0);  // past the end: zeros
+          cp_async16(vd + to, vg + off, sl >= 0);
+        }
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    // every window but the newest `pending` has landed and is visible to the
+    // tensor core
+    auto landed = [&](auto pending) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(decltype(pending)::value) : "memory");
+      ptx::fence_proxy_async_smem();
       __syncwarp();
-      const uint32_t bar = ptx::smem_addr(&sm.bar_kv[st]);
-      tma_gather4(kd + st * kTcTileBytes, &tmK, bar, x, s);
-      tma_gather4(vd + st * kTcTileBytes, &tmV, bar, x, s);
     };
-    int4 nx = slots(0);
-    int loaded = 0;
-    for (; loaded < n_win && loaded < kSt; ++loaded) {
-      const int4 cur = nx;
-      nx = slots(loaded + 1);
-      load(loaded, cur);
-    }
-    if (n_win > 0) wait(&sm.bar_kv[0], 0);
+    slots(0);
+    for (int n = 0; n < kSt; ++n) load(n);
+    landed(std::integral_constant<int, kSt - 1>());
     ptx::named_bar_sync(kBarP, kBarPCount);
     if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
     for (int n = 0; n < n_win; ++n) {
-      if (n + 1 < n_win) wait(&sm.bar_kv[(n + 1) % kSt], ((n + 1) / kSt) & 1);
+      landed(std::integral_constant<int, kSt - 3>());  // window n + 1
       ptx::named_bar_sync(kBarP, kBarPCount);
       if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-      if (n >= 1 && loaded < n_win) {
-        const int4 cur = nx;
-        nx = slots(loaded + 1);
-        load(loaded, cur);
-        ++loaded;
-      }
+      if (n >= 1) load(n - 1 + kSt);
     }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
     constexpr uint32_t idO = ptx::idesc_bf16(128, 64, true);
@@ -789,7 +804,6 @@ __global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
         }
       }
       if (n >= w_ragged) {
-        wait(&sm.bar_kv[n % kSt], (n / kSt) & 1);  // landed long ago: makes it visible here
         uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
         for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
           const uint4 x = v4[c];
@@ -879,24 +893,6 @@ int sm_count() {
   return sms;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-  static const EncodeTiled fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (EncodeTiled)f;
-  }();
-  return fn;
-}
-
 // Which kernel takes a call, and its cut of the work.  All of it follows from
 // the host's bounds, so that a captured call replays for any lengths within
 // them.
@@ -979,18 +975,12 @@ cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const Chunk
 template <int kTiles>
 cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                       int64_t tiles, uint32_t *status, cudaStream_t s) {
-  CUtensorMap mk, mv;
-  // without lists (max_kv = 0) there need be no pools: the maps are not used
-  const bool pools = a.max_kv > 0;
-  if (!make_gather_map(&mk, pools ? a.k : a.q, pools ? a.S : 1, a.Hkv) ||
-      !make_gather_map(&mv, pools ? a.v : a.q, pools ? a.S : 1, a.Hkv))
-    return cudaErrorInvalidValue;
   const int smem = (int)sizeof(TcSmem<kTiles>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<kTiles>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   chunk_tc_kernel<kTiles><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kTiles * 128 + 64, smem, s>>>(
-      mk, mv, a, (__nv_bfloat16 *)out, lse, part, status);
+      a, (__nv_bfloat16 *)out, lse, part, status);
   return cudaGetLastError();
 }
 
@@ -1010,18 +1000,6 @@ cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const Chunk
 }
 
 }  // namespace
-
-bool make_gather_map(CUtensorMap *m, const void *pool, int S, int Hkv) {
-  const EncodeTiled enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)Hkv * kD, (cuuint64_t)S};
-  const cuuint64_t strides[1] = {(cuuint64_t)Hkv * kD * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kD, 1};  // a gather's box is one row high
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);

@@ -51,29 +51,6 @@ constexpr uint32_t kTcTileBytes = kTcKeys * kD * 2;      // one K or V window of
 constexpr long long kTcWaitBudget = 1000000000LL;        // SM clocks (about 0.5 s)
 constexpr size_t kTcStatusBytes = 256;                   // status word at the workspace's start
 
-// 2-D view [S][Hkv * 64] of a bf16 pool for gathers of four 64-column rows,
-// 128-byte swizzle.  False if the driver refuses it.
-bool make_gather_map(CUtensorMap *m, const void *pool, int S, int Hkv);
-
-// Four pool rows (64 columns from column x on) to 512 consecutive bytes of a
-// 128-byte-swizzled tile.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
-                                            const int4 &row) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"((uint64_t)m), "r"(bar), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w)
-      : "memory");
-}
-
-// pool rows of list entries j .. j + 3 (entries from `end` on: row 0)
-__device__ __forceinline__ int4 chunk_slots4(const ChunkBatch &a, const ChunkReq &r, int j, int end) {
-  int s[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) s[e] = j + e < end ? (int)chunk_slot(a, r, j + e) : 0;
-  return make_int4(s[0], s[1], s[2], s[3]);
-}
-
 // A bf16 pair with an infinity or NaN in it.
 __device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
 __device__ __forceinline__ bool nonfinite_hi(uint32_t w) {
