@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
 // bf16, more rows: tcgen05.  CTA = kTiles tiles of 128 packed rows of one KV
 // head (both read the same K/V windows) x one key split.
 //   warps 4 i .. 4 i + 3  softmax of tile i (thread = packed row = TMEM lane)
-//   then the producer warp: 128-key K and V windows through a ring of stages,
+//   then the producer warps: 128-key K and V windows through a ring of stages,
 //        gathered by 16-byte cp.async into the 128-byte-swizzled layout that
 //        the MMA reads.  (TMA gathers of four rows deliver one 128-byte row
 //        per 24 clocks: 353 TFLOP/s at 1,024 rows over 16,384 entries.)
@@ -534,10 +534,11 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
 // return.
 // ---------------------------------------------------------------------------
 constexpr int kBarP = 3;         // hardware barriers kBarP + i (0 is __syncthreads)
-constexpr int kBarPCount = 192;  // a softmax group, the producer warp, the MMA warp
 constexpr float kRescale = 8.f;  // log2 units
 
 constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 6; }
+constexpr int tc_producers(int tiles) { return tiles == 1 ? 1 : 3; }
+constexpr int tc_threads(int tiles) { return 128 * tiles + 32 * tc_producers(tiles) + 32; }
 
 template <int kTiles>
 struct __align__(1024) TcSmem {
@@ -550,12 +551,14 @@ struct __align__(1024) TcSmem {
 };
 
 template <int kTiles>
-__global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
+__global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     chunk_tc_kernel(const ChunkBatch a, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
                     const ChunkParts part, uint32_t *status) {
   constexpr int kSt = tc_stages(kTiles);
-  constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + 1;
-  constexpr int kThreads = kTiles * 128 + 64;
+  constexpr int kProducers = tc_producers(kTiles);
+  constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + kProducers;
+  // a softmax group, the producers, the MMA warp
+  constexpr int kBarPCount = 128 + 32 * kProducers + 32;
   constexpr uint32_t kCols = kTiles == 1 ? 256 : 512;
   constexpr uint32_t kColO = 128 * kTiles, kColQ = 192 * kTiles;
   extern __shared__ uint8_t smem_raw[];
@@ -613,43 +616,48 @@ __global__ void __launch_bounds__(kTiles * 128 + 64, kTiles == 1 ? 2 : 1)
       atomicOr(status, kStatusWaitTimeout);
   };
 
-  if (warp == kProdWarp) {
-    // A window is 128 rows of K and of V, 16 bytes per lane and copy: copy
-    // step s takes entries 4 s .. 4 s + 3, eight lanes each.  Lane l holds the
-    // pool rows of entries l, l + 32, l + 64, l + 96, loaded a window ahead.
-    // A stage is refilled without a wait: generation n + 1 of the last tile's
-    // barrier completes only after its softmax has seen S(n), whose commit
-    // tracks P.V(n - 1), the last reader of that stage.  Each window is one
-    // group of copies (empty past the end), so that "window n + 1 has landed"
-    // is a count of groups still in flight.
-    const int key0 = lane >> 3, ch = lane & 7;
+  if (warp >= kProdWarp && warp < kMmaWarp) {
+    // A window is 128 rows of K and of V, 16 bytes per lane and copy: step s
+    // copies entries 4 s .. 4 s + 3, eight lanes each, and producer warp p
+    // takes steps kSteps p .. of every window (one warp per sub-partition, so
+    // that no softmax warp shares its issue slots with all of them: +x %).
+    // A lane's pool rows are loaded a window ahead.  A stage is refilled
+    // without a wait: generation n + 1 of the last tile's barrier completes
+    // only after its softmax has seen S(n), whose commit tracks P.V(n - 1),
+    // the last reader of that stage.  Each window is one group of copies
+    // (empty past the end), so that "window n + 1 has landed" is a count of
+    // groups still in flight.
+    constexpr int kSteps = (32 + kProducers - 1) / kProducers;
+    const int s0 = (warp - kProdWarp) * kSteps;
+    const int key0 = 4 * s0 + (lane >> 3), ch = lane & 7;
     const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kTcTileBytes;
-    const uint32_t sw0 = (ch ^ key0) << 4, sw1 = (ch ^ (key0 + 4)) << 4;  // even, odd steps
+    const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
     const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
     const char *vg = (const char *)a.v + (g * kD + ch * 8) * 2;
     const int64_t pitch = (int64_t)a.Hkv * kD * 2;
-    int nx[4];
+    int nx[kSteps];
     auto slots = [&](int n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = c0 + n * kTcKeys + 32 * e + lane;
-        nx[e] = n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
+      for (int s = 0; s < kSteps; ++s) {
+        const int j = c0 + n * kTcKeys + key0 + 4 * s;
+        nx[s] = s0 + s < 32 && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
       }
     };
     auto load = [&](int n) {  // window n from the indices at hand, then those of n + 1
-      int cur[4];
+      int cur[kSteps];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cur[e] = nx[e];
+      for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
       slots(n + 1);
       if (n < n_win) {
         const uint32_t at = (n % kSt) * kTcTileBytes;
 #pragma unroll
-        for (int s = 0; s < 32; ++s) {
-          const int sl = __shfl_sync(0xffffffffu, cur[s >> 3], 4 * (s & 7) + key0);
-          const int64_t off = max(sl, 0) * pitch;
-          const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
-          cp_async16(kd + to, kg + off, sl >= 0);  // past the end: zeros
-          cp_async16(vd + to, vg + off, sl >= 0);
+        for (int s = 0; s < kSteps; ++s) {
+          if (s0 + s < 32) {
+            const int64_t off = max(cur[s], 0) * pitch;
+            const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
+            cp_async16(kd + to, kg + off, cur[s] >= 0);  // past the end: zeros
+            cp_async16(vd + to, vg + off, cur[s] >= 0);
+          }
         }
       }
       asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -979,7 +987,7 @@ cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkPar
   cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<kTiles>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_tc_kernel<kTiles><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kTiles * 128 + 64, smem, s>>>(
+  chunk_tc_kernel<kTiles><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), tc_threads(kTiles), smem, s>>>(
       a, (__nv_bfloat16 *)out, lse, part, status);
   return cudaGetLastError();
 }
