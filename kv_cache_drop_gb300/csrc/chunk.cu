@@ -15,11 +15,14 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Split-KV partials: [n_rows][Hq][ns], m in log2 units.
+// Split-KV partials: [n_rows][Hq][ns], m in log2 units.  A row whose visible
+// entries lie in one split is written out by that split; the merge passes it
+// over.
 struct ChunkParts {
   float2 *ml;
   float *o;
   int ns, chunk;
+  __device__ __forceinline__ bool direct(int lim) const { return ns == 1 || lim <= chunk; }
 };
 constexpr int kMaxSplit = 1024;  // the merge keeps one weight per split in shared memory
 
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(kSimtThreads)
   const int last = (min(rows, r0 + kSimt) - 1) / grp;  // the tile's last token
   const int c0 = split * part.chunk;
   const int c1 = min(rq.limit(last), c0 + part.chunk);
-  if (part.ns > 1 && c0 >= c1) return;  // the merge reads only splits with visible entries
+  if (split > 0 && c0 >= c1) return;  // the merge reads only splits with visible entries
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   int lim[4];
 #pragma unroll
@@ -132,7 +135,8 @@ __global__ void __launch_bounds__(kSimtThreads)
     const int r = r0 + 4 * ty + p;
     if (r >= rows) continue;
     const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
-    if (part.ns == 1) {
+    if (part.direct(lim[p])) {
+      if (split > 0) continue;
       const bool none = lim[p] == 0;
       float y[4];
 #pragma unroll
@@ -147,9 +151,63 @@ __global__ void __launch_bounds__(kSimtThreads)
   }
 }
 
-// Joins the splits of a row by their log-sum-exp: a CTA per (row, head), eight
-// groups of 16 threads each summing every eighth split's output row (16 bytes
-// per load).  Launched as a programmatic dependent of the attention kernel.
+// The splits that hold row t's visible entries; 0 where there is nothing to
+// merge (written by its one split, or no request's row).
+__device__ __forceinline__ int merge_used(const ChunkBatch &a, const ChunkParts &part, int t) {
+  int lo = 0, hi = a.B;  // the request that holds row t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.q_indptr + mid) <= t) lo = mid; else hi = mid;
+  }
+  const ChunkReq rq = chunk_req(a, lo);
+  const int i = t - rq.q0;
+  if (i < 0 || i >= rq.m) return 0;
+  const int lim = rq.limit(i);
+  return part.direct(lim) ? 0 : (lim + part.chunk - 1) / part.chunk;
+}
+
+// Joins the splits of a row by their log-sum-exp; launched as a programmatic
+// dependent of the attention kernel.  Up to kWarpMerge splits: a warp per
+// (row, head), two columns per lane, one split's weight per lane (a CTA per
+// row and head took 120 us for 4,097 rows of 24 heads in two splits).
+constexpr int kWarpMerge = 32;
+constexpr int kMergeWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    chunk_merge_warp_kernel(const ChunkBatch a, T *out, float *lse, const ChunkParts part) {
+  const int64_t w = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int t = (int)(w / a.Hq);
+  const int used = t < a.n_rows ? merge_used(a, part, t) : 0;
+  // every warp waits, so that this grid never ends before the one it follows
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (used == 0) return;
+  const float2 ml = lane < used ? __ldcg(part.ml + w * part.ns + lane) : make_float2(-INFINITY, 0.f);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+  float L = ml.y * f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float x0 = 0.f, x1 = 0.f;
+  const float2 *po = reinterpret_cast<const float2 *>(part.o + w * part.ns * kD) + lane;
+#pragma unroll 8
+  for (int s = 0; s < used; ++s) {
+    const float2 v = __ldcg(po + s * (kD / 2));
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+    x0 = fmaf(v.x, fs, x0);
+    x1 = fmaf(v.y, fs, x1);
+  }
+  x0 /= L;
+  x1 /= L;
+  if constexpr (sizeof(T) == 4) reinterpret_cast<float2 *>(out + w * kD)[lane] = make_float2(x0, x1);
+  else reinterpret_cast<__nv_bfloat162 *>(out + w * kD)[lane] = __floats2bfloat162_rn(x0, x1);
+  if (lse && lane == 0) lse[w] = M * kLn2 + logf(L);
+}
+
+// More splits (few rows): a CTA per (row, head), eight groups of 16 threads
+// each summing every eighth split's output row, 16 bytes per load.
 constexpr int kMergeThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -160,16 +218,9 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int64_t w = blockIdx.x;
   const int t = (int)(w / a.Hq);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int lo = 0, hi = a.B;  // the request that holds row t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_indptr[mid] <= t) lo = mid; else hi = mid;
-  }
-  const ChunkReq rq = chunk_req(a, lo);
-  const int i = t - rq.q0;
-  if (i < 0 || i >= rq.m) return;  // no request's row: left as it is
-  const int used = (rq.limit(i) + part.chunk - 1) / part.chunk;
+  const int used = merge_used(a, part, t);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (used == 0) return;
   const float2 *ml = part.ml + w * part.ns;
   float M = -INFINITY;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
@@ -208,7 +259,6 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   red[sg][cg] = acc;
   __syncthreads();
-  const bool none = used == 0;
   if (threadIdx.x < kD / 4) {
     float y[4] = {};
     for (int g = 0; g < 8; ++g) {
@@ -219,10 +269,10 @@ __global__ void __launch_bounds__(kMergeThreads)
       y[3] += v.w;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = none ? 0.f : y[e] / L;
+    for (int e = 0; e < 4; ++e) y[e] /= L;
     store4<T>(out + w * kD + 4 * threadIdx.x, y);
   }
-  if (lse && threadIdx.x == 0) lse[w] = none ? -INFINITY : M * kLn2 + logf(L);
+  if (lse && threadIdx.x == 0) lse[w] = M * kLn2 + logf(L);
 }
 
 
@@ -287,7 +337,7 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   if (rows == 0 || g >= a.Hkv) return;
   const int c0 = split * part.chunk, c1 = min(rq.limit(rq.m - 1), c0 + part.chunk);
-  if (part.ns > 1 && c0 >= c1) return;
+  if (split > 0 && c0 >= c1) return;
   const int nk = max(0, c1 - c0), n_tiles = (nk + kSKeys - 1) / kSKeys;
   const uint32_t wsm = ptx::smem_addr(smem_raw) + warp * kSt * 2 * kSTile;
   uint8_t *const wsm_g = smem_raw + warp * kSt * 2 * kSTile;
@@ -485,7 +535,8 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
       const int r = rt * 16 + gid + 8 * hh;
       if (r >= rows) continue;
       const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
-      if (part.ns == 1) {
+      if (part.direct(lim[rt][hh] + c0)) {
+        if (split > 0) continue;
         const bool none = lim[rt][hh] <= 0;
         const float inv = none ? 0.f : 1.f / x;
 #pragma unroll
@@ -576,7 +627,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   const int64_t r1 = min(rows, r0 + kTiles * kTcRows);
   const int c0 = split * part.chunk;
   const int c1 = min(rq.limit((int)((r1 - 1) / grp)), c0 + part.chunk);
-  if (part.ns > 1 && c0 >= c1) return;  // the merge reads only splits with visible entries
+  if (split > 0 && c0 >= c1) return;  // the merge reads only splits with visible entries
   const int n_win = c1 > c0 ? (c1 - c0 + kTcKeys - 1) / kTcKeys : 0;
   // first window with an entry hidden from a row of this CTA (or past c1)
   const int w_ragged = max(0, min(rq.limit((int)(r0 / grp)), c1) - c0) / kTcKeys;
@@ -740,7 +791,10 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     ptx::named_bar_sync(kBarP + i, kBarPCount);
     const float2 scale2 = make_float2(kScale, kScale);
     float m_run = -INFINITY;
-    float2 l2 = make_float2(0.f, 0.f);
+    // row sum: four chains, so that no addition waits for the one before
+    float2 l4[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
     for (int n = 0; n < n_win; ++n) {
       wait(&sm.bar_s[i], n & 1);
       ptx::tc_fence_after();
@@ -777,8 +831,11 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       if (need) {
         alpha = ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
         m_run = m_new;
-        l2.x *= alpha;
-        l2.y *= alpha;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          l4[k].x *= alpha;
+          l4[k].y *= alpha;
+        }
       }
       const float mref = m_run == -INFINITY ? 0.f : m_run;
       const float2 neg2 = make_float2(-mref, -mref);
@@ -793,7 +850,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
                                       scale2, neg2);
           const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-          l2 = __fadd2_rn(l2, p);
+          l4[k & 3] = __fadd2_rn(l4[k & 3], p);
           pw[k] = pack2(p.x, p.y);
         }
         ptx::tmem_st16(tS + 16 * qtr, pw);
@@ -861,8 +918,10 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         }
       }
     }
-    const float l = l2.x + l2.y;
-    if (valid && part.ns == 1) {
+    const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+    const float l = la.x + la.y;
+    const bool direct = part.direct(lim);
+    if (valid && direct && split == 0) {
       const bool none = lim == 0;
       const float inv = none ? 0.f : 1.f / l;
       uint4 *dst = reinterpret_cast<uint4 *>(out + row * kD);
@@ -876,7 +935,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         dst[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
       if (lse) lse[row] = none ? -INFINITY : m_run * kLn2 + logf(l);
-    } else if (valid) {
+    } else if (valid && !direct) {
       const int64_t pi = row * part.ns + split;
       float4 *dst = reinterpret_cast<float4 *>(part.o + pi * kD);
 #pragma unroll
@@ -995,16 +1054,19 @@ cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkPar
 template <typename T>
 cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                          cudaStream_t s) {
+  const int64_t items = (int64_t)a.n_rows * a.Hq;
+  const bool warps = part.ns <= kWarpMerge;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.n_rows * a.Hq));
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3((unsigned)(warps ? (items + kMergeWarps - 1) / kMergeWarps : items));
+  cfg.blockDim = dim3(warps ? kMergeWarps * 32 : kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<T>, a, (T *)out, lse, part);
+  return cudaLaunchKernelEx(&cfg, warps ? chunk_merge_warp_kernel<T> : chunk_merge_kernel<T>, a,
+                            (T *)out, lse, part);
 }
 
 }  // namespace
