@@ -1286,6 +1286,8 @@ akv_status check_chunk(const akv_shape *shape, int32_t B, int32_t n_rows, int32_
     return fail(AKV_ERR_UNSUPPORTED, "chunk calls support B <= 65535 and Hq <= 65535");
   if (max_kv > kMaxList)
     return fail(AKV_ERR_UNSUPPORTED, "chunk calls support max_kv <= %d", kMaxList);
+  if ((int64_t)max_q * (shape->Hq / shape->Hkv) > kMaxList)
+    return fail(AKV_ERR_UNSUPPORTED, "chunk calls support %d rows per KV head", kMaxList);
   if (max_kv > 0 && S == 0) return fail(AKV_ERR_INVALID, "lists over an empty pool (S = 0)");
   return AKV_OK;
 }

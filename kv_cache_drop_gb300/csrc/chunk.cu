@@ -12,7 +12,6 @@
 namespace akv {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Split-KV partials: [n_rows][Hq][ns], m in log2 units.  A row whose visible
@@ -286,43 +285,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 // registers for P V.  Bound by the gather from HBM; tcgen05 would spend a
 // 128-row tile on 8 rows.
 // ---------------------------------------------------------------------------
-constexpr int kSKeys = 16;
-constexpr int kSTile = kSKeys * kD * 2;    // bytes of a K (or V) tile
-constexpr int kSHeads = 8;                 // warps (KV heads) per CTA at most
 constexpr int small_stages(int rt) { return rt == 1 ? 3 : 6; }
-constexpr float kScale = 0.125f * kLog2e;  // scores to log2 units
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0));
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-// byte offset of (row, 16-byte chunk) in a [16][64] bf16 tile
-__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
-  return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
-}
 
 template <int kRT>
 __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
@@ -953,13 +916,6 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // Which kernel takes a call, and its cut of the work.  All of it follows from
 // the host's bounds, so that a captured call replays for any lengths within
 // them.
@@ -991,7 +947,7 @@ void split_keys(ChunkPlan *p, int64_t ctas, int64_t want, int64_t resident, int 
 
 ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   ChunkPlan p;
-  const int sms = sm_count();
+  const int sms = chunk_sms();
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
   if (dtype == AKV_BF16 && rows <= 32) {
     p.kind = rows <= 16 ? kSmallKind : kSmallKind + 1;

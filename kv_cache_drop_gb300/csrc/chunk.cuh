@@ -51,6 +51,52 @@ constexpr uint32_t kTcTileBytes = kTcKeys * kD * 2;      // one K or V window of
 constexpr long long kTcWaitBudget = 1000000000LL;        // SM clocks (about 0.5 s)
 constexpr size_t kTcStatusBytes = 256;                   // status word at the workspace's start
 
+// ---- mma.sync: 16 keys at a time, a warp per KV head ----
+constexpr int kSKeys = 16;
+constexpr int kSTile = kSKeys * kD * 2;  // bytes of a K (or V) tile
+constexpr int kSHeads = 8;               // warps (KV heads) per CTA at most
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScale = 0.125f * kLog2e;  // scores to log2 units
+
+inline int chunk_sms() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// byte offset of (row, 16-byte chunk) in a [16][64] bf16 tile
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
 // A bf16 pair with an infinity or NaN in it.
 __device__ __forceinline__ bool nonfinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
 __device__ __forceinline__ bool nonfinite_hi(uint32_t w) {

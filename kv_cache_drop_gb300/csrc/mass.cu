@@ -8,10 +8,10 @@
 // row of the chunk, so each sum is formed in one fixed order.
 #include "chunk.cuh"
 
+#include <algorithm>
+
 namespace akv {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct MassArgs {
   const float *lse;
@@ -82,10 +82,483 @@ __global__ void __launch_bounds__(kSimtThreads)
   }
 }
 
+// ---------------------------------------------------------------------------
+// bf16, few rows (decode steps): up to 16 kRT packed rows per KV head.  CTA =
+// `chunk` list entries of a request and all KV heads, a warp per head (heads
+// warp, warp + 8, ..), 16 keys at a time: S = Q K^T in m16n8k16 tiles, the
+// weights summed over the rows in registers and shuffles, over the heads in
+// shared memory.  Bound by the gather of K from HBM.
+// ---------------------------------------------------------------------------
+constexpr int kMSt = 6;  // K tiles per warp
+constexpr int kMChunk = 512;
+
+template <int kRT>
+__global__ void __launch_bounds__(kSHeads * 32, 2)
+    mass_small_kernel(const ChunkBatch a, const MassArgs ma, int chunk) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int b = blockIdx.y, c0 = blockIdx.x * chunk;
+  const ChunkReq rq = chunk_req(a, b);
+  if (c0 >= rq.n) return;
+  const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
+  const int nk = min(rq.n - c0, chunk), n_tiles = (nk + kSKeys - 1) / kSKeys;
+  const uint32_t wsm = ptx::smem_addr(smem_raw) + warp * kMSt * kSTile;
+  float *const sums = reinterpret_cast<float *>(smem_raw + warps * kMSt * kSTile);  // [warps][chunk]
+  float *const mine = sums + warp * chunk;
+
+  for (int g = warp; g < a.Hkv; g += warps) {
+    auto load_slot = [&](int t) {
+      const int k = t * kSKeys + lane;
+      return lane < kSKeys && k < nk ? (int)chunk_slot(a, rq, c0 + k) : 0;
+    };
+    const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + g * kD;
+    auto issue = [&](int t, int slot) {
+      if (t < n_tiles) {
+        const uint32_t at = wsm + (t % kMSt) * kSTile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (lane >> 3) + 4 * i, ch = lane & 7;
+          const int sl = __shfl_sync(0xffffffffu, slot, key);
+          cp_async16(at + tile_at(key, ch), kp + (int64_t)sl * a.Hkv * kD + ch * 8,
+                     t * kSKeys + key < nk);
+        }
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    int slot_nx = load_slot(0);
+#pragma unroll
+    for (int t = 0; t < kMSt - 1; ++t) {
+      const int sl = slot_nx;
+      slot_nx = load_slot(t + 1);
+      issue(t, sl);
+    }
+    uint32_t qa[kRT][4][4];
+    float nl[kRT][2];  // -lse in log2 units; -inf for a row that counts nothing
+    int lim[kRT][2];
+#pragma unroll
+    for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = rt * 16 + gid + 8 * hh;
+        const bool ok = r < rows;
+        const int64_t row = (int64_t)(rq.q0 + (ok ? r / grp : 0)) * a.Hq + g * grp + (ok ? r % grp : 0);
+        const uint32_t *src = reinterpret_cast<const uint32_t *>((const __nv_bfloat16 *)a.q + row * kD);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          qa[rt][ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
+          qa[rt][ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
+        }
+        const float v = ok ? __ldg(ma.lse + row) : -INFINITY;
+        nl[rt][hh] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+        lim[rt][hh] = v == -INFINITY ? INT32_MIN : rq.limit(r / grp) - c0;
+      }
+    for (int it = 0; it < n_tiles; ++it) {
+      const int sl = slot_nx;
+      slot_nx = load_slot(it + kMSt);
+      issue(it + kMSt - 1, sl);
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kMSt - 1) : "memory");
+      __syncwarp();
+      const uint32_t kt = wsm + (it % kMSt) * kSTile;
+      const int k0 = it * kSKeys;
+      float s[kRT][2][4];
+#pragma unroll
+      for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+          s[rt][nb][0] = s[rt][nb][1] = s[rt][nb][2] = s[rt][nb][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t kb[4];
+        const int mi = lane >> 3;
+        ldsm4(kt + tile_at((mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), kb);
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt) {
+          mma16816(s[rt][0], qa[rt][ks], kb[0], kb[1]);
+          mma16816(s[rt][1], qa[rt][ks], kb[2], kb[3]);
+        }
+      }
+      // column sums: key 8 nb + 2 tig + e1
+      float cs[2][2];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e1 = 0; e1 < 2; ++e1) {
+          const int key = k0 + nb * 8 + 2 * tig + e1;
+          float x = 0.f;
+#pragma unroll
+          for (int rt = 0; rt < kRT; ++rt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float p = ptx::ex2(fmaf(s[rt][nb][2 * hh + e1], kScale, nl[rt][hh]));
+              x += key < lim[rt][hh] ? p : 0.f;
+            }
+          x += __shfl_xor_sync(0xffffffffu, x, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 8);
+          x += __shfl_xor_sync(0xffffffffu, x, 16);
+          cs[nb][e1] = x;
+        }
+      if (gid < 2) {  // lanes of gid 0 and 1 write the two halves
+        const int key = k0 + gid * 8 + 2 * tig;
+        const float v0 = gid ? cs[1][0] : cs[0][0], v1 = gid ? cs[1][1] : cs[0][1];
+        float2 *dst = reinterpret_cast<float2 *>(mine + key);
+        if (g == warp) *dst = make_float2(v0, v1);
+        else *dst = make_float2(dst->x + v0, dst->y + v1);
+      }
+      __syncwarp();
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < nk; j += blockDim.x) {
+    float x = 0.f;
+    for (int w = 0; w < min(warps, a.Hkv); ++w) x += sums[w * chunk + j];
+    const int64_t at = (int64_t)b * ma.stride + c0 + j;
+    if (ma.in && c0 + j < rq.n - rq.m) x = fmaf(ma.decay, ma.in[at], x);
+    ma.out[at] = x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16, more rows: tcgen05, the scores transposed.  CTA = 256 list entries
+// (two tiles of 128 keys) x a share of the (KV head, 128-row tile) items:
+//   warps 4 i .. 4 i + 3  key tile i: thread = key = TMEM lane, so that the sum
+//        over rows stays in the thread's registers, with no reduction
+//   3 producer warps      K tiles (once per head), Q tiles and the rows' lse
+//        through a ring, by cp.async into the 128-byte-swizzled layout
+//   MMA warp              S^T = K Q^T, both operands from shared memory, into
+//        two TMEM buffers per key tile (2 x 2 x 128 columns), so that the next
+//        scores are computed while the weights of the last are summed
+// Each Q tile serves both key tiles: the 16 KB of a row tile per 32,768
+// weights keep L2 below its limit.  Bound by the exponentials: 8 per clock and
+// sub-partition, 512 clocks per 128 x 128 tile against 256 for its MMAs.
+// The items of an entry block may be shared by several CTAs (`parts`, when
+// there are few blocks); their sums are added by mass_join_kernel in one
+// fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kQSt = 4;
+constexpr int kNlSt = 8;
+static_assert(kNlSt >= kQSt + 2, "slots of the rows' lse");
+constexpr int kMProducers = 3;
+constexpr int kMThreads = 256 + 32 * kMProducers + 32;
+constexpr int kMSteps = (32 + kMProducers - 1) / kMProducers;  // 4-row copy steps per warp and tile
+constexpr int kMBlock = 2 * kTcKeys;
+constexpr int kInFlight = 2;  // items whose copies are under way while the next is issued
+
+struct __align__(1024) MassTcSmem {
+  uint8_t k[2][2][kTcTileBytes];  // [buffer][key tile]
+  uint8_t q[kQSt][kTcTileBytes];
+  // -lse in log2 units of an item's rows.  Item x's slot was item x - kNlSt's:
+  // the Q stage of x is free once the MMAs of x - kQSt are done, which began
+  // when the weights of x - kQSt - 2 had been summed, so kQSt + 2 slots do.
+  float nl[kNlSt][kTcRows];
+  uint64_t k_full[2], k_free[2], q_full[kQSt], q_free[kQSt];
+  uint64_t s_full[2][2], s_free[2][2];  // [key tile][buffer]
+  uint32_t tmem_base;
+  uint32_t gave_up;
+};
+
+// packed row x of a tile whose first row is token i0, head h0 of the group
+struct RowSplit {
+  int grp;
+  uint32_t inv;  // ceil(2^20 / grp): exact for h0 + x < 256, grp <= 128
+  __device__ __forceinline__ explicit RowSplit(int g)
+      : grp(g), inv(((1u << 20) + g - 1) / g) {}
+  __device__ __forceinline__ int token(int v) const {
+    return grp <= 128 ? (int)(((uint32_t)v * inv) >> 20) : (v >= grp);
+  }
+};
+
+__global__ void __launch_bounds__(kMThreads, 1)
+    mass_tc_kernel(const ChunkBatch a, const MassArgs ma, int parts, float *partial,
+                   uint32_t *status) {
+  extern __shared__ uint8_t smem_raw[];
+  MassTcSmem &sm = *reinterpret_cast<MassTcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                   ~uintptr_t(1023));
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = blockIdx.x % parts, b = blockIdx.y;
+  const int j0 = (int)(blockIdx.x / parts) * kMBlock;
+  const ChunkReq rq = chunk_req(a, b);
+  if (j0 >= rq.n) return;
+  const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
+  // row tiles from the first that sees an entry of this block on
+  const int old = rq.n - rq.m;  // entries older than the chunk (negative: some rows see nothing)
+  const int n_tiles = (rows + kTcRows - 1) / kTcRows;
+  const int t0 = min(n_tiles, (int)((int64_t)max(0, j0 - old) * grp / kTcRows));
+  const int per_head = n_tiles - t0;
+  const int64_t items = (int64_t)per_head * a.Hkv;
+  const int64_t it0 = items * part / parts;
+  const int mine = (int)(items * (part + 1) / parts - it0);
+  const int g0 = mine ? (int)(it0 / per_head) : 0, tile0 = mine ? t0 + (int)(it0 % per_head) : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&sm.k_full[s], kMProducers);
+      ptx::mbar_init(&sm.k_free[s], 1);
+      for (int u = 0; u < 2; ++u) {
+        ptx::mbar_init(&sm.s_full[s][u], 1);
+        ptx::mbar_init(&sm.s_free[s][u], 4);
+      }
+    }
+    for (int s = 0; s < kQSt; ++s) {
+      ptx::mbar_init(&sm.q_full[s], kMProducers);
+      ptx::mbar_init(&sm.q_free[s], 1);
+    }
+    sm.gave_up = 0u;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 8 + kMProducers) ptx::tmem_alloc(&sm.tmem_base, 512);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (!ptx::mbar_wait_grid(bar, parity, &sm.gave_up, 1u, kTcWaitBudget))
+      atomicOr(status, kStatusWaitTimeout);
+  };
+
+  if (warp >= 8 && warp < 8 + kMProducers) {
+    const int s0 = (warp - 8) * kMSteps;
+    const int row0 = 4 * s0 + (lane >> 3), ch = lane & 7;  // this lane's row of step 0
+    const uint32_t sw0 = (ch ^ (row0 & 7)) << 4, sw1 = (ch ^ ((row0 + 4) & 7)) << 4;
+    const uint32_t kd = ptx::smem_addr(sm.k[0][0]) + row0 * 128;
+    const uint32_t qd = ptx::smem_addr(sm.q[0]) + row0 * 128;
+    const int64_t pitch = (int64_t)a.Hkv * kD * 2;
+    const RowSplit sp(grp);
+    // Each item is one group of copies; its barrier is arrived on once the
+    // group has landed, kInFlight items later.
+    uint64_t *pend[kInFlight];
+#pragma unroll
+    for (int e = 0; e < kInFlight; ++e) pend[e] = nullptr;
+    auto landed = [&](uint64_t *next) {  // the oldest pending item, then `next` joins the queue
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kInFlight) : "memory");
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (pend[0] && lane == 0) ptx::mbar_arrive(pend[0]);
+#pragma unroll
+      for (int e = 0; e + 1 < kInFlight; ++e) pend[e] = pend[e + 1];
+      pend[kInFlight - 1] = next;
+    };
+    int kn = 0, g = g0, t = tile0;
+    for (int qn = 0; qn < mine; ++qn) {
+      if (qn == 0 || t == t0) {  // the head's K tiles
+        const int kb = kn & 1;
+        if (kn >= 2) wait(&sm.k_free[kb], ((kn >> 1) - 1) & 1);
+        const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int s = 0; s < kMSteps; ++s)
+            if (s0 + s < 32) {
+              const int j = j0 + i * kTcKeys + row0 + 4 * s;
+              const bool ok = j < rq.n;
+              const int64_t off = ok ? chunk_slot(a, rq, j) * pitch : 0;
+              cp_async16(kd + (kb * 2 + i) * kTcTileBytes + s * 512 + (s & 1 ? sw1 : sw0), kg + off, ok);
+            }
+        landed(&sm.k_full[kb]);
+        ++kn;
+      }
+      const int st = qn % kQSt;
+      if (qn >= kQSt) wait(&sm.q_free[st], ((qn / kQSt) - 1) & 1);
+      const int r0 = t * kTcRows, i0 = r0 / grp, h0 = r0 - i0 * grp;
+      const char *qg = (const char *)a.q + ((int64_t)(rq.q0 + i0) * a.Hq + g * grp) * (kD * 2) + ch * 16;
+#pragma unroll
+      for (int s = 0; s < kMSteps; ++s)
+        if (s0 + s < 32) {
+          const int x = row0 + 4 * s, v = h0 + x, i = sp.token(v);
+          const bool ok = r0 + x < rows;
+          const int64_t off = ok ? ((int64_t)i * a.Hq + (v - i * grp)) * (kD * 2) : 0;
+          cp_async16(qd + st * kTcTileBytes + s * 512 + (s & 1 ? sw1 : sw0), qg + off, ok);
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // the lse of this warp's rows
+        const int x = 4 * s0 + lane + 32 * u;
+        if (lane + 32 * u < 4 * kMSteps && x < kTcRows) {
+          const int v = h0 + x, i = sp.token(v);
+          float l = -INFINITY;
+          if (r0 + x < rows)
+            l = __ldg(ma.lse + (int64_t)(rq.q0 + i0 + i) * a.Hq + g * grp + (v - i * grp));
+          sm.nl[qn % kNlSt][x] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        }
+      }
+      landed(&sm.q_full[st]);
+      if (++t == n_tiles) {
+        t = t0;
+        ++g;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kInFlight; ++e) landed(nullptr);
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+  } else if (warp == 8 + kMProducers) {
+    constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
+    constexpr uint64_t kTileStep = kTcTileBytes >> 4;
+    const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0][0]));
+    const uint64_t dq = ptx::sdesc_sw128(ptx::smem_addr(sm.q[0]));
+    int kn = 0, t = tile0;
+    for (int qn = 0; qn < mine; ++qn) {
+      if (qn == 0 || t == t0) {  // the next head
+        if (kn > 0 && lane == 0) ptx::mma_commit(&sm.k_free[(kn - 1) & 1]);
+        wait(&sm.k_full[kn & 1], (kn >> 1) & 1);
+        ++kn;
+      }
+      if (++t == n_tiles) t = t0;
+      const int st = qn % kQSt, buf = qn & 1;
+      wait(&sm.q_full[st], (qn / kQSt) & 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (qn >= 2) wait(&sm.s_free[i][buf], ((qn >> 1) - 1) & 1);
+        ptx::tc_fence_after();
+        if (lane == 0) {
+          const uint64_t ak = dk + (((kn - 1) & 1) * 2 + i) * kTileStep, bq = dq + st * kTileStep;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ss(tmem + (i * 2 + buf) * 128, ak + 2 * kk, bq + 2 * kk, idS, kk > 0);
+          ptx::mma_commit(&sm.s_full[i][buf]);
+          if (i == 1) ptx::mma_commit(&sm.q_free[st]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    const int i = warp >> 2;
+    const int key = j0 + i * kTcKeys + (threadIdx.x & 127);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    // packed rows [r_min, rows) see this key (none past the list's end)
+    const int64_t r_min = key < rq.n ? (int64_t)max(0, key - old) * grp : INT32_MAX;
+    // the last key of this tile that is listed sees the fewest rows
+    const int last = min(rq.n, j0 + (i + 1) * kTcKeys) - 1;
+    const int64_t all_see = (int64_t)max(0, last - old) * grp;
+    const float2 scale2 = make_float2(kScale, kScale);
+    float2 sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
+    int t = tile0;
+    for (int qn = 0; qn < mine; ++qn) {
+      const int buf = qn & 1, r0 = t * kTcRows;
+      if (++t == n_tiles) t = t0;
+      wait(&sm.s_full[i][buf], (qn >> 1) & 1);
+      ptx::tc_fence_after();
+      const uint32_t ts = tmem + lane_base + (i * 2 + buf) * 128;
+      uint32_t sr[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + 32 * c, sr + 32 * c);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+      const float4 *nl4 = reinterpret_cast<const float4 *>(sm.nl[qn % kNlSt]);
+      if (r0 >= all_see && r0 + kTcRows <= rows) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float4 nl = nl4[c];
+          const float2 x0 = __ffma2_rn(
+              make_float2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), scale2,
+              make_float2(nl.x, nl.y));
+          const float2 x1 = __ffma2_rn(
+              make_float2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])), scale2,
+              make_float2(nl.z, nl.w));
+          sum[(2 * c) & 3] = __fadd2_rn(sum[(2 * c) & 3], make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y)));
+          sum[(2 * c + 1) & 3] =
+              __fadd2_rn(sum[(2 * c + 1) & 3], make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y)));
+        }
+      } else {
+        // rows [lo, hi) of the tile see this key
+        const int lo = (int)min((int64_t)kTcRows, max((int64_t)0, r_min - r0));
+        const int hi = min(kTcRows, rows - r0);
+        const float *nl = sm.nl[qn % kNlSt];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) {
+          const float p = ptx::ex2(fmaf(__uint_as_float(sr[c]), kScale, nl[c]));
+          if (c >= lo && c < hi) sum[c & 3].x += p;
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.s_free[i][buf]);
+    }
+    const float2 s2 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+    if (key < rq.n) {
+      float x = s2.x + s2.y;
+      if (parts > 1) {
+        partial[((int64_t)part * a.B + b) * a.max_kv + key] = x;
+      } else {
+        const int64_t at = (int64_t)b * ma.stride + key;
+        if (ma.in && key < old) x = fmaf(ma.decay, ma.in[at], x);
+        ma.out[at] = x;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 8 + kMProducers) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Sum of the parts of each entry, in part order, and what it had.
+__global__ void __launch_bounds__(256)
+    mass_join_kernel(const ChunkBatch a, const MassArgs ma, int parts, const float *partial) {
+  const int b = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+  const ChunkReq rq = chunk_req(a, b);
+  if (j >= rq.n) return;
+  float x = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) x += partial[((int64_t)p * a.B + b) * a.max_kv + j];
+  const int64_t at = (int64_t)b * ma.stride + j;
+  if (ma.in && j < rq.n - rq.m) x = fmaf(ma.decay, ma.in[at], x);
+  ma.out[at] = x;
+}
+
+struct MassPlan {
+  int kind;   // 0 CUDA cores; 1, 2: mma.sync with that many 16-row tiles; 3: tcgen05
+  int chunk;  // entries per CTA (kinds 1, 2)
+  int parts;  // CTAs per entry block (kind 3)
+};
+
+MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
+  MassPlan p{0, 0, 1};
+  const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+  const int sms = chunk_sms();
+  if (dtype != AKV_BF16) return p;
+  if (rows <= 32) {
+    p.kind = rows <= 16 ? 1 : 2;
+    p.chunk = kMChunk;
+    while (p.chunk > 64 && (int64_t)B * ((max_kv + p.chunk - 1) / p.chunk) < 2LL * sms) p.chunk /= 2;
+    return p;
+  }
+  p.kind = 3;
+  // about four waves of CTAs, none with less than four row tiles
+  const int64_t blocks = (int64_t)B * ((max_kv + kMBlock - 1) / kMBlock);
+  const int64_t items = (rows + kTcRows - 1) / kTcRows * Hkv;
+  p.parts = (int)std::max<int64_t>(
+      1, std::min<int64_t>(std::min<int64_t>((4LL * sms + blocks - 1) / std::max<int64_t>(1, blocks), 64),
+                           items / 4));
+  return p;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int kRT>
+cudaError_t launch_small(const ChunkBatch &a, const MassArgs &ma, int chunk, cudaStream_t s) {
+  const int warps = std::min(a.Hkv, kSHeads);
+  const int smem = warps * (kMSt * kSTile + chunk * (int)sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(mass_small_kernel<kRT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  mass_small_kernel<kRT><<<dim3((unsigned)((a.max_kv + chunk - 1) / chunk), a.B), warps * 32, smem, s>>>(
+      a, ma, chunk);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t mass_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
-  return 0;
+  const MassPlan p = mass_plan(dtype, B, Hq, Hkv, max_q, max_kv);
+  return kTcStatusBytes + (p.parts > 1 ? up256((size_t)p.parts * B * max_kv * sizeof(float)) : 0);
 }
 
 cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
@@ -96,9 +569,25 @@ cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   const ChunkBatch a{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q, k,
                      nullptr};
   const MassArgs ma{lse, decay, in, out, stride};
-  const dim3 grid((unsigned)((max_kv + kSimt - 1) / kSimt), B);
-  if (dtype == AKV_BF16) mass_simt_kernel<__nv_bfloat16><<<grid, kSimtThreads, 0, s>>>(a, ma);
-  else mass_simt_kernel<float><<<grid, kSimtThreads, 0, s>>>(a, ma);
+  const MassPlan p = mass_plan(dtype, B, Hq, Hkv, max_q, max_kv);
+  if (p.kind == 0) {
+    mass_simt_kernel<float>
+        <<<dim3((unsigned)((max_kv + kSimt - 1) / kSimt), B), kSimtThreads, 0, s>>>(a, ma);
+    return cudaGetLastError();
+  }
+  if (p.kind < 3)
+    return p.kind == 1 ? launch_small<1>(a, ma, p.chunk, s) : launch_small<2>(a, ma, p.chunk, s);
+  float *const partial = (float *)((char *)ws + kTcStatusBytes);
+  const int smem = (int)sizeof(MassTcSmem) + 1024;
+  cudaError_t e =
+      cudaFuncSetAttribute(mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (max_kv + kMBlock - 1) / kMBlock;
+  mass_tc_kernel<<<dim3((unsigned)(blocks * p.parts), B), kMThreads, smem, s>>>(
+      a, ma, p.parts, partial, (uint32_t *)ws);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.parts == 1) return e;
+  mass_join_kernel<<<dim3((unsigned)((max_kv + 255) / 256), B), 256, 0, s>>>(a, ma, p.parts, partial);
   return cudaGetLastError();
 }
 
