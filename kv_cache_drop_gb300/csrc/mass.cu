@@ -222,51 +222,56 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 
 // ---------------------------------------------------------------------------
 // bf16, more rows: tcgen05, the scores transposed.  CTA = 256 list entries
-// (two tiles of 128 keys) x a share of the (KV head, 128-row tile) items:
+// (two tiles of 128 keys) x a share of the (KV head, 256-row tile) items:
 //   warps 4 i .. 4 i + 3  key tile i: thread = key = TMEM lane, so that the sum
 //        over rows stays in the thread's registers, with no reduction
 //   3 producer warps      K tiles (once per head), Q tiles and the rows' lse
 //        through a ring, by cp.async into the 128-byte-swizzled layout
-//   MMA warp              S^T = K Q^T, both operands from shared memory, into
-//        two TMEM buffers per key tile (2 x 2 x 128 columns), so that the next
-//        scores are computed while the weights of the last are summed
-// Each Q tile serves both key tiles: the 16 KB of a row tile per 32,768
-// weights keep L2 below its limit.  Bound by the exponentials: 8 per clock and
-// sub-partition, 512 clocks per 128 x 128 tile against 256 for its MMAs.
+//   MMA warp              S^T = K Q^T (128 x 256), both operands from shared
+//        memory, one 256-column TMEM buffer per key tile
+// A key tile's threads take its scores in two halves of 128 rows and give the
+// buffer back when the second is in registers, so that the next product runs
+// while those weights are summed, and beside the other key tile's.  (Items of
+// 128 rows with two buffers per key tile: 2.55 ms where this takes @@ ms; the
+// MMA warp's waits, three for each 256 x 128 weights, held it up.)  Each Q tile
+// serves both key tiles: 32 KB from L2 per 65,536 weights.
 // The items of an entry block may be shared by several CTAs (`parts`, when
 // there are few blocks); their sums are added by mass_join_kernel in one
 // fixed order.
 // ---------------------------------------------------------------------------
+constexpr int kQRows = 2 * kTcRows;
 constexpr int kQSt = 4;
 constexpr int kNlSt = 8;
 static_assert(kNlSt >= kQSt + 2, "slots of the rows' lse");
 constexpr int kMProducers = 3;
 constexpr int kMThreads = 256 + 32 * kMProducers + 32;
-constexpr int kMSteps = (32 + kMProducers - 1) / kMProducers;  // 4-row copy steps per warp and tile
+constexpr int kKSteps = (kTcKeys / 4 + kMProducers - 1) / kMProducers;  // 4-row copy steps, per warp
+constexpr int kQSteps = (kQRows / 4 + kMProducers - 1) / kMProducers;
 constexpr int kMBlock = 2 * kTcKeys;
-constexpr int kInFlight = 2;  // items whose copies are under way while the next is issued
+constexpr int kInFlight = 3;  // items whose copies are under way while the next is issued
 
 struct __align__(1024) MassTcSmem {
   uint8_t k[2][2][kTcTileBytes];  // [buffer][key tile]
-  uint8_t q[kQSt][kTcTileBytes];
+  uint8_t q[kQSt][2 * kTcTileBytes];
   // -lse in log2 units of an item's rows.  Item x's slot was item x - kNlSt's:
   // the Q stage of x is free once the MMAs of x - kQSt are done, which began
-  // when the weights of x - kQSt - 2 had been summed, so kQSt + 2 slots do.
-  float nl[kNlSt][kTcRows];
+  // when the scores of x - kQSt - 1 were in registers.
+  float nl[kNlSt][kQRows];
   uint64_t k_full[2], k_free[2], q_full[kQSt], q_free[kQSt];
-  uint64_t s_full[2][2], s_free[2][2];  // [key tile][buffer]
+  uint64_t s_full[2], s_free[2];  // per key tile
   uint32_t tmem_base;
   uint32_t gave_up;
 };
 
-// packed row x of a tile whose first row is token i0, head h0 of the group
+// tokens that v packed rows from a token's first row on reach over; exact for
+// v < 512 + grp
 struct RowSplit {
   int grp;
-  uint32_t inv;  // ceil(2^20 / grp): exact for h0 + x < 256, grp <= 128
+  uint32_t inv;  // ceil(2^20 / grp)
   __device__ __forceinline__ explicit RowSplit(int g)
       : grp(g), inv(((1u << 20) + g - 1) / g) {}
   __device__ __forceinline__ int token(int v) const {
-    return grp <= 128 ? (int)(((uint32_t)v * inv) >> 20) : (v >= grp);
+    return grp <= 128 ? (int)(((uint32_t)v * inv) >> 20) : (v >= grp) + (v >= 2 * grp);
   }
 };
 
@@ -285,8 +290,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   // row tiles from the first that sees an entry of this block on
   const int old = rq.n - rq.m;  // entries older than the chunk (negative: some rows see nothing)
-  const int n_tiles = (rows + kTcRows - 1) / kTcRows;
-  const int t0 = min(n_tiles, (int)((int64_t)max(0, j0 - old) * grp / kTcRows));
+  const int n_tiles = (rows + kQRows - 1) / kQRows;
+  const int t0 = min(n_tiles, (int)((int64_t)max(0, j0 - old) * grp / kQRows));
   const int per_head = n_tiles - t0;
   const int64_t items = (int64_t)per_head * a.Hkv;
   const int64_t it0 = items * part / parts;
@@ -297,10 +302,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&sm.k_full[s], kMProducers);
       ptx::mbar_init(&sm.k_free[s], 1);
-      for (int u = 0; u < 2; ++u) {
-        ptx::mbar_init(&sm.s_full[s][u], 1);
-        ptx::mbar_init(&sm.s_free[s][u], 4);
-      }
+      ptx::mbar_init(&sm.s_full[s], 1);
+      ptx::mbar_init(&sm.s_free[s], 4);
     }
     for (int s = 0; s < kQSt; ++s) {
       ptx::mbar_init(&sm.q_full[s], kMProducers);
@@ -320,11 +323,14 @@ __global__ void __launch_bounds__(kMThreads, 1)
   };
 
   if (warp >= 8 && warp < 8 + kMProducers) {
-    const int s0 = (warp - 8) * kMSteps;
-    const int row0 = 4 * s0 + (lane >> 3), ch = lane & 7;  // this lane's row of step 0
-    const uint32_t sw0 = (ch ^ (row0 & 7)) << 4, sw1 = (ch ^ ((row0 + 4) & 7)) << 4;
-    const uint32_t kd = ptx::smem_addr(sm.k[0][0]) + row0 * 128;
-    const uint32_t qd = ptx::smem_addr(sm.q[0]) + row0 * 128;
+    const int ch = lane & 7;
+    const int ks0 = (warp - 8) * kKSteps, krow = 4 * ks0 + (lane >> 3);  // this lane's row of step 0
+    const int qs0 = (warp - 8) * kQSteps, qrow = 4 * qs0 + (lane >> 3);
+    const uint32_t kd = ptx::smem_addr(sm.k[0][0]) + krow * 128;
+    const uint32_t qd = ptx::smem_addr(sm.q[0]) + qrow * 128;
+    auto swizzle = [&](int row) { return (uint32_t)((ch ^ (row & 7)) << 4); };
+    const uint32_t ksw0 = swizzle(krow), ksw1 = swizzle(krow + 4);
+    const uint32_t qsw0 = swizzle(qrow), qsw1 = swizzle(qrow + 4);
     const int64_t pitch = (int64_t)a.Hkv * kD * 2;
     const RowSplit sp(grp);
     // Each item is one group of copies; its barrier is arrived on once the
@@ -342,59 +348,100 @@ __global__ void __launch_bounds__(kMThreads, 1)
       for (int e = 0; e + 1 < kInFlight; ++e) pend[e] = pend[e + 1];
       pend[kInFlight - 1] = next;
     };
+    // a buffer's release: before this warp waits for one it tells the MMA
+    // warp of everything that has been copied, which it may be waiting for
+    auto acquire = [&](uint64_t *bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, ptx::mbar_test(bar, parity))) return;
+      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < kInFlight; ++e) {
+        if (pend[e] && lane == 0) ptx::mbar_arrive(pend[e]);
+        pend[e] = nullptr;
+      }
+      wait(bar, parity);
+    };
+    // lse of rows x = 4 qs0 + lane + 32 u of a tile, loaded an item ahead
+    constexpr int kLse = (4 * kQSteps + 31) / 32;
+    float lse_nx[kLse];
+    auto load_lse = [&](int g, int t) {
+      const int r0 = t * kQRows, i0 = r0 / grp, h0 = r0 - i0 * grp;
+#pragma unroll
+      for (int u = 0; u < kLse; ++u) {
+        const int x = 4 * qs0 + lane + 32 * u, v = h0 + x, i = sp.token(v);
+        lse_nx[u] = -INFINITY;
+        if (lane + 32 * u < 4 * kQSteps && x < kQRows && r0 + x < rows)
+          lse_nx[u] = __ldg(ma.lse + (int64_t)(rq.q0 + i0 + i) * a.Hq + g * grp + (v - i * grp));
+      }
+    };
+    // bytes from a tile's first token to this lane's row of each step: the
+    // same for every tile that starts at the same head of its group
+    int off[kQSteps], h_off = -1;
     int kn = 0, g = g0, t = tile0;
+    if (mine) load_lse(g, t);
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the head's K tiles
         const int kb = kn & 1;
-        if (kn >= 2) wait(&sm.k_free[kb], ((kn >> 1) - 1) & 1);
+        if (kn >= 2) acquire(&sm.k_free[kb], ((kn >> 1) - 1) & 1);
         const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int s = 0; s < kMSteps; ++s)
-            if (s0 + s < 32) {
-              const int j = j0 + i * kTcKeys + row0 + 4 * s;
+          for (int s = 0; s < kKSteps; ++s)
+            if (ks0 + s < kTcKeys / 4) {
+              const int j = j0 + i * kTcKeys + krow + 4 * s;
               const bool ok = j < rq.n;
-              const int64_t off = ok ? chunk_slot(a, rq, j) * pitch : 0;
-              cp_async16(kd + (kb * 2 + i) * kTcTileBytes + s * 512 + (s & 1 ? sw1 : sw0), kg + off, ok);
+              const int64_t at = ok ? chunk_slot(a, rq, j) * pitch : 0;
+              cp_async16(kd + (kb * 2 + i) * kTcTileBytes + s * 512 + (s & 1 ? ksw1 : ksw0), kg + at, ok);
             }
         landed(&sm.k_full[kb]);
         ++kn;
       }
       const int st = qn % kQSt;
-      if (qn >= kQSt) wait(&sm.q_free[st], ((qn / kQSt) - 1) & 1);
-      const int r0 = t * kTcRows, i0 = r0 / grp, h0 = r0 - i0 * grp;
+      if (qn >= kQSt) acquire(&sm.q_free[st], ((qn / kQSt) - 1) & 1);
+      const int r0 = t * kQRows, i0 = r0 / grp, h0 = r0 - i0 * grp;
+      if (h0 != h_off) {
+        h_off = h0;
+#pragma unroll
+        for (int s = 0; s < kQSteps; ++s) {
+          const int v = h0 + qrow + 4 * s, i = sp.token(v);
+          off[s] = (i * a.Hq + (v - i * grp)) * (kD * 2);
+        }
+      }
       const char *qg = (const char *)a.q + ((int64_t)(rq.q0 + i0) * a.Hq + g * grp) * (kD * 2) + ch * 16;
+      const uint32_t to = qd + st * 2 * kTcTileBytes;
+      if (r0 + kQRows <= rows) {
 #pragma unroll
-      for (int s = 0; s < kMSteps; ++s)
-        if (s0 + s < 32) {
-          const int x = row0 + 4 * s, v = h0 + x, i = sp.token(v);
-          const bool ok = r0 + x < rows;
-          const int64_t off = ok ? ((int64_t)i * a.Hq + (v - i * grp)) * (kD * 2) : 0;
-          cp_async16(qd + st * kTcTileBytes + s * 512 + (s & 1 ? sw1 : sw0), qg + off, ok);
-        }
+        for (int s = 0; s < kQSteps; ++s)
+          if (qs0 + s < kQRows / 4)
+            cp_async16(to + s * 512 + (s & 1 ? qsw1 : qsw0), qg + off[s], true);
+      } else {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // the lse of this warp's rows
-        const int x = 4 * s0 + lane + 32 * u;
-        if (lane + 32 * u < 4 * kMSteps && x < kTcRows) {
-          const int v = h0 + x, i = sp.token(v);
-          float l = -INFINITY;
-          if (r0 + x < rows)
-            l = __ldg(ma.lse + (int64_t)(rq.q0 + i0 + i) * a.Hq + g * grp + (v - i * grp));
-          sm.nl[qn % kNlSt][x] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        }
+        for (int s = 0; s < kQSteps; ++s)
+          if (qs0 + s < kQRows / 4) {
+            const bool ok = r0 + qrow + 4 * s < rows;
+            cp_async16(to + s * 512 + (s & 1 ? qsw1 : qsw0), qg + (ok ? off[s] : 0), ok);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kLse; ++u) {
+        const int x = 4 * qs0 + lane + 32 * u;
+        if (lane + 32 * u < 4 * kQSteps && x < kQRows)
+          sm.nl[qn % kNlSt][x] = lse_nx[u] == -INFINITY ? -INFINITY : -lse_nx[u] * kLog2e;
       }
       landed(&sm.q_full[st]);
       if (++t == n_tiles) {
         t = t0;
         ++g;
       }
+      if (qn + 1 < mine) load_lse(g, t);
     }
 #pragma unroll
     for (int e = 0; e < kInFlight; ++e) landed(nullptr);
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
   } else if (warp == 8 + kMProducers) {
-    constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
+    constexpr uint32_t id256 = ptx::idesc_bf16(128, 256, false), id128 = ptx::idesc_bf16(128, 128, false);
     constexpr uint64_t kTileStep = kTcTileBytes >> 4;
     const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0][0]));
     const uint64_t dq = ptx::sdesc_sw128(ptx::smem_addr(sm.q[0]));
@@ -405,19 +452,20 @@ __global__ void __launch_bounds__(kMThreads, 1)
         wait(&sm.k_full[kn & 1], (kn >> 1) & 1);
         ++kn;
       }
+      const uint32_t id = rows - t * kQRows > kTcRows ? id256 : id128;
       if (++t == n_tiles) t = t0;
-      const int st = qn % kQSt, buf = qn & 1;
+      const int st = qn % kQSt;
       wait(&sm.q_full[st], (qn / kQSt) & 1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (qn >= 2) wait(&sm.s_free[i][buf], ((qn >> 1) - 1) & 1);
+        if (qn >= 1) wait(&sm.s_free[i], (qn - 1) & 1);
         ptx::tc_fence_after();
         if (lane == 0) {
-          const uint64_t ak = dk + (((kn - 1) & 1) * 2 + i) * kTileStep, bq = dq + st * kTileStep;
+          const uint64_t ak = dk + (((kn - 1) & 1) * 2 + i) * kTileStep, bq = dq + st * 2 * kTileStep;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_ss(tmem + (i * 2 + buf) * 128, ak + 2 * kk, bq + 2 * kk, idS, kk > 0);
-          ptx::mma_commit(&sm.s_full[i][buf]);
+            ptx::mma_f16_ss(tmem + i * 256, ak + 2 * kk, bq + 2 * kk, id, kk > 0);
+          ptx::mma_commit(&sm.s_full[i]);
           if (i == 1) ptx::mma_commit(&sm.q_free[st]);
         }
         __syncwarp();
@@ -426,7 +474,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
   } else {
     const int i = warp >> 2;
     const int key = j0 + i * kTcKeys + (threadIdx.x & 127);
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + i * 256;
     // packed rows [r_min, rows) see this key (none past the list's end)
     const int64_t r_min = key < rq.n ? (int64_t)max(0, key - old) * grp : INT32_MAX;
     // the last key of this tile that is listed sees the fewest rows
@@ -438,46 +486,51 @@ __global__ void __launch_bounds__(kMThreads, 1)
     for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
     int t = tile0;
     for (int qn = 0; qn < mine; ++qn) {
-      const int buf = qn & 1, r0 = t * kTcRows;
+      const int r_tile = t * kQRows, halves = rows - r_tile > kTcRows ? 2 : 1;
       if (++t == n_tiles) t = t0;
-      wait(&sm.s_full[i][buf], (qn >> 1) & 1);
+      wait(&sm.s_full[i], qn & 1);
       ptx::tc_fence_after();
-      const uint32_t ts = tmem + lane_base + (i * 2 + buf) * 128;
-      uint32_t sr[128];
+#pragma unroll 1
+      for (int hf = 0; hf < halves; ++hf) {
+        const int r0 = r_tile + hf * kTcRows;
+        const float *nl = sm.nl[qn % kNlSt] + hf * kTcRows;
+        uint32_t sr[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + 32 * c, sr + 32 * c);
-      ptx::tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + hf * kTcRows + 32 * c, sr + 32 * c);
+        ptx::tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
-      const float4 *nl4 = reinterpret_cast<const float4 *>(sm.nl[qn % kNlSt]);
-      if (r0 >= all_see && r0 + kTcRows <= rows) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float4 nl = nl4[c];
-          const float2 x0 = __ffma2_rn(
-              make_float2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), scale2,
-              make_float2(nl.x, nl.y));
-          const float2 x1 = __ffma2_rn(
-              make_float2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])), scale2,
-              make_float2(nl.z, nl.w));
-          sum[(2 * c) & 3] = __fadd2_rn(sum[(2 * c) & 3], make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y)));
-          sum[(2 * c + 1) & 3] =
-              __fadd2_rn(sum[(2 * c + 1) & 3], make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y)));
+        for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+        if (hf + 1 == halves) {  // all scores of the item are in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.s_free[i]);
         }
-      } else {
-        // rows [lo, hi) of the tile see this key
-        const int lo = (int)min((int64_t)kTcRows, max((int64_t)0, r_min - r0));
-        const int hi = min(kTcRows, rows - r0);
-        const float *nl = sm.nl[qn % kNlSt];
+        if (r0 >= all_see && r0 + kTcRows <= rows) {
+          const float4 *nl4 = reinterpret_cast<const float4 *>(nl);
 #pragma unroll
-        for (int c = 0; c < 128; ++c) {
-          const float p = ptx::ex2(fmaf(__uint_as_float(sr[c]), kScale, nl[c]));
-          if (c >= lo && c < hi) sum[c & 3].x += p;
+          for (int c = 0; c < 32; ++c) {
+            const float4 v = nl4[c];
+            const float2 x0 = __ffma2_rn(
+                make_float2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), scale2,
+                make_float2(v.x, v.y));
+            const float2 x1 = __ffma2_rn(
+                make_float2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])), scale2,
+                make_float2(v.z, v.w));
+            sum[(2 * c) & 3] = __fadd2_rn(sum[(2 * c) & 3], make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y)));
+            sum[(2 * c + 1) & 3] =
+                __fadd2_rn(sum[(2 * c + 1) & 3], make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y)));
+          }
+        } else {
+          // rows [lo, hi) of this half see the key
+          const int lo = (int)min((int64_t)kTcRows, max((int64_t)0, r_min - r0));
+          const int hi = min(kTcRows, rows - r0);
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const float p = ptx::ex2(fmaf(__uint_as_float(sr[c]), kScale, nl[c]));
+            if (c >= lo && c < hi) sum[c & 3].x += p;
+          }
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sm.s_free[i][buf]);
     }
     const float2 s2 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
     if (key < rq.n) {
@@ -531,9 +584,9 @@ MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
     return p;
   }
   p.kind = 3;
-  // about four waves of CTAs, none with less than four row tiles
+  // about four waves of CTAs, none with less than four items
   const int64_t blocks = (int64_t)B * ((max_kv + kMBlock - 1) / kMBlock);
-  const int64_t items = (rows + kTcRows - 1) / kTcRows * Hkv;
+  const int64_t items = (rows + kQRows - 1) / kQRows * Hkv;
   p.parts = (int)std::max<int64_t>(
       1, std::min<int64_t>(std::min<int64_t>((4LL * sms + blocks - 1) / std::max<int64_t>(1, blocks), 64),
                            items / 4));
