@@ -223,17 +223,15 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // ---------------------------------------------------------------------------
 // bf16, more rows: tcgen05, the scores transposed.  CTA = 256 list entries
 // (two tiles of 128 keys) x a share of the (KV head, 256-row tile) items:
-//   warps 4 i .. 4 i + 3  key tile i: thread = key = TMEM lane, so that the sum
-//        over rows stays in the thread's registers, with no reduction
+//   warps 4 i .. 4 i + 3  every other 128-row half of the items: thread = TMEM
+//        lane = one key of each key tile, so that the sums over rows stay in
+//        the thread's registers, and one load of a row's lse serves two weights
 //   3 producer warps      K tiles (once per head), Q tiles and the rows' lse
 //        through a ring, by cp.async into the 128-byte-swizzled layout
-//   MMA warp              S^T = K Q^T (128 x 256), both operands from shared
-//        memory, one 256-column TMEM buffer per key tile
-// A key tile's threads take its scores in two halves of 128 rows and give the
-// buffer back when the second is in registers, so that the next product runs
-// while those weights are summed, and beside the other key tile's.  (Items of
-// 128 rows with two buffers per key tile: 2.55 ms where this takes @@ ms; the
-// MMA warp's waits, three for each 256 x 128 weights, held it up.)  Each Q tile
+//   MMA warp              S^T = K Q^T, both operands from shared memory, two
+//        128 x 128 tiles per half, into the TMEM buffer of its warps
+// Scores are taken 16 rows at a time, the next 16 being loaded while a step's
+// weights are summed; the buffer is given back with the last load.  Each Q tile
 // serves both key tiles: 32 KB from L2 per 65,536 weights.
 // The items of an entry block may be shared by several CTAs (`parts`, when
 // there are few blocks); their sums are added by mass_join_kernel in one
@@ -248,17 +246,19 @@ constexpr int kMThreads = 256 + 32 * kMProducers + 32;
 constexpr int kKSteps = (kTcKeys / 4 + kMProducers - 1) / kMProducers;  // 4-row copy steps, per warp
 constexpr int kQSteps = (kQRows / 4 + kMProducers - 1) / kMProducers;
 constexpr int kMBlock = 2 * kTcKeys;
+constexpr int kMaxParts = 64;
 constexpr int kInFlight = 3;  // items whose copies are under way while the next is issued
 
 struct __align__(1024) MassTcSmem {
   uint8_t k[2][2][kTcTileBytes];  // [buffer][key tile]
   uint8_t q[kQSt][2 * kTcTileBytes];
   // -lse in log2 units of an item's rows.  Item x's slot was item x - kNlSt's:
-  // the Q stage of x is free once the MMAs of x - kQSt are done, which began
-  // when the scores of x - kQSt - 1 were in registers.
+  // the Q stage of x is free once the MMAs of x - kQSt are done, the last of
+  // which began when the scores two halves earlier were in registers.
   float nl[kNlSt][kQRows];
   uint64_t k_full[2], k_free[2], q_full[kQSt], q_free[kQSt];
-  uint64_t s_full[2], s_free[2];  // per key tile
+  uint64_t s_full[2], s_free[2];  // per score buffer
+  float join[kMBlock];            // sums of the odd halves
   uint32_t tmem_base;
   uint32_t gave_up;
 };
@@ -441,106 +441,145 @@ __global__ void __launch_bounds__(kMThreads, 1)
     for (int e = 0; e < kInFlight; ++e) landed(nullptr);
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
   } else if (warp == 8 + kMProducers) {
-    constexpr uint32_t id256 = ptx::idesc_bf16(128, 256, false), id128 = ptx::idesc_bf16(128, 128, false);
+    constexpr uint32_t id = ptx::idesc_bf16(128, 128, false);
     constexpr uint64_t kTileStep = kTcTileBytes >> 4;
     const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0][0]));
     const uint64_t dq = ptx::sdesc_sw128(ptx::smem_addr(sm.q[0]));
-    int kn = 0, t = tile0;
+    int kn = 0, t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the next head
         if (kn > 0 && lane == 0) ptx::mma_commit(&sm.k_free[(kn - 1) & 1]);
         wait(&sm.k_full[kn & 1], (kn >> 1) & 1);
         ++kn;
       }
-      const uint32_t id = rows - t * kQRows > kTcRows ? id256 : id128;
+      const int halves = rows - t * kQRows > kTcRows ? 2 : 1;
       if (++t == n_tiles) t = t0;
       const int st = qn % kQSt;
       wait(&sm.q_full[st], (qn / kQSt) & 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (qn >= 1) wait(&sm.s_free[i], (qn - 1) & 1);
+      for (int hf = 0; hf < halves; ++hf, ++hseq) {
+        const int buf = hseq & 1;
+        if (hseq >= 2) wait(&sm.s_free[buf], ((hseq >> 1) - 1) & 1);
         ptx::tc_fence_after();
         if (lane == 0) {
-          const uint64_t ak = dk + (((kn - 1) & 1) * 2 + i) * kTileStep, bq = dq + st * 2 * kTileStep;
+          const uint64_t ak = dk + ((kn - 1) & 1) * 2 * kTileStep, bq = dq + (st * 2 + hf) * kTileStep;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            ptx::mma_f16_ss(tmem + i * 256, ak + 2 * kk, bq + 2 * kk, id, kk > 0);
-          ptx::mma_commit(&sm.s_full[i]);
-          if (i == 1) ptx::mma_commit(&sm.q_free[st]);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_f16_ss(tmem + buf * 256 + i * 128, ak + i * kTileStep + 2 * kk, bq + 2 * kk, id,
+                              kk > 0);
+          ptx::mma_commit(&sm.s_full[buf]);
+          if (hf + 1 == halves) ptx::mma_commit(&sm.q_free[st]);
         }
         __syncwarp();
       }
     }
   } else {
-    const int i = warp >> 2;
-    const int key = j0 + i * kTcKeys + (threadIdx.x & 127);
-    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + i * 256;
-    // packed rows [r_min, rows) see this key (none past the list's end)
-    const int64_t r_min = key < rq.n ? (int64_t)max(0, key - old) * grp : INT32_MAX;
-    // the last key of this tile that is listed sees the fewest rows
-    const int last = min(rq.n, j0 + (i + 1) * kTcKeys) - 1;
-    const int64_t all_see = (int64_t)max(0, last - old) * grp;
+    const int buf = warp >> 2;
+    const int key0 = j0 + (threadIdx.x & 127);  // and key0 + 128
+    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * 256;
+    // packed rows [r_min, rows) see a key (none past the list's end)
+    const int64_t r_min0 = key0 < rq.n ? (int64_t)max(0, key0 - old) * grp : INT32_MAX;
+    const int64_t r_min1 = key0 + 128 < rq.n ? (int64_t)max(0, key0 + 128 - old) * grp : INT32_MAX;
+    // the last listed key of the block sees the fewest rows
+    const int64_t all_see = (int64_t)max(0, min(rq.n, j0 + kMBlock) - 1 - old) * grp;
     const float2 scale2 = make_float2(kScale, kScale);
-    float2 sum[4];
+    float2 sum[2][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = make_float2(0.f, 0.f);
-    int t = tile0;
+    for (int e = 0; e < 2; ++e) sum[e][0] = sum[e][1] = make_float2(0.f, 0.f);
+    constexpr int kStep = 16;
+    int t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
       const int r_tile = t * kQRows, halves = rows - r_tile > kTcRows ? 2 : 1;
       if (++t == n_tiles) t = t0;
-      wait(&sm.s_full[i], qn & 1);
+      const int hf = (hseq & 1) == buf ? 0 : 1;  // the half of this item in this buffer
+      const int seq = hseq + hf;
+      hseq += halves;
+      if (hf >= halves) continue;
+      const int r0 = r_tile + hf * kTcRows;
+      const float4 *nl4 = reinterpret_cast<const float4 *>(sm.nl[qn % kNlSt] + hf * kTcRows);
+      wait(&sm.s_full[buf], (seq >> 1) & 1);
       ptx::tc_fence_after();
-#pragma unroll 1
-      for (int hf = 0; hf < halves; ++hf) {
-        const int r0 = r_tile + hf * kTcRows;
-        const float *nl = sm.nl[qn % kNlSt] + hf * kTcRows;
-        uint32_t sr[128];
+      auto give_back = [&] {  // all scores of the half are in registers
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.s_free[buf]);
+      };
+      if (r0 >= all_see && r0 + kTcRows <= rows) {
+        uint32_t sr[2][2][kStep];  // [step parity][key]
+        ptx::tmem_ld16(ts, sr[0][0]);
+        ptx::tmem_ld16(ts + 128, sr[0][1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + hf * kTcRows + 32 * c, sr + 32 * c);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
-        if (hf + 1 == halves) {  // all scores of the item are in registers
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sm.s_free[i]);
-        }
-        if (r0 >= all_see && r0 + kTcRows <= rows) {
-          const float4 *nl4 = reinterpret_cast<const float4 *>(nl);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float4 v = nl4[c];
-            const float2 x0 = __ffma2_rn(
-                make_float2(__uint_as_float(sr[4 * c]), __uint_as_float(sr[4 * c + 1])), scale2,
-                make_float2(v.x, v.y));
-            const float2 x1 = __ffma2_rn(
-                make_float2(__uint_as_float(sr[4 * c + 2]), __uint_as_float(sr[4 * c + 3])), scale2,
-                make_float2(v.z, v.w));
-            sum[(2 * c) & 3] = __fadd2_rn(sum[(2 * c) & 3], make_float2(ptx::ex2(x0.x), ptx::ex2(x0.y)));
-            sum[(2 * c + 1) & 3] =
-                __fadd2_rn(sum[(2 * c + 1) & 3], make_float2(ptx::ex2(x1.x), ptx::ex2(x1.y)));
+        for (int c = 0; c < kTcRows / kStep; ++c) {
+          uint32_t(&s)[2][kStep] = sr[c & 1];
+          ptx::tmem_wait_ld();
+          ptx::reg_fence16(s[0]);
+          ptx::reg_fence16(s[1]);
+          if (c + 1 < kTcRows / kStep) {
+            ptx::tmem_ld16(ts + (c + 1) * kStep, sr[(c + 1) & 1][0]);
+            ptx::tmem_ld16(ts + 128 + (c + 1) * kStep, sr[(c + 1) & 1][1]);
+          } else {
+            give_back();
           }
-        } else {
-          // rows [lo, hi) of this half see the key
-          const int lo = (int)min((int64_t)kTcRows, max((int64_t)0, r_min - r0));
-          const int hi = min(kTcRows, rows - r0);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const float p = ptx::ex2(fmaf(__uint_as_float(sr[c]), kScale, nl[c]));
-            if (c >= lo && c < hi) sum[c & 3].x += p;
+          for (int q = 0; q < kStep / 4; ++q) {
+            const float4 v = nl4[c * (kStep / 4) + q];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int x = 4 * q + 2 * w;
+                const float2 y = __ffma2_rn(
+                    make_float2(__uint_as_float(s[e][x]), __uint_as_float(s[e][x + 1])), scale2,
+                    w ? make_float2(v.z, v.w) : make_float2(v.x, v.y));
+                sum[e][w] = __fadd2_rn(sum[e][w], make_float2(ptx::ex2(y.x), ptx::ex2(y.y)));
+              }
+          }
+        }
+      } else {
+        // rows [lo, hi) of the half see each key; a few halves per head
+        const int lo0 = (int)min((int64_t)kTcRows, max((int64_t)0, r_min0 - r0));
+        const int lo1 = (int)min((int64_t)kTcRows, max((int64_t)0, r_min1 - r0));
+        const int hi = min(kTcRows, rows - r0);
+        const float *nl = reinterpret_cast<const float *>(nl4);
+#pragma unroll 1
+        for (int c = 0; c < kTcRows; c += kStep) {
+          uint32_t s[2][kStep];
+          ptx::tmem_ld16(ts + c, s[0]);
+          ptx::tmem_ld16(ts + 128 + c, s[1]);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence16(s[0]);
+          ptx::reg_fence16(s[1]);
+          if (c + kStep == kTcRows) give_back();
+#pragma unroll
+          for (int x = 0; x < kStep; ++x) {
+            const float p0 = ptx::ex2(fmaf(__uint_as_float(s[0][x]), kScale, nl[c + x]));
+            const float p1 = ptx::ex2(fmaf(__uint_as_float(s[1][x]), kScale, nl[c + x]));
+            if (c + x >= lo0 && c + x < hi) sum[0][0].x += p0;
+            if (c + x >= lo1 && c + x < hi) sum[1][0].x += p1;
           }
         }
       }
     }
-    const float2 s2 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-    if (key < rq.n) {
-      float x = s2.x + s2.y;
-      if (parts > 1) {
-        partial[((int64_t)part * a.B + b) * a.max_kv + key] = x;
-      } else {
-        const int64_t at = (int64_t)b * ma.stride + key;
-        if (ma.in && key < old) x = fmaf(ma.decay, ma.in[at], x);
-        ma.out[at] = x;
+    const float2 a0 = __fadd2_rn(sum[0][0], sum[0][1]), a1 = __fadd2_rn(sum[1][0], sum[1][1]);
+    if (buf == 1) {
+      sm.join[threadIdx.x & 127] = a0.x + a0.y;
+      sm.join[(threadIdx.x & 127) + 128] = a1.x + a1.y;
+    }
+    ptx::named_bar_sync(1, 256);
+    if (buf == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = key0 + 128 * e;
+        float x = (e ? a1.x + a1.y : a0.x + a0.y) + sm.join[key - j0];
+        if (key >= rq.n) continue;
+        if (parts > 1) {
+          partial[((int64_t)part * a.B + b) * a.max_kv + key] = x;
+        } else {
+          const int64_t at = (int64_t)b * ma.stride + key;
+          if (ma.in && key < old) x = fmaf(ma.decay, ma.in[at], x);
+          ma.out[at] = x;
+        }
       }
     }
   }
@@ -584,12 +623,19 @@ MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
     return p;
   }
   p.kind = 3;
-  // about four waves of CTAs, none with less than four items
-  const int64_t blocks = (int64_t)B * ((max_kv + kMBlock - 1) / kMBlock);
+  // about four waves of CTAs, the last of them as full as twice the parts can
+  // make it; none with less than four items
+  const int64_t blocks = std::max<int64_t>(1, (int64_t)B * ((max_kv + kMBlock - 1) / kMBlock));
   const int64_t items = (rows + kQRows - 1) / kQRows * Hkv;
-  p.parts = (int)std::max<int64_t>(
-      1, std::min<int64_t>(std::min<int64_t>((4LL * sms + blocks - 1) / std::max<int64_t>(1, blocks), 64),
-                           items / 4));
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, items / 4));
+  const int64_t first = std::min<int64_t>(most, (4LL * sms + blocks - 1) / blocks);
+  const auto idle = [&](int64_t n) {  // share of the launch's waves left empty
+    const int64_t ctas = blocks * n, waves = (ctas + sms - 1) / sms;
+    return (double)(waves * sms - ctas) / (double)(waves * sms);
+  };
+  p.parts = (int)first;
+  for (int64_t n = first + 1; n <= std::min<int64_t>(most, 2 * first); ++n)
+    if (idle(n) < idle(p.parts) - 0.02) p.parts = (int)n;
   return p;
 }
 
