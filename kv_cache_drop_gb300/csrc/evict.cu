@@ -5,12 +5,17 @@
 // n_first and last n_recent entries rank above all others.
 //
 // A cluster of CTAs takes one request.  The k-th largest key is found by a
-// radix select over the 32-bit order-preserving image of the mass, 8 bits a
-// round, the CTAs' histograms summed through distributed shared memory; then
-// every warp counts its own contiguous part of the list, the counts are
-// scanned over warps and CTAs, and the warp streams its part again, writing
-// kept and dropped entries in list order by ballot prefix.  No atomics on
-// global memory: the result does not depend on timing.
+// radix select over the 32-bit order-preserving image of the mass, in digits
+// of 11, 11 and 10 bits (the first holds two mantissa bits, so that masses of
+// one magnitude still spread over several counters), the CTAs' histograms
+// summed through distributed shared memory; then every warp counts its own
+// contiguous part of the list, the counts are scanned over warps and CTAs, and
+// the warp goes over its part again, writing kept and dropped entries in list
+// order by ballot prefix.  No atomics on global memory: the result does not
+// depend on timing.  Lists of up to 16,384 entries per CTA stay in registers
+// between the passes; longer ones are read again, from L2, eight loads in
+// flight per thread.  Bound by the latency of the passes and cluster barriers
+// (short lists) and by the L2 bandwidth of the cluster's SMs (long ones).
 #include "common.cuh"
 
 #include <cooperative_groups.h>
@@ -20,9 +25,12 @@ namespace cg = cooperative_groups;
 namespace akv {
 namespace {
 
-constexpr int kEvThreads = 512;
+constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kHold = 16;   // keys per thread that stay in registers
+constexpr int kBatch = 8;   // loads in flight per thread otherwise
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 16;  // above 8 is not portable: asked for only where it fits
 
 struct EvictArgs {
   int B, max_kv;
@@ -49,20 +57,62 @@ __device__ __forceinline__ int req_len(const EvictArgs &a, int b) {
   return min(max(a.indptr[b + 1] - a.indptr[b], 0), a.max_kv);
 }
 
+// kInRegs: a thread's keys (entries j0 + 32 e + lane of its warp's part) are
+// held in registers.
+template <bool kInRegs>
 __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   cg::cluster_group cl = cg::this_cluster();
-  __shared__ int hist[256];
+  __shared__ __align__(16) int hist[2][kBins];  // alternate digits, so that one barrier per digit does
   __shared__ int warp_n[2][kEvWarps];  // per warp: entries above / equal to the threshold
   __shared__ int cta_n[2];
   __shared__ int pick[2];              // chosen digit, entries still wanted in it
+  __shared__ int scan[kEvWarps];
   __shared__ long long base_s[2];
   __shared__ long long red[2][kEvWarps];
-  const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int size = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int b = blockIdx.x / size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = req_len(a, b);
   const int kk = min(max(a.keep[b], 0), n);
   const float *mass = a.mass + (int64_t)b * a.stride;
   const int32_t beg = a.indptr[b];
+
+  // this warp's part of the list
+  const int per_warp = ((n + size * kEvWarps - 1) / (size * kEvWarps) + 31) / 32 * 32;
+  const int j0 = (int)min((int64_t)n, (int64_t)(rank * kEvWarps + warp) * per_warp);
+  const int j1 = min(n, j0 + per_warp);
+  auto key_of = [&](int j, float m) -> uint32_t {
+    return mass_key(j < a.n_first || j >= n - a.n_recent ? INFINITY : m);
+  };
+  uint32_t held[kInRegs ? kHold : 1];
+  if (kInRegs) {
+#pragma unroll
+    for (int e = 0; e < kHold; ++e) {
+      const int j = j0 + 32 * e + lane;
+      held[e] = j < j1 ? __float_as_uint(__ldg(mass + j)) : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < kHold; ++e) held[e] = key_of(j0 + 32 * e + lane, __uint_as_float(held[e]));
+  }
+  // f(j, key) for every entry of this lane
+  auto each = [&](auto f) {
+    if constexpr (kInRegs) {
+#pragma unroll
+      for (int e = 0; e < kHold; ++e) {
+        const int j = j0 + 32 * e + lane;
+        if (j < j1) f(j, held[e]);
+      }
+    } else {
+      for (int j = j0 + lane; j < j1; j += 32 * kBatch) {
+        float m[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) m[e] = j + 32 * e < j1 ? __ldg(mass + j + 32 * e) : 0.f;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+          if (j + 32 * e < j1) f(j + 32 * e, key_of(j + 32 * e, m[e]));
+      }
+    }
+  };
 
   // where this request's kept and dropped entries start
   long long kept_before = 0, drop_before = 0;
@@ -80,6 +130,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     red[0][warp] = kept_before;
     red[1][warp] = drop_before;
   }
+  for (int i = threadIdx.x; i < 2 * kBins; i += kEvThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
   if (threadIdx.x < 2) {
     long long s = 0;
@@ -91,67 +142,74 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
       ptr[b + 1] = (int32_t)(s + (threadIdx.x ? n - kk : kk));
     }
   }
-  __syncthreads();
 
-  // this CTA's and warp's parts of the list
-  const int per_warp = (n + kCluster * kEvWarps - 1) / (kCluster * kEvWarps);
-  const int j0 = min(n, (rank * kEvWarps + warp) * per_warp), j1 = min(n, j0 + per_warp);
-  auto key_at = [&](int j) -> uint32_t {
-    return j < a.n_first || j >= n - a.n_recent ? mass_key(INFINITY) : mass_key(mass[j]);
-  };
-
-  // the kk-th largest key
+  // the kk-th largest key, a digit at a time; every CTA comes to it by itself
   uint32_t prefix = 0;
   int want = kk;
-  for (int shift = 24; kk > 0 && shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kEvThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = j0 + lane; j < j1; j += 32) {
-      const uint32_t k = key_at(j);
-      if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-    }
+  const bool some = kk > 0 && kk < n;  // else all or none are kept
+  for (int d = 0; some && d < 3; ++d) {
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+    const uint32_t digit = d == 2 ? 0x3ffu : 0x7ffu;
+    const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffffc00u;
+    int *h = hist[d & 1];
+    each([&](int, uint32_t k) {
+      if ((k & above) == prefix) atomicAdd(&h[(k >> shift) & digit], 1);
+    });
     cl.sync();
-    if (warp == 0) {  // lane l: bins 255 - 8 l .. 248 - 8 l, highest first
-      int c[8], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = 0;
-        for (int o = 0; o < kCluster; ++o) c[e] += cl.map_shared_rank(hist, o)[255 - 8 * lane - e];
-        sum += c[e];
+    // thread t < 512: bins 4 u .. 4 u + 3 with u = 511 - t, highest first
+    int c[4] = {}, sum = 0;
+    if (threadIdx.x < kBins / 4) {
+      const int u = kBins / 4 - 1 - threadIdx.x;
+#pragma unroll 4
+      for (int o = 0; o < size; ++o) {
+        const int4 v = reinterpret_cast<const int4 *>(cl.map_shared_rank(h, o))[u];
+        c[0] += v.w;
+        c[1] += v.z;
+        c[2] += v.y;
+        c[3] += v.x;
       }
-      int incl = sum;
+      sum = (c[0] + c[1]) + (c[2] + c[3]);
+    }
+    int incl = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      int left = want - (incl - sum);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    if (threadIdx.x < kBins / 4) {
+      int before = incl - sum;
+      for (int w = 0; w < warp; ++w) before += scan[w];
+      int left = want - before;
       if (left > 0 && left <= sum) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
           if (left > 0 && left <= c[e]) {
-            pick[0] = 255 - 8 * lane - e;
+            pick[0] = kBins - 1 - 4 * (int)threadIdx.x - e;
             pick[1] = left;
           }
           left -= c[e];
         }
       }
     }
-    cl.sync();  // every CTA has read the histograms (and this one its pick)
+    __syncthreads();
     prefix |= (uint32_t)pick[0] << shift;
     want = pick[1];
-    __syncthreads();
+    // the other histogram's readers passed this digit's cluster barrier
+    if (d == 1)
+      for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[0][i] = 0;
+    if (d == 1) __syncthreads();
   }
   // kept: keys above `prefix`, and the first `want` equal ones
   int above_n = 0, equal_n = 0;
-  if (kk > 0) {
-    for (int j = j0 + lane; j < j1; j += 32) {
-      const uint32_t k = key_at(j);
+  if (some)
+    each([&](int, uint32_t k) {
       above_n += k > prefix;
       equal_n += k == prefix;
-    }
-  }
+    });
+  else if (kk > 0)
+    above_n = j1 > j0 + lane ? (j1 - j0 - lane + 31) / 32 : 0;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     above_n += __shfl_xor_sync(0xffffffffu, above_n, o);
@@ -182,33 +240,74 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   int equal = equal_before;
   const int64_t kept_base = base_s[0], drop_base = base_s[1];
   const uint32_t below = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    const int e = j + lane;
+  // 32 entries: e = this lane's, its mass, slot and position at hand
+  auto place = [&](int e, uint32_t k, float m, int32_t slot, int32_t pos) {
     const bool there = e < j1;
-    const uint32_t k = there && kk > 0 ? key_at(e) : 0u;
-    const bool eq = there && kk > 0 && k == prefix;
+    const bool eq = some && there && k == prefix;
     const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
     const bool keep = there && kk > 0 &&
-                      (k > prefix || (eq && equal + __popc(eqs & below) < want));
+                      (!some || k > prefix || (eq && equal + __popc(eqs & below) < want));
     const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
-    if (there) {
-      const int32_t slot = a.indices[(int64_t)beg + e];
-      const int kb = kept + __popc(keeps & below);
-      if (keep) {
-        const int64_t to = kept_base + kb;
-        if (to < a.out_cap) {
-          a.out_indices[to] = slot;
-          if (a.out_pos) a.out_pos[to] = a.pos[(int64_t)beg + e];
-        }
-        if (kb < a.out_stride) a.out_mass[(int64_t)b * a.out_stride + kb] = mass[e];
-      } else if (drop_base + (e - kb) < a.dropped_cap) {
-        a.dropped[drop_base + (e - kb)] = slot;
+    const int kb = kept + __popc(keeps & below);
+    if (keep) {
+      const int64_t to = kept_base + kb;
+      if (to < a.out_cap) {
+        a.out_indices[to] = slot;
+        if (a.out_pos) a.out_pos[to] = pos;
       }
+      if (kb < a.out_stride) a.out_mass[(int64_t)b * a.out_stride + kb] = m;
+    } else if (there && drop_base + (e - kb) < a.dropped_cap) {
+      a.dropped[drop_base + (e - kb)] = slot;
     }
     kept += __popc(keeps);
     equal += __popc(eqs);
+  };
+  const int32_t *idx = a.indices + (int64_t)beg, *pos = a.pos ? a.pos + (int64_t)beg : nullptr;
+  for (int j = j0; j < j1; j += 32 * kBatch) {
+    float m[kBatch];
+    int32_t s[kBatch], p[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int at = j + 32 * e + lane;
+      const bool there = at < j1;
+      m[e] = there ? __ldg(mass + at) : 0.f;
+      s[e] = there ? __ldg(idx + at) : 0;
+      p[e] = there && pos ? __ldg(pos + at) : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (j + 32 * e < j1) place(j + 32 * e + lane, key_of(j + 32 * e + lane, m[e]), m[e], s[e], p[e]);
   }
   cl.sync();  // a CTA's counts stay readable until every CTA has them
+}
+
+// CTAs per request: enough for the lists to stay in registers, up to 8, or 16
+// where the device takes such clusters and the requests leave SMs idle.
+bool takes_16() {
+  static int known[64];  // 0 not asked, 1 no, 2 yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(kEvThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool ok = cudaFuncSetAttribute(evict_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                         1) == cudaSuccess &&
+                    cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                         1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&clusters, evict_kernel<false>, &cfg) == cudaSuccess &&
+                    clusters > 0;
+    if (!ok) (void)cudaGetLastError();
+    known[dev] = ok ? 2 : 1;
+  }
+  return known[dev] == 2;
 }
 
 }  // namespace
@@ -222,17 +321,21 @@ cudaError_t launch_evict(int B, const int32_t *indptr, const int32_t *indices, c
   EvictArgs a{B, max_kv, indptr, indices, pos, mass, stride, keep, n_first, n_recent, out_indptr,
               out_indices, out_pos, out_mass, out_stride, out_cap, dropped_cap, dropped_indptr,
               dropped};
+  constexpr int kPerCta = kHold * kEvThreads;
+  int size = 1;
+  while (size < 8 && (int64_t)size * kPerCta < max_kv) size *= 2;
+  if (size == 8 && max_kv > 8 * kPerCta && B <= 8 && takes_16()) size = kMaxCluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)B * kCluster);
+  cfg.gridDim = dim3((unsigned)(B * size));
   cfg.blockDim = dim3(kEvThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = (unsigned)size;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+  return cudaLaunchKernelEx(&cfg, max_kv <= size * kPerCta ? evict_kernel<true> : evict_kernel<false>, a);
 }
 
 }  // namespace akv
