@@ -572,32 +572,36 @@ def akv_append_kv(shp: Shape, n: int, k_new, v_new, pos, slot, k_pool, v_pool, s
 
 
 def _typed(name: str, t, dtype, device, shape=None, rows: bool = False):
-    """Address of a tensor argument of the chunk calls: on `device`, of
-    `dtype`, contiguous (rows: only its inner dimensions), and of the given
-    shape (None: any extent).  None stays None."""
+    """Address of a tensor argument of the chunk calls: on CUDA device
+    `device` (its index), of `dtype`, of the given shape (None: any extent)
+    and contiguous (rows: only its inner dimensions).  None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, need {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(n is not None and n != m for n, m in zip(shape, t.shape))):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{device}")
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need {shape}")
-    if not (t.is_contiguous() or (rows and t.numel() and t[0].is_contiguous())):
+    if not t.is_contiguous() and not (rows and t[0].is_contiguous()):
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _run_on(stream):
-    """(device, raw stream) that a call without tensors' own choice uses: the
-    given stream, or the current one; its device must be the current one."""
+    """(device index, raw stream) of a call: the given stream, or the current
+    one; the library launches on the current device, so the stream's must be
+    that one."""
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    if s.device_index != torch.cuda.current_device():
-        raise ValueError(f"the stream is on cuda:{s.device_index}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return s.device, s.cuda_stream
+    if stream is None:
+        s = torch.cuda.current_stream()
+    else:
+        s = stream
+        if s.device_index != torch.cuda.current_device():
+            raise ValueError(f"the stream is on cuda:{s.device_index}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return s.device_index, s.cuda_stream
 
 
 def _torch_dtype(shp: Shape):

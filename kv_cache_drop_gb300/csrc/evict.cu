@@ -30,6 +30,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kHold = 16;   // keys per thread that stay in registers
 constexpr int kBatch = 8;   // loads in flight per thread otherwise
 constexpr int kBins = 2048;
+static_assert(kEvWarps == 32, "scans over the warps take one lane each");
 constexpr int kMaxCluster = 16;  // above 8 is not portable: asked for only where it fits
 
 struct EvictArgs {
@@ -81,9 +82,12 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   const int per_warp = ((n + size * kEvWarps - 1) / (size * kEvWarps) + 31) / 32 * 32;
   const int j0 = (int)min((int64_t)n, (int64_t)(rank * kEvWarps + warp) * per_warp);
   const int j1 = min(n, j0 + per_warp);
+  const int fixed_end = min(a.n_first, n), fixed_from = n - min(a.n_recent, n);
   auto key_of = [&](int j, float m) -> uint32_t {
-    return mass_key(j < a.n_first || j >= n - a.n_recent ? INFINITY : m);
+    return mass_key(j < fixed_end || j >= fixed_from ? INFINITY : m);
   };
+  // full batches of a part without protected entries skip those tests
+  const bool plain = j0 >= fixed_end && j1 <= fixed_from;
   uint32_t held[kInRegs ? kHold : 1];
   if (kInRegs) {
 #pragma unroll
@@ -94,23 +98,27 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
 #pragma unroll
     for (int e = 0; e < kHold; ++e) held[e] = key_of(j0 + 32 * e + lane, __uint_as_float(held[e]));
   }
-  // f(j, key) for every entry of this lane
+  // f(key) for every entry of this lane
   auto each = [&](auto f) {
     if constexpr (kInRegs) {
 #pragma unroll
-      for (int e = 0; e < kHold; ++e) {
-        const int j = j0 + 32 * e + lane;
-        if (j < j1) f(j, held[e]);
-      }
+      for (int e = 0; e < kHold; ++e)
+        if (j0 + 32 * e + lane < j1) f(held[e]);
     } else {
-      for (int j = j0 + lane; j < j1; j += 32 * kBatch) {
-        float m[kBatch];
+      int j = j0 + lane;
+      if (plain) {
+        const float *p = mass + j;
+        for (int left = (j1 - j0) / (32 * kBatch); left > 0; --left, p += 32 * kBatch) {
+          float m[kBatch];
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) m[e] = j + 32 * e < j1 ? __ldg(mass + j + 32 * e) : 0.f;
+          for (int e = 0; e < kBatch; ++e) m[e] = __ldg(p + 32 * e);
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e)
-          if (j + 32 * e < j1) f(j + 32 * e, key_of(j + 32 * e, m[e]));
+          for (int e = 0; e < kBatch; ++e) f(mass_key(m[e]));
+        }
+        j += (j1 - j0) / (32 * kBatch) * (32 * kBatch);
       }
+#pragma unroll 4
+      for (; j < j1; j += 32) f(key_of(j, __ldg(mass + j)));
     }
   };
 
@@ -132,14 +140,17 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   }
   for (int i = threadIdx.x; i < 2 * kBins; i += kEvThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  if (threadIdx.x < 2) {
-    long long s = 0;
-    for (int w = 0; w < kEvWarps; ++w) s += red[threadIdx.x][w];
-    base_s[threadIdx.x] = s;
-    if (rank == 0) {
-      int32_t *ptr = threadIdx.x ? a.dropped_indptr : a.out_indptr;
-      if (b == 0) ptr[0] = 0;
-      ptr[b + 1] = (int32_t)(s + (threadIdx.x ? n - kk : kk));
+  if (warp < 2) {
+    long long s = red[warp][lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      base_s[warp] = s;
+      if (rank == 0) {
+        int32_t *ptr = warp ? a.dropped_indptr : a.out_indptr;
+        if (b == 0) ptr[0] = 0;
+        ptr[b + 1] = (int32_t)(s + (warp ? n - kk : kk));
+      }
     }
   }
 
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     const uint32_t digit = d == 2 ? 0x3ffu : 0x7ffu;
     const uint32_t above = d == 0 ? 0u : d == 1 ? 0xffe00000u : 0xfffffc00u;
     int *h = hist[d & 1];
-    each([&](int, uint32_t k) {
+    each([&](uint32_t k) {
       if ((k & above) == prefix) atomicAdd(&h[(k >> shift) & digit], 1);
     });
     cl.sync();
@@ -180,7 +191,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     __syncthreads();
     if (threadIdx.x < kBins / 4) {
       int before = incl - sum;
-      for (int w = 0; w < warp; ++w) before += scan[w];
+#pragma unroll
+      for (int w = 0; w < kBins / 128; ++w) before += w < warp ? scan[w] : 0;
       int left = want - before;
       if (left > 0 && left <= sum) {
 #pragma unroll
@@ -201,15 +213,17 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
       for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[0][i] = 0;
     if (d == 1) __syncthreads();
   }
-  // kept: keys above `prefix`, and the first `want` equal ones
+  // kept: keys above `prefix`, and the first `want` equal ones.  No key is 0
+  // (-inf's image is 0x007fffff) and none 0xffffffff: all or none.
+  if (!some) {
+    prefix = kk > 0 ? 0u : 0xffffffffu;
+    want = 0;
+  }
   int above_n = 0, equal_n = 0;
-  if (some)
-    each([&](int, uint32_t k) {
-      above_n += k > prefix;
-      equal_n += k == prefix;
-    });
-  else if (kk > 0)
-    above_n = j1 > j0 + lane ? (j1 - j0 - lane + 31) / 32 : 0;
+  each([&](uint32_t k) {
+    above_n += k > prefix;
+    equal_n += k == prefix;
+  });
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     above_n += __shfl_xor_sync(0xffffffffu, above_n, o);
@@ -220,10 +234,16 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     warp_n[1][warp] = equal_n;
   }
   __syncthreads();
-  if (threadIdx.x < 2) {
-    int s = 0;
-    for (int w = 0; w < kEvWarps; ++w) s += warp_n[threadIdx.x][w];
-    cta_n[threadIdx.x] = s;
+  if (warp < 2) {  // the warps' counts become what lies before each
+    const int x = warp_n[warp][lane];
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    warp_n[warp][lane] = incl - x;
+    if (lane == 31) cta_n[warp] = incl;
   }
   cl.sync();
   int above_before = 0, equal_before = 0;
@@ -232,51 +252,65 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     above_before += c[0];
     equal_before += c[1];
   }
-  for (int w = 0; w < warp; ++w) {
-    above_before += warp_n[0][w];
-    equal_before += warp_n[1][w];
-  }
+  above_before += warp_n[0][warp];
+  equal_before += warp_n[1][warp];
   int kept = above_before + min(equal_before, want);  // kept entries before the next one
   int equal = equal_before;
   const int64_t kept_base = base_s[0], drop_base = base_s[1];
   const uint32_t below = (1u << lane) - 1u;
+  // room from this request's first kept and dropped entry on
+  const auto room = [](int64_t cap, int64_t base) {
+    return (int)max((int64_t)0, min(cap - base, (int64_t)INT32_MAX));
+  };
+  const int kept_room = room(a.out_cap, kept_base), drop_room = room(a.dropped_cap, drop_base);
+  const int mass_room = room(a.out_stride, 0);
+  int32_t *const out_idx = a.out_indices + kept_base;
+  int32_t *const out_pos = a.out_pos ? a.out_pos + kept_base : nullptr;
+  float *const out_mass = a.out_mass + (int64_t)b * a.out_stride;
+  int32_t *const out_drop = a.dropped + drop_base;
   // 32 entries: e = this lane's, its mass, slot and position at hand
-  auto place = [&](int e, uint32_t k, float m, int32_t slot, int32_t pos) {
-    const bool there = e < j1;
-    const bool eq = some && there && k == prefix;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-    const bool keep = there && kk > 0 &&
-                      (!some || k > prefix || (eq && equal + __popc(eqs & below) < want));
+  auto place = [&](int e, bool there, uint32_t k, float m, int32_t slot, int32_t pos) {
+    bool keep = there && k > prefix;
+    uint32_t eqs = __ballot_sync(0xffffffffu, there && k == prefix);
+    if (eqs) {  // the first `want` of these
+      keep |= (eqs >> lane & 1u) && equal + __popc(eqs & below) < want;
+      equal += __popc(eqs);
+    }
     const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
     const int kb = kept + __popc(keeps & below);
-    if (keep) {
-      const int64_t to = kept_base + kb;
-      if (to < a.out_cap) {
-        a.out_indices[to] = slot;
-        if (a.out_pos) a.out_pos[to] = pos;
-      }
-      if (kb < a.out_stride) a.out_mass[(int64_t)b * a.out_stride + kb] = m;
-    } else if (there && drop_base + (e - kb) < a.dropped_cap) {
-      a.dropped[drop_base + (e - kb)] = slot;
-    }
     kept += __popc(keeps);
-    equal += __popc(eqs);
-  };
-  const int32_t *idx = a.indices + (int64_t)beg, *pos = a.pos ? a.pos + (int64_t)beg : nullptr;
-  for (int j = j0; j < j1; j += 32 * kBatch) {
-    float m[kBatch];
-    int32_t s[kBatch], p[kBatch];
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int at = j + 32 * e + lane;
-      const bool there = at < j1;
-      m[e] = there ? __ldg(mass + at) : 0.f;
-      s[e] = there ? __ldg(idx + at) : 0;
-      p[e] = there && pos ? __ldg(pos + at) : 0;
+    if (keep) {
+      if (kb < kept_room) {
+        out_idx[kb] = slot;
+        if (out_pos) out_pos[kb] = pos;
+      }
+      if (kb < mass_room) out_mass[kb] = m;
+    } else if (there && e - kb < drop_room) {
+      out_drop[e - kb] = slot;
     }
+  };
+  const int32_t *idx = a.indices + (int64_t)beg, *pos = a.pos ? a.pos + (int64_t)beg : idx;
+  int j = j0;
+  if (plain)
+    for (; j + 32 * kBatch <= j1; j += 32 * kBatch) {
+      float m[kBatch];
+      int32_t s[kBatch], p[kBatch];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e)
-      if (j + 32 * e < j1) place(j + 32 * e + lane, key_of(j + 32 * e + lane, m[e]), m[e], s[e], p[e]);
+      for (int e = 0; e < kBatch; ++e) {
+        m[e] = __ldg(mass + j + lane + 32 * e);
+        s[e] = __ldg(idx + j + lane + 32 * e);
+        p[e] = __ldg(pos + j + lane + 32 * e);
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        place(j + lane + 32 * e, true, mass_key(m[e]), m[e], s[e], p[e]);
+    }
+#pragma unroll 2
+  for (; j < j1; j += 32) {
+    const int e = j + lane;
+    const bool there = e < j1;
+    const float m = there ? __ldg(mass + e) : 0.f;
+    place(e, there, key_of(e, m), m, there ? __ldg(idx + e) : 0, there ? __ldg(pos + e) : 0);
   }
   cl.sync();  // a CTA's counts stay readable until every CTA has them
 }

@@ -11,8 +11,8 @@
 // are the two halves of its rotation pairs, so the norm is log2(kLanes)
 // shuffles and the rotation needs no exchange.  A warp walks head rows of one
 // token, so lane f forms the angle of frequency f once per token and the
-// lanes fetch theirs by shuffle; the next pass's loads are issued before a
-// pass is computed.  Few tokens: a token's passes are spread over `parts`
+// lanes fetch theirs by shuffle; passes go two at a time, the next two's
+// loads issued before a pair is computed.  Few tokens: a token's passes are spread over `parts`
 // warps, which only repeat the one angle per lane.
 #include "common.cuh"
 
@@ -22,6 +22,7 @@ namespace akv {
 namespace {
 
 constexpr int kNormWarps = 8;
+constexpr int kPair = 2;
 
 template <typename T>
 struct RowArgs {
@@ -38,20 +39,24 @@ struct RowArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kNormWarps * 32)
+__global__ void __launch_bounds__(kNormWarps * 32, 3)
     qk_norm_append_kernel(const RowArgs<T> a, const __grid_constant__ RopeTheta th) {
   constexpr int E = Chunk<T>::kElems;
   constexpr int kLanes = (kD / 2) / E;  // lanes per head row: 4 (bf16), 8 (fp32)
   constexpr int kRows = 32 / kLanes;    // head rows per pass of a warp
   __shared__ ThetaSmem ts;
+  __shared__ __align__(16) float wt[2][kD];
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
   const int64_t i = w / a.parts;
   const int part = (int)(w % a.parts);
   stage_theta(th, ts);
+  if (threadIdx.x < 2 * kD) {
+    const float *src = threadIdx.x < kD ? a.qw : a.kw;
+    wt[threadIdx.x / kD][threadIdx.x % kD] = src ? __ldg(src + threadIdx.x % kD) : 1.f;
+  }
+  const int slot = i < a.n ? a.slot[i] : -1;
   __syncthreads();
-  if (i >= a.n) return;
-  const int slot = a.slot[i];
   if ((unsigned)slot >= (unsigned)a.S) return;  // padding: nothing read or written
   const int pos = (a.flags & (AKV_ROPE_Q | AKV_ROPE_K)) ? a.pos[i] : 0;
   const int c = lane % kLanes, r = lane / kLanes;
@@ -66,17 +71,25 @@ __global__ void __launch_bounds__(kNormWarps * 32)
       const int h = p * kRows + r;
       return h < a.Hq ? reinterpret_cast<const uint4 *>(a.q + i * a.qs + (int64_t)h * kD) : nullptr;
     }
-    const int h = ((p - pq) % pk) * kRows + r;
+    const int h = (p - pq - (p < pq + pk ? 0 : pk)) * kRows + r;
     if (h >= a.Hkv) return nullptr;
     const T *b = p < pq + pk ? a.k + i * a.ks : a.v + i * a.vs;
     return reinterpret_cast<const uint4 *>(b + (int64_t)h * kD);
   };
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 x0 = zero, x1 = zero;
-  if (const uint4 *s = source(p0)) {
-    x0 = s[c];
-    x1 = s[c + kLanes];
-  }
+  uint4 x[kPair][2];
+  auto fetch = [&](int p) {
+#pragma unroll
+    for (int u = 0; u < kPair; ++u) {
+      x[u][0] = x[u][1] = zero;
+      const uint4 *s = p + u < p1 ? source(p + u) : nullptr;
+      if (s) {
+        x[u][0] = s[c];
+        x[u][1] = s[c + kLanes];
+      }
+    }
+  };
+  fetch(p0);
   // cos/sin of this lane's frequencies c * E .. c * E + E - 1
   float co[E], si[E];
   {
@@ -88,68 +101,61 @@ __global__ void __launch_bounds__(kNormWarps * 32)
       si[e] = __shfl_sync(0xffffffffu, sf, c * E + e);
     }
   }
-  float w0[E], w1[E];
-  int kind_held = -1;
-  for (int p = p0; p < p1; ++p) {
-    const uint4 y0 = x0, y1 = x1;
-    const bool mine = source(p) != nullptr;
-    if (p + 1 < p1) {
-      x0 = x1 = zero;
-      if (const uint4 *s = source(p + 1)) {
-        x0 = s[c];
-        x1 = s[c + kLanes];
-      }
+  for (int pp = p0; pp < p1; pp += kPair) {
+    uint4 y[kPair][2];
+#pragma unroll
+    for (int u = 0; u < kPair; ++u) {
+      y[u][0] = x[u][0];
+      y[u][1] = x[u][1];
     }
-    const int kind = p < pq ? 0 : p < pq + pk ? 1 : 2;
-    const int h = (kind == 0 ? p : (p - pq) % pk) * kRows + r;
-    uint4 z0 = y0, z1 = y1;
-    if (kind < 2) {
-      const bool norm = a.flags & (kind ? AKV_NORM_K : AKV_NORM_Q);
-      const bool rope = a.flags & (kind ? AKV_ROPE_K : AKV_ROPE_Q);
-      float f0[E], f1[E];
-      chunk_to_f32<T>(y0, f0);
-      chunk_to_f32<T>(y1, f1);
-      if (norm) {
-        if (kind != kind_held) {
-          const float *wt = kind ? a.kw : a.qw;
+    if (pp + kPair < p1) fetch(pp + kPair);
+#pragma unroll
+    for (int u = 0; u < kPair; ++u) {
+      const int p = pp + u;
+      if (p >= p1) break;
+      const uint4 y0 = y[u][0], y1 = y[u][1];
+      const int kind = p < pq ? 0 : p < pq + pk ? 1 : 2;
+      const int h = (kind == 0 ? p : p - pq - (kind == 1 ? 0 : pk)) * kRows + r;
+      uint4 z0 = y0, z1 = y1;
+      if (kind < 2) {
+        const bool norm = a.flags & (kind ? AKV_NORM_K : AKV_NORM_Q);
+        const bool rope = a.flags & (kind ? AKV_ROPE_K : AKV_ROPE_Q);
+        float f0[E], f1[E];
+        chunk_to_f32<T>(y0, f0);
+        chunk_to_f32<T>(y1, f1);
+        if (norm) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) ss = fmaf(f0[e], f0[e], fmaf(f1[e], f1[e], ss));
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            w0[e] = wt ? __ldg(wt + c * E + e) : 1.f;
-            w1[e] = wt ? __ldg(wt + kD / 2 + c * E + e) : 1.f;
+            f0[e] = f0[e] * inv * wt[kind][c * E + e];
+            f1[e] = f1[e] * inv * wt[kind][kD / 2 + c * E + e];
           }
-          kind_held = kind;
         }
-        float ss = 0.f;
+        if (rope) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(f0[e], f0[e], fmaf(f1[e], f1[e], ss));
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          f0[e] = f0[e] * inv * w0[e];
-          f1[e] = f1[e] * inv * w1[e];
+          for (int e = 0; e < E; ++e) {
+            const float u = f0[e], v = f1[e];
+            f0[e] = u * co[e] - v * si[e];
+            f1[e] = u * si[e] + v * co[e];
+          }
         }
-      }
-      if (rope) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float u = f0[e], v = f1[e];
-          f0[e] = u * co[e] - v * si[e];
-          f1[e] = u * si[e] + v * co[e];
+        if (norm || rope) {
+          z0 = f32_to_chunk<T>(f0);
+          z1 = f32_to_chunk<T>(f1);
         }
       }
-      if (norm || rope) {
-        z0 = f32_to_chunk<T>(f0);
-        z1 = f32_to_chunk<T>(f1);
+      if (h < (kind ? a.Hkv : a.Hq)) {
+        T *dst = kind == 0   ? a.q_out + (i * a.Hq + h) * kD
+                 : kind == 1 ? a.kp + ((int64_t)slot * a.Hkv + h) * kD
+                             : a.vp + ((int64_t)slot * a.Hkv + h) * kD;
+        reinterpret_cast<uint4 *>(dst)[c] = z0;
+        reinterpret_cast<uint4 *>(dst)[c + kLanes] = z1;
       }
-    }
-    if (mine) {
-      T *dst = kind == 0   ? a.q_out + (i * a.Hq + h) * kD
-               : kind == 1 ? a.kp + ((int64_t)slot * a.Hkv + h) * kD
-                           : a.vp + ((int64_t)slot * a.Hkv + h) * kD;
-      reinterpret_cast<uint4 *>(dst)[c] = z0;
-      reinterpret_cast<uint4 *>(dst)[c + kLanes] = z1;
     }
   }
 }
