@@ -30,7 +30,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kHold = 16;   // keys per thread that stay in registers
 constexpr int kBatch = 8;   // loads in flight per thread otherwise
 constexpr int kBins = 2048;
-static_assert(kEvWarps == 32, "scans over the warps take one lane each");
+static_assert(kEvWarps == 32 && kBins == 64 * kEvWarps, "a lane per warp, 64 bins per warp");
 constexpr int kMaxCluster = 16;  // above 8 is not portable: asked for only where it fits
 
 struct EvictArgs {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   __shared__ int warp_n[2][kEvWarps];  // per warp: entries above / equal to the threshold
   __shared__ int cta_n[2];
   __shared__ int pick[2];              // chosen digit, entries still wanted in it
-  __shared__ int scan[kEvWarps];
+  __shared__ int coarse[2][kEvWarps];
   __shared__ long long base_s[2];
   __shared__ long long red[2][kEvWarps];
   const int size = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -166,43 +166,47 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
     each([&](uint32_t k) {
       if ((k & above) == prefix) atomicAdd(&h[(k >> shift) & digit], 1);
     });
-    cl.sync();
-    // thread t < 512: bins 4 u .. 4 u + 3 with u = 511 - t, highest first
-    int c[4] = {}, sum = 0;
-    if (threadIdx.x < kBins / 4) {
-      const int u = kBins / 4 - 1 - threadIdx.x;
-#pragma unroll 4
-      for (int o = 0; o < size; ++o) {
-        const int4 v = reinterpret_cast<const int4 *>(cl.map_shared_rank(h, o))[u];
-        c[0] += v.w;
-        c[1] += v.z;
-        c[2] += v.y;
-        c[3] += v.x;
-      }
-      sum = (c[0] + c[1]) + (c[2] + c[3]);
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    if (threadIdx.x < kBins / 4) {
-      int before = incl - sum;
+    // Coarse counts of 64 bins, one per warp, so that the cluster's counts are
+    // found in two short steps: the coarse bin, then the bin in it.  (Every
+    // CTA reading every bin of every other moved 64 KB: 4.2 us a digit.)
+    {
+      int x = h[64 * warp + lane] + h[64 * warp + 32 + lane];
 #pragma unroll
-      for (int w = 0; w < kBins / 128; ++w) before += w < warp ? scan[w] : 0;
-      int left = want - before;
-      if (left > 0 && left <= sum) {
+      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) coarse[d & 1][warp] = x;
+    }
+    cl.sync();
+    if (warp == 0) {
+      // lane l stands for the coarse bin 31 - l, then for two bins of the one
+      // found, highest first
+      const auto above_me = [&](int x) {  // sum over the lanes before this one
+        int incl = x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (left > 0 && left <= c[e]) {
-            pick[0] = kBins - 1 - 4 * (int)threadIdx.x - e;
-            pick[1] = left;
-          }
-          left -= c[e];
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += t;
         }
+        return incl - x;
+      };
+      int x = 0;
+#pragma unroll 8
+      for (int o = 0; o < size; ++o) x += cl.map_shared_rank(coarse[d & 1], o)[31 - lane];
+      int left = want - above_me(x);
+      const int at = __ffs(__ballot_sync(0xffffffffu, left > 0 && left <= x)) - 1;
+      left = __shfl_sync(0xffffffffu, left, at);
+      int hi = 0, lo = 0;
+      const int bin = 64 * (31 - at) + 62 - 2 * lane;
+#pragma unroll 8
+      for (int o = 0; o < size; ++o) {
+        const int2 v = *reinterpret_cast<const int2 *>(cl.map_shared_rank(h, o) + bin);
+        lo += v.x;
+        hi += v.y;
+      }
+      left -= above_me(hi + lo);
+      if (left > 0 && left <= hi + lo) {
+        pick[0] = left <= hi ? bin + 1 : bin;
+        pick[1] = left <= hi ? left : left - hi;
       }
     }
     __syncthreads();
