@@ -38,69 +38,71 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *dst, const 
                                                *reinterpret_cast<const uint32_t *>(&b));
 }
 
-struct SimtSmem {
-  float q[kD][kSimtPad], k[kD][kSimtPad], v[kSimt][kSimtPad], p[kSimt][kSimtPad];
+// fp32, CUDA cores: CTA = 128 packed rows of one KV head x one key split, 64
+// keys at a time, online softmax.  K of the next keys is copied while a step's
+// weights are formed and multiplied with V, V while the next scores are.
+// Tensor cores take no fp32 operands; this path is for single-precision
+// parity, bound by the fp32 pipes and their shared-memory operands.
+struct F32Smem {
+  float q[kFRows][kFPitch], p[kFRows][kFPitch], k[kFKeys][kFPitch], v[kFKeys][kFPitch];
 };
 
-// CUDA-core form, every type and head count: CTA = 64 packed rows of one KV
-// head x one key split, 64-key tiles, online softmax.
-template <typename T>
-__global__ void __launch_bounds__(kSimtThreads)
-    chunk_simt_kernel(const ChunkBatch a, T *out, float *lse, const ChunkParts part) {
+__global__ void __launch_bounds__(kFThreads, 2)
+    chunk_f32_kernel(const ChunkBatch a, float *out, float *lse, const ChunkParts part) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SimtSmem &sm = *reinterpret_cast<SimtSmem *>(smem_raw);
-  const int split = blockIdx.x % part.ns, rt = blockIdx.x / part.ns, g = blockIdx.y, b = blockIdx.z;
+  F32Smem &sm = *reinterpret_cast<F32Smem *>(smem_raw);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
+  const int64_t r0 = (int64_t)(blockIdx.x / part.ns) * kFRows;
   const ChunkReq rq = chunk_req(a, b);
-  const int grp = a.Hq / a.Hkv, rows = rq.m * grp, r0 = rt * kSimt;
+  const int grp = a.Hq / a.Hkv;
+  const int64_t rows = (int64_t)rq.m * grp;
   if (r0 >= rows) return;
-  const int last = (min(rows, r0 + kSimt) - 1) / grp;  // the tile's last token
+  const int64_t r1 = min(rows, r0 + kFRows);
   const int c0 = split * part.chunk;
-  const int c1 = min(rq.limit(last), c0 + part.chunk);
+  const int c1 = min(rq.limit((int)((r1 - 1) / grp)), c0 + part.chunk);
   if (split > 0 && c0 >= c1) return;  // the merge reads only splits with visible entries
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  int lim[4];
+  const int first = rq.limit((int)(r0 / grp));  // every row sees the entries before it
+  int lim[8];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int r = r0 + 4 * ty + p;
-    lim[p] = r < rows ? rq.limit(r / grp) : 0;
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + ty + 16 * p;
+    lim[p] = r < r1 ? rq.limit((int)(r / grp)) : 0;
   }
-  simt_load_q<T>(sm.q, a, rq, g, r0);
-  float o[4][4] = {}, m[4], l[4] = {};
+  const auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
+  f32_load_q(sm.q, a, rq, g, r0);
+  f32_load_kv(sm.k, a.k, a, rq, g, c0, c1);
+  commit();
+  f32_load_kv(sm.v, a.v, a, rq, g, c0, c1);
+  commit();
+  float o[8][4], m[8], l[8];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) m[p] = -INFINITY;
-  for (int j0 = c0; j0 < c1; j0 += kSimt) {
-    __syncthreads();  // the previous tile's readers are done
-    simt_load_k<T>(sm.k, a, rq, g, j0, c1);
-    for (int u = threadIdx.x; u < kSimt * (kD / Chunk<T>::kElems); u += kSimtThreads) {
-      constexpr int E = Chunk<T>::kElems, C = kD / E;
-      const int key = u / C, c = u % C;
-      float f[E];
+  for (int p = 0; p < 8; ++p) {
+    o[p][0] = o[p][1] = o[p][2] = o[p][3] = l[p] = 0.f;
+    m[p] = -INFINITY;
+  }
+  for (int j0 = c0; j0 < c1; j0 += kFKeys) {
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    __syncthreads();  // K (and Q) landed
+    float s[8][4];
+    f32_scores(sm.q, sm.k, ty, tx, s);
+    __syncthreads();  // K's readers are done
+    f32_load_kv(sm.k, a.k, a, rq, g, j0 + kFKeys, c1);
+    commit();
+    const bool ragged = j0 + kFKeys > min(first, c1);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = 0.f;
-      if (j0 + key < c1)
-        chunk_to_f32<T>(__ldg(reinterpret_cast<const uint4 *>(
-                            (const T *)a.v + (chunk_slot(a, rq, j0 + key) * a.Hkv + g) * kD) + c), f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) sm.v[key][c * E + e] = f[e];
-    }
-    __syncthreads();
-    float s[4][4] = {};
-    simt_mma(sm.q, sm.k, ty, tx, s);
-    // A tile with a hidden entry keeps that entry's value out of the sum
-    // whatever it holds (0 * NaN): such tiles skip hidden keys per row.
-    const bool ragged = j0 + kSimt > rq.limit(r0 / grp);
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < 8; ++p) {
       float mx = -INFINITY;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (j0 + 4 * tx + q >= min(lim[p], c1)) s[p][q] = -INFINITY;
+        if (ragged && j0 + tx + 16 * q >= min(lim[p], c1)) s[p][q] = -INFINITY;
         mx = fmaxf(mx, s[p][q]);
       }
 #pragma unroll
       for (int x = 8; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
       const float mn = fmaxf(m[p], mx), ref = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f((m[p] - ref) * (0.125f * kLog2e));
+      const float alpha = exp2f((m[p] - ref) * kScale);
       m[p] = mn;
       l[p] *= alpha;
 #pragma unroll
@@ -108,44 +110,73 @@ __global__ void __launch_bounds__(kSimtThreads)
         o[p][q] *= alpha;
         // the difference is taken before the scale: its rounding is relative
         // to the distance from the maximum
-        s[p][q] = exp2f((s[p][q] - ref) * (0.125f * kLog2e));
-        l[p] += s[p][q];
-        sm.p[4 * tx + q][4 * ty + p] = s[p][q];
+        const float w = exp2f((s[p][q] - ref) * kScale);
+        l[p] += w;
+        sm.p[ty + 16 * p][tx + 16 * q] = w;
       }
     }
-    __syncthreads();
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    __syncthreads();  // V landed, P written
+    // o[p][q]: column 4 tx + q
     if (!ragged) {
-      simt_mma(sm.p, sm.v, ty, tx, o);
+#pragma unroll 4
+      for (int j = 0; j < kFKeys; j += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const float4 *>(&sm.v[j + e][4 * tx]);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const float4 u = *reinterpret_cast<const float4 *>(&sm.p[ty + 16 * p][j]);
+          const float uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[p][0] = fmaf(uu[e], w[e].x, o[p][0]);
+            o[p][1] = fmaf(uu[e], w[e].y, o[p][1]);
+            o[p][2] = fmaf(uu[e], w[e].z, o[p][2]);
+            o[p][3] = fmaf(uu[e], w[e].w, o[p][3]);
+          }
+        }
+      }
     } else {
-      for (int d = 0; d < kSimt; ++d) {
+      // a hidden entry's value stays out of the sum whatever it holds (0 * NaN)
+#pragma unroll 1
+      for (int j = 0; j < kFKeys; ++j) {
+        const float4 w = *reinterpret_cast<const float4 *>(&sm.v[j][4 * tx]);
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-          if (j0 + d < lim[p])
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              o[p][q] = fmaf(sm.p[d][4 * ty + p], sm.v[d][4 * tx + q], o[p][q]);
+        for (int p = 0; p < 8; ++p)
+          if (j0 + j < min(lim[p], c1)) {
+            const float u = sm.p[ty + 16 * p][j];
+            o[p][0] = fmaf(u, w.x, o[p][0]);
+            o[p][1] = fmaf(u, w.y, o[p][1]);
+            o[p][2] = fmaf(u, w.z, o[p][2]);
+            o[p][3] = fmaf(u, w.w, o[p][3]);
+          }
       }
     }
+    __syncthreads();  // V's and P's readers are done
+    f32_load_kv(sm.v, a.v, a, rq, g, j0 + kFKeys, c1);
+    commit();
   }
+  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
+  for (int p = 0; p < 8; ++p) {
 #pragma unroll
     for (int x = 8; x; x >>= 1) l[p] += __shfl_xor_sync(0xffffffffu, l[p], x);
-    const int r = r0 + 4 * ty + p;
-    if (r >= rows) continue;
-    const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
+    const int64_t r = r0 + ty + 16 * p;
+    if (r >= r1) continue;
+    const int64_t row = (int64_t)(rq.q0 + (int)(r / grp)) * a.Hq + g * grp + (int)(r % grp);
     if (part.direct(lim[p])) {
       if (split > 0) continue;
       const bool none = lim[p] == 0;
       float y[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) y[q] = none ? 0.f : o[p][q] / l[p];
-      store4<T>(out + row * kD + 4 * tx, y);
+      store4<float>(out + row * kD + 4 * tx, y);
       if (lse && tx == 0) lse[row] = none ? -INFINITY : m[p] * 0.125f + logf(l[p]);
     } else {
       const int64_t pi = row * part.ns + split;
       store4<float>(part.o + pi * kD + 4 * tx, o[p]);
-      if (tx == 0) part.ml[pi] = make_float2(m[p] * (0.125f * kLog2e), l[p]);
+      if (tx == 0) part.ml[pi] = make_float2(m[p] * kScale, l[p]);
     }
   }
 }
@@ -925,7 +956,7 @@ struct ChunkPlan {
   int ns, chunk;  // key splits and entries of each
   int64_t tiles;  // row tiles of one (request, KV head)
 };
-constexpr int kSimtKind = 0, kSmallKind = 1, kTcKind = 3;
+constexpr int kF32Kind = 0, kSmallKind = 1, kTcKind = 3;
 
 // Key splits: none if `ctas` (the unsplit grid) reaches `want`; otherwise
 // chunks of max_chunk entries halved until it does, but not below `least` --
@@ -962,24 +993,23 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
     split_keys(&p, p.tiles * B * Hkv, 4LL * per_sm * sms, (int64_t)per_sm * sms, max_kv, 16384, 2048,
                512);
   } else {
-    p.kind = kSimtKind;
-    p.tiles = (rows + kSimt - 1) / kSimt;
-    split_keys(&p, p.tiles * B * Hkv, 4LL * sms, 3LL * sms, max_kv, 4096, 512, 128);
+    p.kind = kF32Kind;
+    p.tiles = (rows + kFRows - 1) / kFRows;
+    split_keys(&p, p.tiles * B * Hkv, 4LL * 2 * sms, 2LL * sms, max_kv, 4096, 512, 128);
   }
   return p;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <typename T>
-cudaError_t launch_simt(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
-                        int64_t tiles, cudaStream_t s) {
-  const int smem = (int)sizeof(SimtSmem);
-  cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_f32(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+                       int64_t tiles, cudaStream_t s) {
+  const int smem = (int)sizeof(F32Smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(chunk_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_simt_kernel<T><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kSimtThreads, smem, s>>>(
-      a, (T *)out, lse, part);
+  chunk_f32_kernel<<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kFThreads, smem, s>>>(
+      a, (float *)out, lse, part);
   return cudaGetLastError();
 }
 
@@ -1053,7 +1083,7 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   else if (p.kind == kTcKind + 1) e = launch_tc<2>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
   else if (p.kind == kSmallKind) e = launch_small<1>(a, out, lse, part, s);
   else if (p.kind == kSmallKind + 1) e = launch_small<2>(a, out, lse, part, s);
-  else e = launch_simt<float>(a, out, lse, part, p.tiles, s);
+  else e = launch_f32(a, out, lse, part, p.tiles, s);
   if (e != cudaSuccess || p.ns == 1) return e;
   return dtype == AKV_BF16 ? launch_merge<__nv_bfloat16>(a, out, lse, part, s)
                            : launch_merge<float>(a, out, lse, part, s);

@@ -106,59 +106,64 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return (nonfinite_lo(w) ? 0u : w & 0xffffu) | (nonfinite_hi(w) ? 0u : w & 0xffff0000u);
 }
 
-// ---- 64 x 64 score tile on the CUDA cores, 256 threads, 4 x 4 per thread ----
-// Thread (ty, tx) = (tid / 16, tid % 16) holds rows 4 ty .. + 3 and keys (or
-// value columns) 4 tx .. + 3.  Q and K are staged transposed ([d][row]) so
-// that both operands of a step are one 16-byte shared load.
-constexpr int kSimt = 64;
-constexpr int kSimtPad = kSimt + 4;
-constexpr int kSimtThreads = 256;
+// ---- CUDA cores (fp32): 128 packed rows x 64 keys, 256 threads ----
+// Thread (ty, tx) = (tid / 16, tid % 16) holds rows ty + 16 p (p < 8) and keys
+// tx + 16 q (q < 4).  All tiles are row-major with rows of 272 bytes, so that
+// they are copied as they lie in memory (cp.async) and every operand is a
+// 16-byte shared load: a warp's two Q rows are broadcast, its 16 K rows fall in
+// different banks.  12 loads feed 128 multiply-adds.
+constexpr int kFRows = 128;
+constexpr int kFKeys = 64;
+constexpr int kFPitch = kD + 4;  // floats
+constexpr int kFThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ void simt_stage_t(float (*dst)[kSimtPad], int row, int part,
-                                             const T *src) {
-  constexpr int E = Chunk<T>::kElems;
+// packed rows r0.. of KV head g (rows past the chunk: zeros)
+__device__ __forceinline__ void f32_load_q(float (*dst)[kFPitch], const ChunkBatch &a,
+                                           const ChunkReq &rq, int g, int64_t r0) {
+  const int grp = a.Hq / a.Hkv, c = threadIdx.x % 16;
+  const int64_t rows = (int64_t)rq.m * grp;
+  for (int x = threadIdx.x / 16; x < kFRows; x += kFThreads / 16) {
+    const int64_t r = r0 + x;
+    const bool ok = r < rows;
+    const int i = ok ? (int)(r / grp) : 0, h = ok ? (int)(r % grp) : 0;
+    cp_async16(ptx::smem_addr(&dst[x][4 * c]),
+               (const float *)a.q + ((int64_t)(rq.q0 + i) * a.Hq + g * grp + h) * kD + 4 * c, ok);
+  }
+}
+// list entries j0 .. of a pool, KV head g (entries from `end` on: zeros)
+__device__ __forceinline__ void f32_load_kv(float (*dst)[kFPitch], const void *pool,
+                                            const ChunkBatch &a, const ChunkReq &rq, int g, int j0,
+                                            int end) {
+  const int c = threadIdx.x % 16;
 #pragma unroll
-  for (int c = 0; c < 16 / E; ++c) {
-    float f[E];
-    if (src) chunk_to_f32<T>(__ldg(reinterpret_cast<const uint4 *>(src + part * 16) + c), f);
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[part * 16 + c * E + e][row] = src ? f[e] : 0.f;
+  for (int x = threadIdx.x / 16; x < kFKeys; x += kFThreads / 16) {
+    const bool ok = j0 + x < end;
+    const int64_t row = ok ? chunk_slot(a, rq, j0 + x) : 0;
+    cp_async16(ptx::smem_addr(&dst[x][4 * c]), (const float *)pool + (row * a.Hkv + g) * kD + 4 * c, ok);
   }
 }
 
-// packed rows r0.. of KV head g (rows past the chunk: zeros)
-template <typename T>
-__device__ __forceinline__ void simt_load_q(float (*dst)[kSimtPad], const ChunkBatch &a,
-                                            const ChunkReq &rq, int g, int r0) {
-  const int grp = a.Hq / a.Hkv, row = threadIdx.x % kSimt, r = r0 + row;
-  const T *src = nullptr;
-  if (r < rq.m * grp)
-    src = (const T *)a.q + ((int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp) * kD;
-  simt_stage_t<T>(dst, row, threadIdx.x / kSimt, src);
-}
-
-// keys j0.. of KV head g (entries from `end` on: zeros)
-template <typename T>
-__device__ __forceinline__ void simt_load_k(float (*dst)[kSimtPad], const ChunkBatch &a,
-                                            const ChunkReq &rq, int g, int j0, int end) {
-  const int row = threadIdx.x % kSimt, j = j0 + row;
-  const T *src =
-      j < end ? (const T *)a.k + (chunk_slot(a, rq, j) * a.Hkv + g) * kD : nullptr;
-  simt_stage_t<T>(dst, row, threadIdx.x / kSimt, src);
-}
-
-__device__ __forceinline__ void simt_mma(const float (*x)[kSimtPad], const float (*y)[kSimtPad],
-                                         int ty, int tx, float (*acc)[4]) {
-#pragma unroll 16
-  for (int d = 0; d < kSimt; ++d) {
-    const float4 u = *reinterpret_cast<const float4 *>(&x[d][4 * ty]);
-    const float4 w = *reinterpret_cast<const float4 *>(&y[d][4 * tx]);
-    const float uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+// acc[p][q] = q row . k row
+__device__ __forceinline__ void f32_scores(const float (*q)[kFPitch], const float (*k)[kFPitch],
+                                           int ty, int tx, float (*acc)[4]) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+  for (int p = 0; p < 8; ++p) acc[p][0] = acc[p][1] = acc[p][2] = acc[p][3] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < kD; d += 4) {
+    float4 w[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[p][q] = fmaf(uu[p], ww[q], acc[p][q]);
+    for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const float4 *>(&k[tx + 16 * e][d]);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float4 u = *reinterpret_cast<const float4 *>(&q[ty + 16 * p][d]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[p][e] = fmaf(u.x, w[e].x, acc[p][e]);
+        acc[p][e] = fmaf(u.y, w[e].y, acc[p][e]);
+        acc[p][e] = fmaf(u.z, w[e].z, acc[p][e]);
+        acc[p][e] = fmaf(u.w, w[e].w, acc[p][e]);
+      }
+    }
   }
 }
 

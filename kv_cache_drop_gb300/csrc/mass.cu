@@ -4,8 +4,8 @@
 // the first term for entries older than the chunk (the chunk's own entries
 // start at zero).  The weights are recomputed from the log-sum-exp that the
 // chunk attention leaves, so neither the scores nor the values are stored or
-// read.  A CTA owns 64 list entries of a request and walks every KV head and
-// row of the chunk, so each sum is formed in one fixed order.
+// read.  A CTA owns some list entries of a request and goes over KV heads and
+// rows; every sum is formed in one fixed order, whatever the timing.
 #include "chunk.cuh"
 
 #include <algorithm>
@@ -21,63 +21,93 @@ struct MassArgs {
   int64_t stride;
 };
 
-struct MassSmem {
-  float q[kD][kSimtPad], k[kD][kSimtPad];
-  float lse[kSimt];
-  float red[16][kSimt];
+// fp32, CUDA cores: CTA = 64 list entries x a share of the (KV head, 128-row
+// tile) items; the next item's rows are copied while one is computed.  Each
+// thread sums its four keys over its rows of every item, the 16 threads of a
+// key are joined at the end.
+struct MassF32Smem {
+  float q[2][kFRows][kFPitch], k[kFKeys][kFPitch];
+  float lse[2][kFRows];
+  float red[16][kFKeys];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kSimtThreads)
-    mass_simt_kernel(const ChunkBatch a, const MassArgs ma) {
-  __shared__ __align__(16) MassSmem sm;
-  const int b = blockIdx.y, j0 = blockIdx.x * kSimt;
+__global__ void __launch_bounds__(kFThreads, 2)
+    mass_f32_kernel(const ChunkBatch a, const MassArgs ma, int parts, float *partial) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  MassF32Smem &sm = *reinterpret_cast<MassF32Smem *>(smem_raw);
+  const int part = blockIdx.x % parts, b = blockIdx.y;
+  const int j0 = (int)(blockIdx.x / parts) * kFKeys;
   const ChunkReq rq = chunk_req(a, b);
   if (j0 >= rq.n) return;
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  // first token that sees anything of this tile
-  const int i0 = max(0, j0 - (rq.n - rq.m));
-  float sum[4] = {};
-  for (int g = 0; g < a.Hkv; ++g) {
-    __syncthreads();
-    simt_load_k<T>(sm.k, a, rq, g, j0, rq.n);
-    for (int r0 = i0 * grp; r0 < rows; r0 += kSimt) {
-      __syncthreads();
-      simt_load_q<T>(sm.q, a, rq, g, r0);
-      if (threadIdx.x < kSimt) {
-        const int r = r0 + threadIdx.x;
-        // +inf: a row that saw nothing, or no row, weighs 0
-        float v = INFINITY;
-        if (r < rows) {
-          v = ma.lse[(int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp];
-          if (v == -INFINITY) v = INFINITY;
-        }
-        sm.lse[threadIdx.x] = v;
+  const int old = rq.n - rq.m;
+  const int n_tiles = (rows + kFRows - 1) / kFRows;
+  // first row tile that sees anything of this block
+  const int t0 = min(n_tiles, (int)((int64_t)max(0, j0 - old) * grp / kFRows));
+  const int per_head = n_tiles - t0;
+  const int64_t items = (int64_t)per_head * a.Hkv;
+  const int64_t it0 = items * part / parts;
+  const int mine = (int)(items * (part + 1) / parts - it0);
+  int g = mine ? (int)(it0 / per_head) : 0, t = mine ? t0 + (int)(it0 % per_head) : 0;
+  auto load_rows = [&](int buf, int g, int t) {
+    f32_load_q(sm.q[buf], a, rq, g, (int64_t)t * kFRows);
+    if (threadIdx.x < kFRows) {
+      const int r = t * kFRows + threadIdx.x;
+      // +inf: a row that saw nothing, or no row, weighs 0
+      float v = INFINITY;
+      if (r < rows) {
+        v = __ldg(ma.lse + (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp);
+        if (v == -INFINITY) v = INFINITY;
       }
-      __syncthreads();
-      float s[4][4] = {};
-      simt_mma(sm.q, sm.k, ty, tx, s);
+      sm.lse[buf][threadIdx.x] = v;
+    }
+  };
+  float sum[4] = {};
+  if (mine) load_rows(0, g, t);
+  for (int it = 0; it < mine; ++it) {
+    const int r0 = t * kFRows, buf = it & 1;
+    if (it == 0 || t == t0) f32_load_kv(sm.k, a.k, a, rq, g, j0, rq.n);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    if (++t == n_tiles) {
+      t = t0;
+      ++g;
+    }
+    if (it + 1 < mine) load_rows(buf ^ 1, g, t);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    __syncthreads();
+    float s[8][4];
+    f32_scores(sm.q[buf], sm.k, ty, tx, s);
+    const int last = min(rq.n, j0 + kFKeys) - 1;  // sees the fewest rows
+    const bool plain = r0 >= (int64_t)max(0, last - old) * grp && r0 + kFRows <= rows;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int r = r0 + 4 * ty + p;
-        const float v = sm.lse[4 * ty + p];
-        const int lim = r < rows && v != INFINITY ? rq.limit(r / grp) : 0;
+    for (int p = 0; p < 8; ++p) {
+      const int r = r0 + ty + 16 * p;
+      const float v = sm.lse[buf][ty + 16 * p];
+      const int lim = plain ? INT32_MAX : r < rows && v != INFINITY ? rq.limit(r / grp) : 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (j0 + 4 * tx + q < lim) sum[q] += exp2f(fmaf(s[p][q], 0.125f, -v) * kLog2e);
+      for (int q = 0; q < 4; ++q) {
+        const float w = exp2f(fmaf(s[p][q], 0.125f, -v) * kLog2e);
+        sum[q] += j0 + tx + 16 * q < lim ? w : 0.f;
       }
     }
+    __syncthreads();  // readers of this buffer and of K are done
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sm.red[ty][4 * tx + q] = sum[q];
+  for (int q = 0; q < 4; ++q) sm.red[ty][tx + 16 * q] = sum[q];
   __syncthreads();
   const int j = j0 + threadIdx.x;
-  if (threadIdx.x < kSimt && j < rq.n) {
+  if (threadIdx.x < kFKeys && j < rq.n) {
     float x = 0.f;
+#pragma unroll
     for (int y = 0; y < 16; ++y) x += sm.red[y][threadIdx.x];
+    if (parts > 1) {
+      partial[((int64_t)part * a.B + b) * a.max_kv + j] = x;
+      return;
+    }
     const int64_t at = (int64_t)b * ma.stride + j;
-    if (ma.in && j < rq.n - rq.m) x = fmaf(ma.decay, ma.in[at], x);
+    if (ma.in && j < old) x = fmaf(ma.decay, ma.in[at], x);
     ma.out[at] = x;
   }
 }
@@ -612,30 +642,31 @@ __global__ void __launch_bounds__(256)
 struct MassPlan {
   int kind;   // 0 CUDA cores; 1, 2: mma.sync with that many 16-row tiles; 3: tcgen05
   int chunk;  // entries per CTA (kinds 1, 2)
-  int parts;  // CTAs per entry block (kind 3)
+  int parts;  // CTAs per entry block (kinds 0, 3)
 };
 
 MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   MassPlan p{0, 0, 1};
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
   const int sms = chunk_sms();
-  if (dtype != AKV_BF16) return p;
-  if (rows <= 32) {
+  if (dtype == AKV_BF16 && rows <= 32) {
     p.kind = rows <= 16 ? 1 : 2;
     p.chunk = kMChunk;
     while (p.chunk > 64 && (int64_t)B * ((max_kv + p.chunk - 1) / p.chunk) < 2LL * sms) p.chunk /= 2;
     return p;
   }
-  p.kind = 3;
+  const bool tc = dtype == AKV_BF16;
+  const int block = tc ? kMBlock : kFKeys, tile = tc ? kQRows : kFRows, resident = tc ? sms : 2 * sms;
+  p.kind = tc ? 3 : 0;
   // about four waves of CTAs, the last of them as full as twice the parts can
   // make it; none with less than four items
-  const int64_t blocks = std::max<int64_t>(1, (int64_t)B * ((max_kv + kMBlock - 1) / kMBlock));
-  const int64_t items = (rows + kQRows - 1) / kQRows * Hkv;
+  const int64_t blocks = std::max<int64_t>(1, (int64_t)B * ((max_kv + block - 1) / block));
+  const int64_t items = (rows + tile - 1) / tile * Hkv;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, items / 4));
-  const int64_t first = std::min<int64_t>(most, (4LL * sms + blocks - 1) / blocks);
+  const int64_t first = std::min<int64_t>(most, (4LL * resident + blocks - 1) / blocks);
   const auto idle = [&](int64_t n) {  // share of the launch's waves left empty
-    const int64_t ctas = blocks * n, waves = (ctas + sms - 1) / sms;
-    return (double)(waves * sms - ctas) / (double)(waves * sms);
+    const int64_t ctas = blocks * n, waves = (ctas + resident - 1) / resident;
+    return (double)(waves * resident - ctas) / (double)(waves * resident);
   };
   p.parts = (int)first;
   for (int64_t n = first + 1; n <= std::min<int64_t>(most, 2 * first); ++n)
@@ -673,21 +704,24 @@ cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                      nullptr};
   const MassArgs ma{lse, decay, in, out, stride};
   const MassPlan p = mass_plan(dtype, B, Hq, Hkv, max_q, max_kv);
-  if (p.kind == 0) {
-    mass_simt_kernel<float>
-        <<<dim3((unsigned)((max_kv + kSimt - 1) / kSimt), B), kSimtThreads, 0, s>>>(a, ma);
-    return cudaGetLastError();
-  }
-  if (p.kind < 3)
-    return p.kind == 1 ? launch_small<1>(a, ma, p.chunk, s) : launch_small<2>(a, ma, p.chunk, s);
   float *const partial = (float *)((char *)ws + kTcStatusBytes);
-  const int smem = (int)sizeof(MassTcSmem) + 1024;
-  cudaError_t e =
-      cudaFuncSetAttribute(mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = (max_kv + kMBlock - 1) / kMBlock;
-  mass_tc_kernel<<<dim3((unsigned)(blocks * p.parts), B), kMThreads, smem, s>>>(
-      a, ma, p.parts, partial, (uint32_t *)ws);
+  cudaError_t e;
+  if (p.kind == 1 || p.kind == 2)
+    return p.kind == 1 ? launch_small<1>(a, ma, p.chunk, s) : launch_small<2>(a, ma, p.chunk, s);
+  if (p.kind == 0) {
+    const int smem = (int)sizeof(MassF32Smem);
+    e = cudaFuncSetAttribute(mass_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (max_kv + kFKeys - 1) / kFKeys;
+    mass_f32_kernel<<<dim3((unsigned)(blocks * p.parts), B), kFThreads, smem, s>>>(a, ma, p.parts, partial);
+  } else {
+    const int smem = (int)sizeof(MassTcSmem) + 1024;
+    e = cudaFuncSetAttribute(mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (max_kv + kMBlock - 1) / kMBlock;
+    mass_tc_kernel<<<dim3((unsigned)(blocks * p.parts), B), kMThreads, smem, s>>>(a, ma, p.parts, partial,
+                                                                               (uint32_t *)ws);
+  }
   e = cudaGetLastError();
   if (e != cudaSuccess || p.parts == 1) return e;
   mass_join_kernel<<<dim3((unsigned)((max_kv + 255) / 256), B), 256, 0, s>>>(a, ma, p.parts, partial);
