@@ -222,7 +222,7 @@ cudaError_t launch_qk_norm_append(int dtype, int Hq, int Hkv, int n, const void 
                                   const int32_t *pos, const int32_t *slot, int S, void *q_out,
                                   void *kp, void *vp, const RopeTheta &th, cudaStream_t s);
 // CTAs along the first grid axis of the chunk attention (its limit is 2^31 - 1)
-int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv);
+int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv);
 size_t chunk_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv);
 cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                          const int32_t *q_indptr, int max_q, const void *q, const void *k,

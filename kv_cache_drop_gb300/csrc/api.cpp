@@ -1358,7 +1358,7 @@ akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t 
     return fail(AKV_ERR_INVALID, "NULL argument");
   if (misaligned(q) || misaligned(k_pool) || misaligned(v_pool) || misaligned(out))
     return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
-  if (chunk_grid_x(shape->dtype, B, shape->Hq, shape->Hkv, max_q, max_kv) > INT32_MAX ||
+  if (chunk_grid_x(shape->dtype, B, shape->Hq, shape->Hkv, n_rows, max_q, max_kv) > INT32_MAX ||
       (int64_t)n_rows * shape->Hq > INT32_MAX)
     return fail(AKV_ERR_UNSUPPORTED, "chunk attention: %d rows of %d heads exceed a grid", max_q,
                 shape->Hq);

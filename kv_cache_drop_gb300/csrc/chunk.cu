@@ -581,9 +581,18 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
 constexpr int kBarP = 3;         // hardware barriers kBarP + i (0 is __syncthreads)
 constexpr float kRescale = 8.f;  // log2 units
 
-constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 6; }
-constexpr int tc_producers(int tiles) { return tiles == 1 ? 1 : 3; }
-constexpr int tc_threads(int tiles) { return 128 * tiles + 32 * tc_producers(tiles) + 32; }
+constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 5; }
+// Warps: the softmax groups (a warpgroup each), then the producers and the MMA
+// warp.  A softmax thread holds a row of 128 scores, so registers move from
+// the other warpgroups to these (setmaxnreg): with one tile 128 x 200 + 128 x
+// 56 = 256 x 128 launched, two CTAs per SM; with two tiles twice that, one CTA.
+// A warp's copies in flight are few (about 4 bytes per clock and warp), so all
+// warps that are left over are producers, and every warp takes part in the
+// first windows' copies.
+constexpr int tc_producers(int tiles) { return tiles == 1 ? 3 : 7; }
+constexpr int tc_threads(int tiles) { return 256 * tiles; }
+constexpr int kTcLaunchRegs = 128, kSoftmaxRegs = 200, kOtherRegs = 56;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * kTcLaunchRegs, "the shares add up to the launch's");
 
 template <int kTiles>
 struct __align__(1024) TcSmem {
@@ -599,7 +608,7 @@ template <int kTiles>
 __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     chunk_tc_kernel(const ChunkBatch a, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
                     const ChunkParts part, uint32_t *status) {
-  constexpr int kSt = tc_stages(kTiles);
+  constexpr int kSt = tc_stages(kTiles), kFill = kTiles;
   constexpr int kProducers = tc_producers(kTiles);
   constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + kProducers;
   // a softmax group, the producers, the MMA warp
@@ -612,8 +621,9 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the last row tiles see the most: they come first
   const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
-  const int64_t r0 = (int64_t)(blockIdx.x / part.ns) * (kTiles * kTcRows);
+  const int64_t r0 = (int64_t)(gridDim.x / part.ns - 1 - blockIdx.x / part.ns) * (kTiles * kTcRows);
   const ChunkReq rq = chunk_req(a, b);
   const int grp = a.Hq / a.Hkv;
   const int64_t rows = (int64_t)rq.m * grp;
@@ -625,6 +635,37 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   const int n_win = c1 > c0 ? (c1 - c0 + kTcKeys - 1) / kTcKeys : 0;
   // first window with an entry hidden from a row of this CTA (or past c1)
   const int w_ragged = max(0, min(rq.limit((int)(r0 / grp)), c1) - c0) / kTcKeys;
+
+  // Windows 0 .. kFill - 1, by all warps: step u of the 32 kFill steps is
+  // entries 4 (u % 32) .. + 3 of window u / 32, eight lanes each.
+  constexpr int kWarps = tc_threads(kTiles) / 32, kFillSteps = 32 * kFill / kWarps;
+  const int64_t pitch = (int64_t)a.Hkv * kD * 2;
+  const int ch = lane & 7;
+  const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
+  const char *vg = (const char *)a.v + (g * kD + ch * 8) * 2;
+  {
+    int fill[kFillSteps];
+#pragma unroll
+    for (int e = 0; e < kFillSteps; ++e) {
+      const int j = c0 + 4 * (warp * kFillSteps + e) + (lane >> 3);
+      fill[e] = j < c1 ? (int)chunk_slot(a, rq, j) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < kFillSteps; ++e) {
+      const int x = 4 * (warp * kFillSteps + e) + (lane >> 3);  // row of the windows, one after the other
+      const uint32_t to = x * 128 + ((ch ^ (x & 7)) << 4);
+      const int64_t off = max(fill[e], 0) * pitch;
+      cp_async16(ptx::smem_addr(sm.k[0]) + to, kg + off, fill[e] >= 0);  // past the end: zeros
+      cp_async16(ptx::smem_addr(sm.v[0]) + to, vg + off, fill[e] >= 0);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  }
+  // this warp's copies of those windows, before its first barrier
+  auto filled = [] {
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+  };
 
   // this thread's packed row
   const int i = warp >> 2;
@@ -661,282 +702,293 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       atomicOr(status, kStatusWaitTimeout);
   };
 
-  if (warp >= kProdWarp && warp < kMmaWarp) {
-    // A window is 128 rows of K and of V, 16 bytes per lane and copy: step s
-    // copies entries 4 s .. 4 s + 3, eight lanes each, and producer warp p
-    // takes steps kSteps p .. of every window (one warp per sub-partition, so
-    // that no softmax warp shares its issue slots with all of them: +x %).
-    // A lane's pool rows are loaded a window ahead.  A stage is refilled
-    // without a wait: generation n + 1 of the last tile's barrier completes
-    // only after its softmax has seen S(n), whose commit tracks P.V(n - 1),
-    // the last reader of that stage.  Each window is one group of copies
-    // (empty past the end), so that "window n + 1 has landed" is a count of
-    // groups still in flight.
-    constexpr int kSteps = (32 + kProducers - 1) / kProducers;
-    const int s0 = (warp - kProdWarp) * kSteps;
-    const int key0 = 4 * s0 + (lane >> 3), ch = lane & 7;
-    const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kTcTileBytes;
-    const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
-    const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
-    const char *vg = (const char *)a.v + (g * kD + ch * 8) * 2;
-    const int64_t pitch = (int64_t)a.Hkv * kD * 2;
-    int nx[kSteps];
-    auto slots = [&](int n) {
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int j = c0 + n * kTcKeys + key0 + 4 * s;
-        nx[s] = s0 + s < 32 && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
-      }
-    };
-    auto load = [&](int n) {  // window n from the indices at hand, then those of n + 1
-      int cur[kSteps];
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
-      slots(n + 1);
-      if (n < n_win) {
-        const uint32_t at = (n % kSt) * kTcTileBytes;
+  if (warp >= kProdWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp < kMmaWarp) {
+      // A window is 128 rows of K and of V, 16 bytes per lane and copy: step s
+      // copies entries 4 s .. 4 s + 3, eight lanes each, and producer warp p
+      // takes steps kSteps p .. of every window.  A lane's pool rows are loaded
+      // a window ahead.  A stage is refilled without a wait: generation n + 1 of
+      // the last tile's barrier completes only after its softmax has seen S(n),
+      // whose commit tracks P.V(n - 1), the last reader of that stage.  Each
+      // window is one group of copies (empty past the end), so that "window
+      // n + 1 has landed" is a count of groups still in flight.
+      constexpr int kSteps = (32 + kProducers - 1) / kProducers;
+      const int s0 = (warp - kProdWarp) * kSteps, key0 = 4 * s0 + (lane >> 3);
+      const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kTcTileBytes;
+      const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
+      int nx[kSteps];
+      auto slots = [&](int n, int *row) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          if (s0 + s < 32) {
-            const int64_t off = max(cur[s], 0) * pitch;
-            const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
-            cp_async16(kd + to, kg + off, cur[s] >= 0);  // past the end: zeros
-            cp_async16(vd + to, vg + off, cur[s] >= 0);
+          const int j = c0 + n * kTcKeys + key0 + 4 * s;
+          row[s] = s0 + s < 32 && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
+        }
+      };
+      auto copy = [&](int n, const int *row) {
+        if (n < n_win) {
+          const uint32_t at = (n % kSt) * kTcTileBytes;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            if (s0 + s < 32) {
+              const int64_t off = max(row[s], 0) * pitch;
+              const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
+              cp_async16(kd + to, kg + off, row[s] >= 0);
+              cp_async16(vd + to, vg + off, row[s] >= 0);
+            }
           }
         }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+      };
+      // every window but the newest `pending` has landed and is visible to the
+      // tensor core
+      auto landed = [&](auto pending) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(decltype(pending)::value) : "memory");
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      };
+      {
+        int first[kSt - kFill][kSteps];
+#pragma unroll
+        for (int n = kFill; n < kSt; ++n) slots(n, first[n - kFill]);
+#pragma unroll
+        for (int n = kFill; n < kSt; ++n) copy(n, first[n - kFill]);
       }
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
-    };
-    // every window but the newest `pending` has landed and is visible to the
-    // tensor core
-    auto landed = [&](auto pending) {
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(decltype(pending)::value) : "memory");
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-    };
-    slots(0);
-    for (int n = 0; n < kSt; ++n) load(n);
-    landed(std::integral_constant<int, kSt - 1>());
-    ptx::named_bar_sync(kBarP, kBarPCount);
-    if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-    for (int n = 0; n < n_win; ++n) {
-      landed(std::integral_constant<int, kSt - 3>());  // window n + 1
+      slots(kSt, nx);
+      landed(std::integral_constant<int, kSt - kFill>());  // windows 0 .. kFill - 1
       ptx::named_bar_sync(kBarP, kBarPCount);
       if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-      if (n >= 1) load(n - 1 + kSt);
-    }
-    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-  } else if (warp == kMmaWarp) {
-    constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
-    constexpr uint32_t idO = ptx::idesc_bf16(128, 64, true);
-    constexpr uint64_t kTileStep = kTcTileBytes >> 4;
-    const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0]));
-    const uint64_t dv = ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]));
-    const bool leader = lane == 0;
-    auto issue_s = [&](int t, int st) {
-      if (!leader) return;
+      for (int n = 0; n < n_win; ++n) {
+        if (n + 1 >= kFill) landed(std::integral_constant<int, kSt - 3>());  // window n + 1
+        ptx::named_bar_sync(kBarP, kBarPCount);
+        if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+        if (n >= 1) {
+          int cur[kSteps];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        ptx::mma_f16_ts(tmem + 128 * t, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk,
-                        idS, kk > 0);
-      ptx::mma_commit(&sm.bar_s[t]);
-    };
-    auto issue_o = [&](int t, int st, bool acc) {
-      if (!leader) return;
+          for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
+          slots(n + kSt, nx);
+          copy(n - 1 + kSt, cur);
+        }
+      }
+      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    } else {
+      constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
+      constexpr uint32_t idO = ptx::idesc_bf16(128, 64, true);
+      constexpr uint64_t kTileStep = kTcTileBytes >> 4;
+      const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0]));
+      const uint64_t dv = ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]));
+      const bool leader = lane == 0;
+      filled();
+      auto issue_s = [&](int t, int st) {
+        if (!leader) return;
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        ptx::mma_f16_ts(tmem + kColO + 64 * t, tmem + 128 * t + 8 * kk, dv + st * kTileStep + 128 * kk,
-                        idO, (acc || kk > 0) ? 1u : 0u);
-    };
-    ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
-    if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-    ptx::tc_fence_after();
-    if (n_win > 0) {
-      issue_s(0, 0);
-      if (two) issue_s(1, 0);
-    }
-    for (int n = 0; n < n_win; ++n) {
-      const int st = n % kSt, st1 = (n + 1) % kSt;
-      ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
+        for (int kk = 0; kk < 4; ++kk)
+          ptx::mma_f16_ts(tmem + 128 * t, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk,
+                          idS, kk > 0);
+        ptx::mma_commit(&sm.bar_s[t]);
+      };
+      auto issue_o = [&](int t, int st, bool acc) {
+        if (!leader) return;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_f16_ts(tmem + kColO + 64 * t, tmem + 128 * t + 8 * kk, dv + st * kTileStep + 128 * kk,
+                          idO, (acc || kk > 0) ? 1u : 0u);
+      };
+      ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
+      if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
       ptx::tc_fence_after();
-      issue_o(0, st, n > 0);
-      if (n + 1 < n_win) issue_s(0, st1);
-      if (kTiles == 2) {
-        ptx::named_bar_sync(kBarP + 1, kBarPCount);
+      if (n_win > 0) {
+        issue_s(0, 0);
+        if (two) issue_s(1, 0);
+      }
+      for (int n = 0; n < n_win; ++n) {
+        const int st = n % kSt, st1 = (n + 1) % kSt;
+        ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
         ptx::tc_fence_after();
-        if (two) {
-          issue_o(1, st, n > 0);
-          if (n + 1 < n_win) issue_s(1, st1);
-        }
-      }
-    }
-    if (leader) ptx::mma_commit(&sm.bar_done);
-    wait(&sm.bar_done, 0);
-  } else if (i == 1 && !two) {
-    // no row in this tile: only the barriers
-    for (int n = 0; n <= n_win; ++n) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-    wait(&sm.bar_done, 0);
-  } else {
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + 64 * i;
-    ptx::tmem_st32(tmem + lane_base + kColQ + 32 * i, qw);
-    ptx::tmem_wait_st();
-    ptx::tc_fence_before();
-    ptx::named_bar_sync(kBarP + i, kBarPCount);
-    const float2 scale2 = make_float2(kScale, kScale);
-    float m_run = -INFINITY;
-    // row sum: four chains, so that no addition waits for the one before
-    float2 l4[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
-    for (int n = 0; n < n_win; ++n) {
-      wait(&sm.bar_s[i], n & 1);
-      ptx::tc_fence_after();
-      uint32_t sr[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
-      ptx::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
-      if (n >= w_ragged) {
-        const int seen = min(lim, c1) - (c0 + n * kTcKeys);
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= seen) sr[c] = 0xff800000u;  // -inf
-      }
-      float mx8[8];
-#pragma unroll
-      for (int k8 = 0; k8 < 8; ++k8)
-        mx8[k8] = ptx::max3(__uint_as_float(sr[k8]), __uint_as_float(sr[8 + k8]),
-                            __uint_as_float(sr[16 + k8]));
-#pragma unroll
-      for (int c = 24; c + 16 <= 120; c += 16)
-#pragma unroll
-        for (int k8 = 0; k8 < 8; ++k8)
-          mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
-#pragma unroll
-      for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = fmaxf(mx8[k8], __uint_as_float(sr[120 + k8]));
-      const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
-                             fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-      const float m_new = fmaxf(m_run, mx * kScale);
-      const bool need = m_new > m_run + kRescale;
-      const bool any = __any_sync(0xffffffffu, need);
-      float alpha = 1.f;
-      if (need) {
-        alpha = ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
-        m_run = m_new;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          l4[k].x *= alpha;
-          l4[k].y *= alpha;
-        }
-      }
-      const float mref = m_run == -INFINITY ? 0.f : m_run;
-      const float2 neg2 = make_float2(-mref, -mref);
-      // weights in fp32 (summed as they are), rounded to bf16 pairs: word k
-      // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
-#pragma unroll
-      for (int qtr = 0; qtr < 4; ++qtr) {
-        uint32_t pw[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int c = 2 * (16 * qtr + k);
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                      scale2, neg2);
-          const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-          l4[k & 3] = __fadd2_rn(l4[k & 3], p);
-          pw[k] = pack2(p.x, p.y);
-        }
-        ptx::tmem_st16(tS + 16 * qtr, pw);
-      }
-      if (n > 0 && any) {
-        // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
-#pragma unroll
-        for (int hlf = 0; hlf < 2; ++hlf) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + 32 * hlf, o);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence32(o);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-          ptx::tmem_st32(tO + 32 * hlf, o);
-        }
-      }
-      if (n >= w_ragged) {
-        uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
-        for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
-          const uint4 x = v4[c];
-          const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
-                                     finite_or_zero(x.w));
-          if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-            *(volatile uint32_t *)&sm.odd = 1u;
-            __threadfence_block();
-            v4[c] = y;
+        issue_o(0, st, n > 0);
+        if (n + 1 < n_win) issue_s(0, st1);
+        if (kTiles == 2) {
+          ptx::named_bar_sync(kBarP + 1, kBarPCount);
+          ptx::tc_fence_after();
+          if (two) {
+            issue_o(1, st, n > 0);
+            if (n + 1 < n_win) issue_s(1, st1);
           }
         }
-        ptx::fence_proxy_async_smem();  // before the tensor core reads the window
       }
+      if (leader) ptx::mma_commit(&sm.bar_done);
+      wait(&sm.bar_done, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    if (i == 1 && !two) {
+      // no row in this tile: only the barriers
+      filled();
+      for (int n = 0; n <= n_win; ++n) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+      wait(&sm.bar_done, 0);
+    } else {
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + 64 * i;
+      ptx::tmem_st32(tmem + lane_base + kColQ + 32 * i, qw);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
+      filled();
       ptx::named_bar_sync(kBarP + i, kBarPCount);
-    }
-    wait(&sm.bar_done, 0);  // the last P.V
-    ptx::tc_fence_after();
-    uint32_t o[64];
-    if (n_win > 0) {
-      ptx::tmem_ld32(tO, o);
-      ptx::tmem_ld32(tO + 32, o + 32);
-      ptx::tmem_wait_ld();
-      ptx::reg_fence32(o);
-      ptx::reg_fence32(o + 32);
-    } else {
+      const float2 scale2 = make_float2(kScale, kScale);
+      float m_run = -INFINITY;
+      // row sum: four chains, so that no addition waits for the one before
+      float2 l4[4];
 #pragma unroll
-      for (int c = 0; c < 64; ++c) o[c] = 0u;
-    }
-    if (*(volatile uint32_t *)&sm.odd && valid) {
-      for (int j = c0 + w_ragged * kTcKeys; j < min(lim, c1); ++j) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            (const __nv_bfloat16 *)a.v + (chunk_slot(a, rq, j) * a.Hkv + g) * kD);
+      for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
+      for (int n = 0; n < n_win; ++n) {
+        wait(&sm.bar_s[i], n & 1);
+        ptx::tc_fence_after();
+        uint32_t sr[128];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 x = __ldg(src + c);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
+        ptx::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 8 * c + 2 * e;
-            if (nonfinite_lo(w[e]))
-              o[d] = __float_as_uint(__uint_as_float(o[d]) + __uint_as_float(w[e] << 16));
-            if (nonfinite_hi(w[e]))
-              o[d + 1] = __float_as_uint(__uint_as_float(o[d + 1]) + __uint_as_float(w[e] & 0xffff0000u));
+        for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+        if (n >= w_ragged) {
+          const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= seen) sr[c] = 0xff800000u;  // -inf
+        }
+        float mx8[8];
+#pragma unroll
+        for (int k8 = 0; k8 < 8; ++k8)
+          mx8[k8] = ptx::max3(__uint_as_float(sr[k8]), __uint_as_float(sr[8 + k8]),
+                              __uint_as_float(sr[16 + k8]));
+#pragma unroll
+        for (int c = 24; c + 16 <= 120; c += 16)
+#pragma unroll
+          for (int k8 = 0; k8 < 8; ++k8)
+            mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
+#pragma unroll
+        for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = fmaxf(mx8[k8], __uint_as_float(sr[120 + k8]));
+        const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
+                               fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const float m_new = fmaxf(m_run, mx * kScale);
+        const bool need = m_new > m_run + kRescale;
+        const bool any = __any_sync(0xffffffffu, need);
+        float alpha = 1.f;
+        if (need) {
+          alpha = ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
+          m_run = m_new;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            l4[k].x *= alpha;
+            l4[k].y *= alpha;
+          }
+        }
+        const float mref = m_run == -INFINITY ? 0.f : m_run;
+        const float2 neg2 = make_float2(-mref, -mref);
+        // weights in fp32 (summed as they are), rounded to bf16 pairs: word k
+        // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
+#pragma unroll
+        for (int qtr = 0; qtr < 4; ++qtr) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int c = 2 * (16 * qtr + k);
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                        scale2, neg2);
+            const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+            l4[k & 3] = __fadd2_rn(l4[k & 3], p);
+            pw[k] = pack2(p.x, p.y);
+          }
+          ptx::tmem_st16(tS + 16 * qtr, pw);
+        }
+        if (n > 0 && any) {
+          // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
+#pragma unroll
+          for (int hlf = 0; hlf < 2; ++hlf) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + 32 * hlf, o);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence32(o);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            ptx::tmem_st32(tO + 32 * hlf, o);
+          }
+        }
+        if (n >= w_ragged) {
+          uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
+          for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
+            const uint4 x = v4[c];
+            const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
+                                       finite_or_zero(x.w));
+            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+              *(volatile uint32_t *)&sm.odd = 1u;
+              __threadfence_block();
+              v4[c] = y;
+            }
+          }
+          ptx::fence_proxy_async_smem();  // before the tensor core reads the window
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::named_bar_sync(kBarP + i, kBarPCount);
+      }
+      wait(&sm.bar_done, 0);  // the last P.V
+      ptx::tc_fence_after();
+      uint32_t o[64];
+      if (n_win > 0) {
+        ptx::tmem_ld32(tO, o);
+        ptx::tmem_ld32(tO + 32, o + 32);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence32(o);
+        ptx::reg_fence32(o + 32);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) o[c] = 0u;
+      }
+      if (*(volatile uint32_t *)&sm.odd && valid) {
+        for (int j = c0 + w_ragged * kTcKeys; j < min(lim, c1); ++j) {
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              (const __nv_bfloat16 *)a.v + (chunk_slot(a, rq, j) * a.Hkv + g) * kD);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = __ldg(src + c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int d = 8 * c + 2 * e;
+              if (nonfinite_lo(w[e]))
+                o[d] = __float_as_uint(__uint_as_float(o[d]) + __uint_as_float(w[e] << 16));
+              if (nonfinite_hi(w[e]))
+                o[d + 1] = __float_as_uint(__uint_as_float(o[d + 1]) + __uint_as_float(w[e] & 0xffff0000u));
+            }
           }
         }
       }
-    }
-    const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
-    const float l = la.x + la.y;
-    const bool direct = part.direct(lim);
-    if (valid && direct && split == 0) {
-      const bool none = lim == 0;
-      const float inv = none ? 0.f : 1.f / l;
-      uint4 *dst = reinterpret_cast<uint4 *>(out + row * kD);
+      const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+      const float l = la.x + la.y;
+      const bool direct = part.direct(lim);
+      if (valid && direct && split == 0) {
+        const bool none = lim == 0;
+        const float inv = none ? 0.f : 1.f / l;
+        uint4 *dst = reinterpret_cast<uint4 *>(out + row * kD);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t w4[4];
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w4[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w4[e] = none ? 0u : pack2(__uint_as_float(o[8 * c + 2 * e]) * inv,
-                                    __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
-        dst[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          for (int e = 0; e < 4; ++e)
+            w4[e] = none ? 0u : pack2(__uint_as_float(o[8 * c + 2 * e]) * inv,
+                                      __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+          dst[c] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        if (lse) lse[row] = none ? -INFINITY : m_run * kLn2 + logf(l);
+      } else if (valid && !direct) {
+        const int64_t pi = row * part.ns + split;
+        float4 *dst = reinterpret_cast<float4 *>(part.o + pi * kD);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+        part.ml[pi] = make_float2(m_run, l);
       }
-      if (lse) lse[row] = none ? -INFINITY : m_run * kLn2 + logf(l);
-    } else if (valid && !direct) {
-      const int64_t pi = row * part.ns + split;
-      float4 *dst = reinterpret_cast<float4 *>(part.o + pi * kD);
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                             __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-      part.ml[pi] = make_float2(m_run, l);
     }
   }
   ptx::tc_fence_before();
@@ -976,7 +1028,32 @@ void split_keys(ChunkPlan *p, int64_t ctas, int64_t want, int64_t resident, int 
   p->ns = (int)splits(c);
 }
 
-ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
+// Key splits of the tcgen05 kernels, from what their CTAs measured: `window`
+// us for 128 keys beside its neighbours, 6 us to start and end, and the
+// partials written and read at 5 TB/s.  The count that ends first when every
+// list is max_kv long: the splits then fill whole waves of CTAs (448 CTAs of
+// 196 windows instead of 896 of 128 and fewer: 1,078 -> @@ us for 14 chunks of
+// 64 over 50,000 entries).
+void split_windows(ChunkPlan *p, int64_t ctas, int64_t slots, double window, double row_bytes,
+                   int max_kv) {
+  const int windows = std::max(1, (max_kv + kTcKeys - 1) / kTcKeys);
+  const int most = std::min(kMaxSplit, std::max(1, windows / 4));
+  double best = 0;
+  p->ns = 1;
+  for (int ns = 1; ns <= most; ++ns) {
+    const int per = (windows + ns - 1) / ns;
+    if (ns > 1 && per * (ns - 1) >= windows) continue;  // a split would be empty
+    const double t = (double)((ctas * ns + slots - 1) / slots) * (per * window + 6) +
+                     (ns > 1 ? 4 + ns * row_bytes / 5e6 : 0);
+    if (ns == 1 || t < best) {
+      best = t;
+      p->ns = ns;
+    }
+  }
+  p->chunk = (windows + p->ns - 1) / p->ns * kTcKeys;
+}
+
+ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
   ChunkPlan p;
   const int sms = chunk_sms();
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
@@ -990,8 +1067,8 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
     p.kind = rows <= kTcRows ? kTcKind : kTcKind + 1;
     const int per_sm = p.kind == kTcKind ? 2 : 1, tile = p.kind == kTcKind ? kTcRows : 2 * kTcRows;
     p.tiles = (rows + tile - 1) / tile;
-    split_keys(&p, p.tiles * B * Hkv, 4LL * per_sm * sms, (int64_t)per_sm * sms, max_kv, 16384, 2048,
-               512);
+    split_windows(&p, p.tiles * B * Hkv, (int64_t)per_sm * sms, p.kind == kTcKind ? 2.0 : 1.44,
+                  (double)n_rows * Hq * 528, max_kv);
   } else {
     p.kind = kF32Kind;
     p.tiles = (rows + kFRows - 1) / kFRows;
@@ -1028,6 +1105,14 @@ cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const Chunk
 template <int kTiles>
 cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                       int64_t tiles, uint32_t *status, cudaStream_t s) {
+  // the register shares hold for the launch's 128 only: an inc beyond them
+  // would wait forever
+  static const bool regs_ok = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, chunk_tc_kernel<kTiles>) == cudaSuccess &&
+           at.numRegs == kTcLaunchRegs;
+  }();
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
   const int smem = (int)sizeof(TcSmem<kTiles>) + 1024;
   cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<kTiles>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1057,13 +1142,13 @@ cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const Chunk
 
 }  // namespace
 
-int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
-  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
+int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
+  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
   return p.tiles * p.ns;
 }
 
 size_t chunk_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
-  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
+  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
   if (p.ns == 1) return kTcStatusBytes;
   const size_t parts = (size_t)n_rows * Hq * p.ns;
   return kTcStatusBytes + up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
@@ -1073,7 +1158,7 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                          const int32_t *q_indptr, int max_q, const void *q, const void *k,
                          const void *v, const int32_t *kv_indptr, const int32_t *kv_indices,
                          int max_kv, void *out, float *lse, void *ws, cudaStream_t s) {
-  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, max_q, max_kv);
+  const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
   const ChunkBatch a{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q, k, v};
   char *const w = (char *)ws + kTcStatusBytes;
   const ChunkParts part{(float2 *)w, (float *)(w + up256((size_t)n_rows * Hq * p.ns * sizeof(float2))),

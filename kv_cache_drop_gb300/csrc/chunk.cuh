@@ -134,13 +134,16 @@ __device__ __forceinline__ void f32_load_q(float (*dst)[kFPitch], const ChunkBat
 __device__ __forceinline__ void f32_load_kv(float (*dst)[kFPitch], const void *pool,
                                             const ChunkBatch &a, const ChunkReq &rq, int g, int j0,
                                             int end) {
-  const int c = threadIdx.x % 16;
+  const int c = threadIdx.x % 16, x0 = threadIdx.x / 16;
+  constexpr int kStep = kFThreads / 16;
+  int64_t row[kFKeys / kStep];  // all indices before the first copy
 #pragma unroll
-  for (int x = threadIdx.x / 16; x < kFKeys; x += kFThreads / 16) {
-    const bool ok = j0 + x < end;
-    const int64_t row = ok ? chunk_slot(a, rq, j0 + x) : 0;
-    cp_async16(ptx::smem_addr(&dst[x][4 * c]), (const float *)pool + (row * a.Hkv + g) * kD + 4 * c, ok);
-  }
+  for (int e = 0; e < kFKeys / kStep; ++e)
+    row[e] = j0 + x0 + e * kStep < end ? chunk_slot(a, rq, j0 + x0 + e * kStep) : -1;
+#pragma unroll
+  for (int e = 0; e < kFKeys / kStep; ++e)
+    cp_async16(ptx::smem_addr(&dst[x0 + e * kStep][4 * c]),
+               (const float *)pool + (max(row[e], (int64_t)0) * a.Hkv + g) * kD + 4 * c, row[e] >= 0);
 }
 
 // acc[p][q] = q row . k row

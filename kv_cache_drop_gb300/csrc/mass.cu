@@ -396,6 +396,15 @@ __global__ void __launch_bounds__(kMThreads, 1)
       }
       wait(bar, parity);
     };
+    // pool rows of the block's entries, the same for every head
+    int slot[2][kKSteps];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < kKSteps; ++s) {
+        const int j = j0 + i * kTcKeys + krow + 4 * s;
+        slot[i][s] = ks0 + s < kTcKeys / 4 && j < rq.n ? (int)chunk_slot(a, rq, j) : -1;
+      }
     // lse of rows x = 4 qs0 + lane + 32 u of a tile, loaded an item ahead
     constexpr int kLse = (4 * kQSteps + 31) / 32;
     float lse_nx[kLse];
@@ -423,12 +432,9 @@ __global__ void __launch_bounds__(kMThreads, 1)
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int s = 0; s < kKSteps; ++s)
-            if (ks0 + s < kTcKeys / 4) {
-              const int j = j0 + i * kTcKeys + krow + 4 * s;
-              const bool ok = j < rq.n;
-              const int64_t at = ok ? chunk_slot(a, rq, j) * pitch : 0;
-              cp_async16(kd + (kb * 2 + i) * kTcTileBytes + s * 512 + (s & 1 ? ksw1 : ksw0), kg + at, ok);
-            }
+            if (ks0 + s < kTcKeys / 4)
+              cp_async16(kd + (kb * 2 + i) * kTcTileBytes + s * 512 + (s & 1 ? ksw1 : ksw0),
+                         kg + max(slot[i][s], 0) * pitch, slot[i][s] >= 0);
         landed(&sm.k_full[kb]);
         ++kn;
       }
