@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 
 // ---------------------------------------------------------------------------
-// bf16, few rows (decode steps, short verification chunks): up to 16 kRT
+// bf16, few rows (decode steps, short verification chunks): up to 16
 // packed rows per KV head.  CTA = key split x request, a warp per KV head (up
 // to eight heads a CTA), so that a key's heads are read together.  Keys and
 // values are gathered 16 rows at a time by 16-byte cp.async into an
@@ -316,12 +316,11 @@ __global__ void __launch_bounds__(kMergeThreads)
 // registers for P V.  Bound by the gather from HBM; tcgen05 would spend a
 // 128-row tile on 8 rows.
 // ---------------------------------------------------------------------------
-constexpr int small_stages(int rt) { return rt == 1 ? 3 : 6; }
+constexpr int kSSt = 3;  // K and V tiles per warp
 
-template <int kRT>
-__global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kSHeads * 32, 2)
     chunk_small_kernel(const ChunkBatch a, __nv_bfloat16 *out, float *lse, const ChunkParts part) {
-  constexpr int kSt = small_stages(kRT);
+  constexpr int kSt = kSSt;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -367,34 +366,29 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
   }
 
   // Q fragments and the rows' limits (relative to c0)
-  uint32_t qa[kRT][4][4];
-  int lim[kRT][2], lim_min = INT32_MAX;
-#pragma unroll
-  for (int rt = 0; rt < kRT; ++rt)
+  uint32_t qa[4][4];
+  int lim[2];
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      const int r = rt * 16 + gid + 8 * hh;
+      const int r = gid + 8 * hh;
       const bool ok = r < rows;
       const uint32_t *src = reinterpret_cast<const uint32_t *>(
           (const __nv_bfloat16 *)a.q +
           ((int64_t)(rq.q0 + (ok ? r / grp : 0)) * a.Hq + g * grp + (ok ? r % grp : 0)) * kD);
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        qa[rt][ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
-        qa[rt][ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
+        qa[ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
+        qa[ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
       }
-      lim[rt][hh] = (ok ? rq.limit(r / grp) : 0) - c0;
+      lim[hh] = (ok ? rq.limit(r / grp) : 0) - c0;
     }
-  lim_min = rq.limit(0) - c0;  // the first token sees the least
+  const int lim_min = rq.limit(0) - c0;  // the first token sees the least
 
-  float o[kRT][8][4], m[kRT][2], l[kRT][2];
+  float o[8][4], m[2], l[2];
 #pragma unroll
-  for (int rt = 0; rt < kRT; ++rt) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
-    m[rt][0] = m[rt][1] = -INFINITY;
-    l[rt][0] = l[rt][1] = 0.f;
-  }
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  m[0] = m[1] = -INFINITY;
+  l[0] = l[1] = 0.f;
 
   for (int it = 0; it < n_tiles; ++it) {
     const int sl = slot_nx;
@@ -405,67 +399,57 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
     const uint32_t kt = wsm + (it % kSt) * 2 * kSTile, vt = kt + kSTile;
     const int k0 = it * kSKeys;
     const bool ragged = k0 + kSKeys > min(lim_min, nk);
-    float s[kRT][2][4];
+    float s[2][4];
 #pragma unroll
-    for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
-      for (int nb = 0; nb < 2; ++nb) s[rt][nb][0] = s[rt][nb][1] = s[rt][nb][2] = s[rt][nb][3] = 0.f;
+      for (int nb = 0; nb < 2; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t kb[4];
       const int mi = lane >> 3;
       ldsm4(kt + tile_at((mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), kb);
-#pragma unroll
-      for (int rt = 0; rt < kRT; ++rt) {
-        mma16816(s[rt][0], qa[rt][ks], kb[0], kb[1]);
-        mma16816(s[rt][1], qa[rt][ks], kb[2], kb[3]);
-      }
+      mma16816(s[0], qa[ks], kb[0], kb[1]);
+      mma16816(s[1], qa[ks], kb[2], kb[3]);
     }
     if (ragged) {
-#pragma unroll
-      for (int rt = 0; rt < kRT; ++rt)
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (k0 + nb * 8 + 2 * tig + (e & 1) >= min(lim[rt][e >> 1], nk)) s[rt][nb][e] = -INFINITY;
+            if (k0 + nb * 8 + 2 * tig + (e & 1) >= min(lim[e >> 1], nk)) s[nb][e] = -INFINITY;
     }
-    uint32_t pa[kRT][4];
+    uint32_t pa[4];
+    float alpha[2], ref[2];
 #pragma unroll
-    for (int rt = 0; rt < kRT; ++rt) {
-      float alpha[2], ref[2];
+    for (int hh = 0; hh < 2; ++hh) {
+      float mx = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]),
+                       fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[hh], mx * kScale);
+      ref[hh] = mn == -INFINITY ? 0.f : mn;
+      alpha[hh] = ptx::ex2(m[hh] - ref[hh]);
+      m[hh] = mn;
+      l[hh] *= alpha[hh];
+    }
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float mx = fmaxf(fmaxf(s[rt][0][2 * hh], s[rt][0][2 * hh + 1]),
-                         fmaxf(s[rt][1][2 * hh], s[rt][1][2 * hh + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[rt][hh], mx * kScale);
-        ref[hh] = mn == -INFINITY ? 0.f : mn;
-        alpha[hh] = ptx::ex2(m[rt][hh] - ref[hh]);
-        m[rt][hh] = mn;
-        l[rt][hh] *= alpha[hh];
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[nb][e] = ptx::ex2(fmaf(s[nb][e], kScale, -ref[e >> 1]));
+        l[e >> 1] += s[nb][e];
       }
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[rt][nb][e] = ptx::ex2(fmaf(s[rt][nb][e], kScale, -ref[e >> 1]));
-          l[rt][e >> 1] += s[rt][nb][e];
-        }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[rt][i][0] *= alpha[0];
-        o[rt][i][1] *= alpha[0];
-        o[rt][i][2] *= alpha[1];
-        o[rt][i][3] *= alpha[1];
-      }
-      // weights rounded to bf16 for the product; their sum l is not
-      pa[rt][0] = pack2(s[rt][0][0], s[rt][0][1]);
-      pa[rt][1] = pack2(s[rt][0][2], s[rt][0][3]);
-      pa[rt][2] = pack2(s[rt][1][0], s[rt][1][1]);
-      pa[rt][3] = pack2(s[rt][1][2], s[rt][1][3]);
+    for (int i = 0; i < 8; ++i) {
+      o[i][0] *= alpha[0];
+      o[i][1] *= alpha[0];
+      o[i][2] *= alpha[1];
+      o[i][3] *= alpha[1];
     }
+    // weights rounded to bf16 for the product; their sum l is not
+    pa[0] = pack2(s[0][0], s[0][1]);
+    pa[1] = pack2(s[0][2], s[0][3]);
+    pa[2] = pack2(s[1][0], s[1][1]);
+    pa[3] = pack2(s[1][2], s[1][3]);
     if (ragged) {
       // An infinity or NaN in a hidden entry's value would reach every row
       // of the tile as 0 * inf: such values are added to the rows that see
@@ -486,12 +470,10 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
             const uint32_t w = *reinterpret_cast<const uint32_t *>(
                 reinterpret_cast<const uint8_t *>(vg) + tile_at(key, i) + 4 * tig);
 #pragma unroll
-            for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
               for (int hh = 0; hh < 2; ++hh)
-                if (k0 + key < min(lim[rt][hh], nk)) {
-                  if (nonfinite_lo(w)) o[rt][i][2 * hh] += __uint_as_float(w << 16);
-                  if (nonfinite_hi(w)) o[rt][i][2 * hh + 1] += __uint_as_float(w & 0xffff0000u);
+                if (k0 + key < min(lim[hh], nk)) {
+                  if (nonfinite_lo(w)) o[i][2 * hh] += __uint_as_float(w << 16);
+                  if (nonfinite_hi(w)) o[i][2 * hh + 1] += __uint_as_float(w & 0xffff0000u);
                 }
           }
         __syncwarp();
@@ -509,42 +491,37 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 2 : 1)
       const int mi = lane >> 3;
       uint32_t vb[4];
       ldsm4_t(vt + tile_at((mi & 1) * 8 + (lane & 7), nb2 * 2 + (mi >> 1)), vb);
-#pragma unroll
-      for (int rt = 0; rt < kRT; ++rt) {
-        mma16816(o[rt][2 * nb2], pa[rt], vb[0], vb[1]);
-        mma16816(o[rt][2 * nb2 + 1], pa[rt], vb[2], vb[3]);
-      }
+      mma16816(o[2 * nb2], pa, vb[0], vb[1]);
+      mma16816(o[2 * nb2 + 1], pa, vb[2], vb[3]);
     }
     __syncwarp();  // the tile's readers are done before it is refilled
   }
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 
 #pragma unroll
-  for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      float x = l[rt][hh];
+      float x = l[hh];
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
-      const int r = rt * 16 + gid + 8 * hh;
+      const int r = gid + 8 * hh;
       if (r >= rows) continue;
       const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
-      if (part.direct(lim[rt][hh] + c0)) {
+      if (part.direct(lim[hh] + c0)) {
         if (split > 0) continue;
-        const bool none = lim[rt][hh] <= 0;
+        const bool none = lim[hh] <= 0;
         const float inv = none ? 0.f : 1.f / x;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           reinterpret_cast<uint32_t *>(out + row * kD)[4 * i + tig] =
-              none ? 0u : pack2(o[rt][i][2 * hh] * inv, o[rt][i][2 * hh + 1] * inv);
-        if (lse && tig == 0) lse[row] = none ? -INFINITY : m[rt][hh] * kLn2 + logf(x);
+              none ? 0u : pack2(o[i][2 * hh] * inv, o[i][2 * hh + 1] * inv);
+        if (lse && tig == 0) lse[row] = none ? -INFINITY : m[hh] * kLn2 + logf(x);
       } else {
         const int64_t pi = row * part.ns + split;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           reinterpret_cast<float2 *>(part.o + pi * kD)[4 * i + tig] =
-              make_float2(o[rt][i][2 * hh], o[rt][i][2 * hh + 1]);
-        if (tig == 0) part.ml[pi] = make_float2(m[rt][hh], x);
+              make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+        if (tig == 0) part.ml[pi] = make_float2(m[hh], x);
       }
     }
 }
@@ -1003,12 +980,11 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
 // the host's bounds, so that a captured call replays for any lengths within
 // them.
 struct ChunkPlan {
-  int kind;       // 0 CUDA cores; 1, 2: mma.sync with that many 16-row tiles; 3, 4: tcgen05 with
-                  // one or two 128-row tiles
+  int kind;       // CUDA cores; mma.sync; tcgen05 with one or two (+ 1) 128-row tiles
   int ns, chunk;  // key splits and entries of each
   int64_t tiles;  // row tiles of one (request, KV head)
 };
-constexpr int kF32Kind = 0, kSmallKind = 1, kTcKind = 3;
+constexpr int kF32Kind = 0, kSmallKind = 1, kTcKind = 2;
 
 // Key splits: none if `ctas` (the unsplit grid) reaches `want`; otherwise
 // chunks of max_chunk entries halved until it does, but not below `least` --
@@ -1057,10 +1033,10 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, i
   ChunkPlan p;
   const int sms = chunk_sms();
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
-  if (dtype == AKV_BF16 && rows <= 32) {
-    p.kind = rows <= 16 ? kSmallKind : kSmallKind + 1;
+  if (dtype == AKV_BF16 && rows <= 16) {
+    p.kind = kSmallKind;
     p.tiles = 1;
-    const int warps = std::min(Hkv, kSHeads), per_sm = p.kind == kSmallKind ? 16 / warps : 8 / warps;
+    const int warps = std::min(Hkv, kSHeads), per_sm = 16 / warps;
     const int64_t ctas = (int64_t)B * ((Hkv + kSHeads - 1) / kSHeads);
     split_keys(&p, ctas, 8LL * per_sm * sms, (int64_t)per_sm * sms, max_kv, 4096, 1024, 128);
   } else if (dtype == AKV_BF16) {
@@ -1090,14 +1066,13 @@ cudaError_t launch_f32(const ChunkBatch &a, void *out, float *lse, const ChunkPa
   return cudaGetLastError();
 }
 
-template <int kRT>
 cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                          cudaStream_t s) {
-  const int warps = std::min(a.Hkv, kSHeads), smem = warps * small_stages(kRT) * 2 * kSTile;
-  cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel<kRT>,
+  const int warps = std::min(a.Hkv, kSHeads), smem = warps * kSSt * 2 * kSTile;
+  cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  chunk_small_kernel<kRT><<<dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads), warps * 32, smem, s>>>(
+  chunk_small_kernel<<<dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads), warps * 32, smem, s>>>(
       a, (__nv_bfloat16 *)out, lse, part);
   return cudaGetLastError();
 }
@@ -1166,8 +1141,7 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   cudaError_t e;
   if (p.kind == kTcKind) e = launch_tc<1>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
   else if (p.kind == kTcKind + 1) e = launch_tc<2>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
-  else if (p.kind == kSmallKind) e = launch_small<1>(a, out, lse, part, s);
-  else if (p.kind == kSmallKind + 1) e = launch_small<2>(a, out, lse, part, s);
+  else if (p.kind == kSmallKind) e = launch_small(a, out, lse, part, s);
   else e = launch_f32(a, out, lse, part, p.tiles, s);
   if (e != cudaSuccess || p.ns == 1) return e;
   return dtype == AKV_BF16 ? launch_merge<__nv_bfloat16>(a, out, lse, part, s)

@@ -21,6 +21,18 @@ struct MassArgs {
   int64_t stride;
 };
 
+// Running sum of the items' sums.  One fp32 chain over a long chunk's rows and
+// heads (some 10,000 terms) was off by 6e-6 of the mass; with the rounding of
+// each addition carried over (Kahan) it is an item's own few roundings.
+struct Total {
+  float sum = 0.f, lost = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float y = __fadd_rn(x, -lost), t = __fadd_rn(sum, y);
+    lost = __fadd_rn(__fadd_rn(t, -sum), -y);
+    sum = t;
+  }
+};
+
 // fp32, CUDA cores: CTA = 64 list entries x a share of the (KV head, 128-row
 // tile) items; the next item's rows are copied while one is computed.  Each
 // thread sums its four keys over its rows of every item, the 16 threads of a
@@ -63,7 +75,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
       sm.lse[buf][threadIdx.x] = v;
     }
   };
-  float sum[4] = {};
+  Total sum[4];
   if (mine) load_rows(0, g, t);
   for (int it = 0; it < mine; ++it) {
     const int r0 = t * kFRows, buf = it & 1;
@@ -81,6 +93,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
     f32_scores(sm.q[buf], sm.k, ty, tx, s);
     const int last = min(rq.n, j0 + kFKeys) - 1;  // sees the fewest rows
     const bool plain = r0 >= (int64_t)max(0, last - old) * grp && r0 + kFRows <= rows;
+    float x[4] = {};
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int r = r0 + ty + 16 * p;
@@ -89,13 +102,15 @@ __global__ void __launch_bounds__(kFThreads, 2)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float w = exp2f(fmaf(s[p][q], 0.125f, -v) * kLog2e);
-        sum[q] += j0 + tx + 16 * q < lim ? w : 0.f;
+        x[q] += j0 + tx + 16 * q < lim ? w : 0.f;
       }
     }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q].add(x[q]);
     __syncthreads();  // readers of this buffer and of K are done
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sm.red[ty][tx + 16 * q] = sum[q];
+  for (int q = 0; q < 4; ++q) sm.red[ty][tx + 16 * q] = sum[q].sum;
   __syncthreads();
   const int j = j0 + threadIdx.x;
   if (threadIdx.x < kFKeys && j < rq.n) {
@@ -123,10 +138,11 @@ __global__ void __launch_bounds__(kFThreads, 2)
 // of 40,000 entries, 64 / 8 heads: 256 / 3 / 4 102 us, 256 / 4 / 3 105,
 // 512 / 3 / 3 114, 128 / 4 / 3 112, 512 / 6 / 2 135, 256 / 6 / 2 142.
 constexpr int kMChunk = 256;
-constexpr int mass_stages(int rt) { return rt == 1 ? 3 : 6; }
+constexpr int mass_stages(int rt) { return rt == 1 ? 3 : rt == 2 ? 4 : 6; }
+constexpr int mass_ctas(int rt) { return rt == 1 ? 4 : rt == 2 ? 3 : 2; }
 
 template <int kRT>
-__global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
     mass_small_kernel(const ChunkBatch a, const MassArgs ma, int chunk) {
   constexpr int kMSt = mass_stages(kRT);
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -195,43 +211,38 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 4 : 2)
       __syncwarp();
       const uint32_t kt = wsm + (it % kMSt) * kSTile;
       const int k0 = it * kSKeys;
-      float s[kRT][2][4];
-#pragma unroll
-      for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-          s[rt][nb][0] = s[rt][nb][1] = s[rt][nb][2] = s[rt][nb][3] = 0.f;
+      uint32_t kb[4][4];
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t kb[4];
         const int mi = lane >> 3;
-        ldsm4(kt + tile_at((mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), kb);
-#pragma unroll
-        for (int rt = 0; rt < kRT; ++rt) {
-          mma16816(s[rt][0], qa[rt][ks], kb[0], kb[1]);
-          mma16816(s[rt][1], qa[rt][ks], kb[2], kb[3]);
-        }
+        ldsm4(kt + tile_at((mi >> 1) * 8 + (lane & 7), ks * 2 + (mi & 1)), kb[ks]);
       }
       // column sums: key 8 nb + 2 tig + e1
-      float cs[2][2];
+      float cs[2][2] = {};
+#pragma unroll
+      for (int rt = 0; rt < kRT; ++rt) {
+        float s[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          mma16816(s[0], qa[rt][ks], kb[ks][0], kb[ks][1]);
+          mma16816(s[1], qa[rt][ks], kb[ks][2], kb[ks][3]);
+        }
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int e1 = 0; e1 < 2; ++e1)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float p = ptx::ex2(fmaf(s[nb][2 * hh + e1], kScale, nl[rt][hh]));
+              cs[nb][e1] += k0 + nb * 8 + 2 * tig + e1 < lim[rt][hh] ? p : 0.f;
+            }
+      }
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-        for (int e1 = 0; e1 < 2; ++e1) {
-          const int key = k0 + nb * 8 + 2 * tig + e1;
-          float x = 0.f;
+        for (int e1 = 0; e1 < 2; ++e1)
 #pragma unroll
-          for (int rt = 0; rt < kRT; ++rt)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float p = ptx::ex2(fmaf(s[rt][nb][2 * hh + e1], kScale, nl[rt][hh]));
-              x += key < lim[rt][hh] ? p : 0.f;
-            }
-          x += __shfl_xor_sync(0xffffffffu, x, 4);
-          x += __shfl_xor_sync(0xffffffffu, x, 8);
-          x += __shfl_xor_sync(0xffffffffu, x, 16);
-          cs[nb][e1] = x;
-        }
+          for (int o = 4; o < 32; o <<= 1) cs[nb][e1] += __shfl_xor_sync(0xffffffffu, cs[nb][e1], o);
       if (gid < 2) {  // lanes of gid 0 and 1 write the two halves
         const int key = k0 + gid * 8 + 2 * tig;
         const float v0 = gid ? cs[1][0] : cs[0][0], v1 = gid ? cs[1][1] : cs[0][1];
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(kSHeads * 32, kRT == 1 ? 4 : 2)
 // fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kQRows = 2 * kTcRows;
-constexpr int kQSt = 4;
+constexpr int kQSt = 4, kKBuf = 2;
 constexpr int kNlSt = 8;
 static_assert(kNlSt >= kQSt + 2, "slots of the rows' lse");
 constexpr int kMProducers = 3;
@@ -281,16 +292,19 @@ constexpr int kKSteps = (kTcKeys / 4 + kMProducers - 1) / kMProducers;  // 4-row
 constexpr int kQSteps = (kQRows / 4 + kMProducers - 1) / kMProducers;
 constexpr int kMBlock = 2 * kTcKeys;
 constexpr int kMaxParts = 64;
-constexpr int kInFlight = 3;  // items whose copies are under way while the next is issued
+// Items whose copies are under way while the next is issued.  Measured with 2:
+// 1,634 us where 1 takes 1,627 (mass of 2 x 1,100-1,500 rows over 40k-56k
+// entries), 185 for 173 (14 x 256 rows over 20,000).
+constexpr int kInFlight = 1;
 
 struct __align__(1024) MassTcSmem {
-  uint8_t k[2][2][kTcTileBytes];  // [buffer][key tile]
+  uint8_t k[kKBuf][2][kTcTileBytes];  // [buffer][key tile]
   uint8_t q[kQSt][2 * kTcTileBytes];
   // -lse in log2 units of an item's rows.  Item x's slot was item x - kNlSt's:
   // the Q stage of x is free once the MMAs of x - kQSt are done, the last of
   // which began when the scores two halves earlier were in registers.
   float nl[kNlSt][kQRows];
-  uint64_t k_full[2], k_free[2], q_full[kQSt], q_free[kQSt];
+  uint64_t k_full[kKBuf], k_free[kKBuf], q_full[kQSt], q_free[kQSt];
   uint64_t s_full[2], s_free[2];  // per score buffer
   float join[kMBlock];            // sums of the odd halves
   uint32_t tmem_base;
@@ -333,9 +347,11 @@ __global__ void __launch_bounds__(kMThreads, 1)
   const int g0 = mine ? (int)(it0 / per_head) : 0, tile0 = mine ? t0 + (int)(it0 % per_head) : 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKBuf; ++s) {
       ptx::mbar_init(&sm.k_full[s], kMProducers);
       ptx::mbar_init(&sm.k_free[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&sm.s_full[s], 1);
       ptx::mbar_init(&sm.s_free[s], 4);
     }
@@ -425,8 +441,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
     if (mine) load_lse(g, t);
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the head's K tiles
-        const int kb = kn & 1;
-        if (kn >= 2) acquire(&sm.k_free[kb], ((kn >> 1) - 1) & 1);
+        const int kb = kn % kKBuf;
+        if (kn >= kKBuf) acquire(&sm.k_free[kb], (kn / kKBuf - 1) & 1);
         const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -488,8 +504,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
     int kn = 0, t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the next head
-        if (kn > 0 && lane == 0) ptx::mma_commit(&sm.k_free[(kn - 1) & 1]);
-        wait(&sm.k_full[kn & 1], (kn >> 1) & 1);
+        if (kn > 0 && lane == 0) ptx::mma_commit(&sm.k_free[(kn - 1) % kKBuf]);
+        wait(&sm.k_full[kn % kKBuf], (kn / kKBuf) & 1);
         ++kn;
       }
       const int halves = rows - t * kQRows > kTcRows ? 2 : 1;
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
         if (hseq >= 2) wait(&sm.s_free[buf], ((hseq >> 1) - 1) & 1);
         ptx::tc_fence_after();
         if (lane == 0) {
-          const uint64_t ak = dk + ((kn - 1) & 1) * 2 * kTileStep, bq = dq + (st * 2 + hf) * kTileStep;
+          const uint64_t ak = dk + ((kn - 1) % kKBuf) * 2 * kTileStep, bq = dq + (st * 2 + hf) * kTileStep;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -524,9 +540,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
     // the last listed key of the block sees the fewest rows
     const int64_t all_see = (int64_t)max(0, min(rq.n, j0 + kMBlock) - 1 - old) * grp;
     const float2 scale2 = make_float2(kScale, kScale);
-    float2 sum[2][2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) sum[e][0] = sum[e][1] = make_float2(0.f, 0.f);
+    Total total[2];
     constexpr int kStep = 16;
     int t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
@@ -538,6 +552,9 @@ __global__ void __launch_bounds__(kMThreads, 1)
       if (hf >= halves) continue;
       const int r0 = r_tile + hf * kTcRows;
       const float4 *nl4 = reinterpret_cast<const float4 *>(sm.nl[qn % kNlSt] + hf * kTcRows);
+      float2 sum[2][2];  // of this half: [key][pair of rows]
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sum[e][0] = sum[e][1] = make_float2(0.f, 0.f);
       wait(&sm.s_full[buf], (seq >> 1) & 1);
       ptx::tc_fence_after();
       auto give_back = [&] {  // all scores of the half are in registers
@@ -600,18 +617,22 @@ __global__ void __launch_bounds__(kMThreads, 1)
           }
         }
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 x = __fadd2_rn(sum[e][0], sum[e][1]);
+        total[e].add(x.x + x.y);
+      }
     }
-    const float2 a0 = __fadd2_rn(sum[0][0], sum[0][1]), a1 = __fadd2_rn(sum[1][0], sum[1][1]);
     if (buf == 1) {
-      sm.join[threadIdx.x & 127] = a0.x + a0.y;
-      sm.join[(threadIdx.x & 127) + 128] = a1.x + a1.y;
+      sm.join[threadIdx.x & 127] = total[0].sum;
+      sm.join[(threadIdx.x & 127) + 128] = total[1].sum;
     }
     ptx::named_bar_sync(1, 256);
     if (buf == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = key0 + 128 * e;
-        float x = (e ? a1.x + a1.y : a0.x + a0.y) + sm.join[key - j0];
+        float x = total[e].sum + sm.join[key - j0];
         if (key >= rq.n) continue;
         if (parts > 1) {
           partial[((int64_t)part * a.B + b) * a.max_kv + key] = x;
@@ -646,8 +667,8 @@ __global__ void __launch_bounds__(256)
 }
 
 struct MassPlan {
-  int kind;   // 0 CUDA cores; 1, 2: mma.sync with that many 16-row tiles; 3: tcgen05
-  int chunk;  // entries per CTA (kinds 1, 2)
+  int kind;   // 0 CUDA cores; 1, 2, 4: mma.sync with that many 16-row tiles; 3: tcgen05
+  int chunk;  // entries per CTA (kinds 1, 2, 4)
   int parts;  // CTAs per entry block (kinds 0, 3)
 };
 
@@ -655,8 +676,8 @@ MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
   MassPlan p{0, 0, 1};
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
   const int sms = chunk_sms();
-  if (dtype == AKV_BF16 && rows <= 32) {
-    p.kind = rows <= 16 ? 1 : 2;
+  if (dtype == AKV_BF16 && rows <= 64) {
+    p.kind = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.chunk = kMChunk;
     while (p.chunk > 64 && (int64_t)B * ((max_kv + p.chunk - 1) / p.chunk) < 2LL * sms) p.chunk /= 2;
     return p;
@@ -712,8 +733,9 @@ cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   const MassPlan p = mass_plan(dtype, B, Hq, Hkv, max_q, max_kv);
   float *const partial = (float *)((char *)ws + kTcStatusBytes);
   cudaError_t e;
-  if (p.kind == 1 || p.kind == 2)
-    return p.kind == 1 ? launch_small<1>(a, ma, p.chunk, s) : launch_small<2>(a, ma, p.chunk, s);
+  if (p.kind == 1) return launch_small<1>(a, ma, p.chunk, s);
+  if (p.kind == 2) return launch_small<2>(a, ma, p.chunk, s);
+  if (p.kind == 4) return launch_small<4>(a, ma, p.chunk, s);
   if (p.kind == 0) {
     const int smem = (int)sizeof(MassF32Smem);
     e = cudaFuncSetAttribute(mass_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
