@@ -594,14 +594,15 @@ def _run_on(stream):
     one; the library launches on the current device, so the stream's must be
     that one."""
     import torch
+    dev = torch.cuda.current_device()
     if stream is None:
-        s = torch.cuda.current_stream()
-    else:
-        s = stream
-        if s.device_index != torch.cuda.current_device():
-            raise ValueError(f"the stream is on cuda:{s.device_index}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-    return s.device_index, s.cuda_stream
+        # the raw handle without a Stream object: 2 us less of a 15 us call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return dev, raw(dev) if raw else torch.cuda.current_stream().cuda_stream
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is "
+                         f"cuda:{dev}")
+    return dev, stream.cuda_stream
 
 
 def _torch_dtype(shp: Shape):
@@ -619,18 +620,18 @@ def akv_qk_norm_append(shp: Shape, n: int, q, k, v, pos, slot, k_pool, v_pool, q
     padding rows."""
     import torch
     dev, st = _run_on(stream)
-    dt, D = _torch_dtype(shp), shp.D
-    args = [(_typed(x, t, dt, dev, (n, h, D), rows=True), t.stride(0) if n > 1 else h * D)
-            for x, t, h in (("q", q, shp.Hq), ("k", k, shp.Hkv), ("v", v, shp.Hkv))]
-    S = k_pool.shape[0]
+    dt, D, Hq, Hkv, f32, i32 = _torch_dtype(shp), shp.D, shp.Hq, shp.Hkv, torch.float32, torch.int32
+    rows, S = (n, Hkv, D), k_pool.shape[0]
+    pool = (S, Hkv, D)
     _check(lib().akv_qk_norm_append(
-        ctypes.byref(shp), n, *args[0], *args[1], *args[2],
-        _typed("q_weight", q_weight, torch.float32, dev, (D,)),
-        _typed("k_weight", k_weight, torch.float32, dev, (D,)), eps, flags,
-        _typed("pos", pos, torch.int32, dev, (n,)), _typed("slot", slot, torch.int32, dev, (n,)),
-        S, _typed("q_out", q_out, dt, dev, (n, shp.Hq, D)),
-        _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
-        _typed("v_pool", v_pool, dt, dev, (S, shp.Hkv, D)), st))
+        ctypes.byref(shp), n,
+        _typed("q", q, dt, dev, (n, Hq, D), True), q.stride(0) if n > 1 else Hq * D,
+        _typed("k", k, dt, dev, rows, True), k.stride(0) if n > 1 else Hkv * D,
+        _typed("v", v, dt, dev, rows, True), v.stride(0) if n > 1 else Hkv * D,
+        _typed("q_weight", q_weight, f32, dev, (D,)), _typed("k_weight", k_weight, f32, dev, (D,)),
+        eps, flags, _typed("pos", pos, i32, dev, (n,)), _typed("slot", slot, i32, dev, (n,)), S,
+        _typed("q_out", q_out, dt, dev, (n, Hq, D)), _typed("k_pool", k_pool, dt, dev, pool),
+        _typed("v_pool", v_pool, dt, dev, pool), st))
 
 
 def akv_chunk_workspace(shp: Shape, B: int, n_rows: int, max_q: int, max_kv: int) -> int:

@@ -369,19 +369,19 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   uint32_t qa[4][4];
   int lim[2];
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = gid + 8 * hh;
-      const bool ok = r < rows;
-      const uint32_t *src = reinterpret_cast<const uint32_t *>(
-          (const __nv_bfloat16 *)a.q +
-          ((int64_t)(rq.q0 + (ok ? r / grp : 0)) * a.Hq + g * grp + (ok ? r % grp : 0)) * kD);
+  for (int hh = 0; hh < 2; ++hh) {
+    const int r = gid + 8 * hh;
+    const bool ok = r < rows;
+    const uint32_t *src = reinterpret_cast<const uint32_t *>(
+        (const __nv_bfloat16 *)a.q +
+        ((int64_t)(rq.q0 + (ok ? r / grp : 0)) * a.Hq + g * grp + (ok ? r % grp : 0)) * kD);
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        qa[ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
-        qa[ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
-      }
-      lim[hh] = (ok ? rq.limit(r / grp) : 0) - c0;
+    for (int ks = 0; ks < 4; ++ks) {
+      qa[ks][hh] = ok ? __ldg(src + ks * 8 + tig) : 0u;
+      qa[ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
     }
+    lim[hh] = (ok ? rq.limit(r / grp) : 0) - c0;
+  }
   const int lim_min = rq.limit(0) - c0;  // the first token sees the least
 
   float o[8][4], m[2], l[2];
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
     const bool ragged = k0 + kSKeys > min(lim_min, nk);
     float s[2][4];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+    for (int nb = 0; nb < 2; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       uint32_t kb[4];
@@ -412,10 +412,10 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
     }
     if (ragged) {
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+      for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k0 + nb * 8 + 2 * tig + (e & 1) >= min(lim[e >> 1], nk)) s[nb][e] = -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (k0 + nb * 8 + 2 * tig + (e & 1) >= min(lim[e >> 1], nk)) s[nb][e] = -INFINITY;
     }
     uint32_t pa[4];
     float alpha[2], ref[2];
@@ -470,11 +470,11 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
             const uint32_t w = *reinterpret_cast<const uint32_t *>(
                 reinterpret_cast<const uint8_t *>(vg) + tile_at(key, i) + 4 * tig);
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-                if (k0 + key < min(lim[hh], nk)) {
-                  if (nonfinite_lo(w)) o[i][2 * hh] += __uint_as_float(w << 16);
-                  if (nonfinite_hi(w)) o[i][2 * hh + 1] += __uint_as_float(w & 0xffff0000u);
-                }
+            for (int hh = 0; hh < 2; ++hh)
+              if (k0 + key < min(lim[hh], nk)) {
+                if (nonfinite_lo(w)) o[i][2 * hh] += __uint_as_float(w << 16);
+                if (nonfinite_hi(w)) o[i][2 * hh + 1] += __uint_as_float(w & 0xffff0000u);
+              }
           }
         __syncwarp();
 #pragma unroll
@@ -499,31 +499,31 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      float x = l[hh];
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      const int r = gid + 8 * hh;
-      if (r >= rows) continue;
-      const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
-      if (part.direct(lim[hh] + c0)) {
-        if (split > 0) continue;
-        const bool none = lim[hh] <= 0;
-        const float inv = none ? 0.f : 1.f / x;
+  for (int hh = 0; hh < 2; ++hh) {
+    float x = l[hh];
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    const int r = gid + 8 * hh;
+    if (r >= rows) continue;
+    const int64_t row = (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp;
+    if (part.direct(lim[hh] + c0)) {
+      if (split > 0) continue;
+      const bool none = lim[hh] <= 0;
+      const float inv = none ? 0.f : 1.f / x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<uint32_t *>(out + row * kD)[4 * i + tig] =
-              none ? 0u : pack2(o[i][2 * hh] * inv, o[i][2 * hh + 1] * inv);
-        if (lse && tig == 0) lse[row] = none ? -INFINITY : m[hh] * kLn2 + logf(x);
-      } else {
-        const int64_t pi = row * part.ns + split;
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint32_t *>(out + row * kD)[4 * i + tig] =
+            none ? 0u : pack2(o[i][2 * hh] * inv, o[i][2 * hh + 1] * inv);
+      if (lse && tig == 0) lse[row] = none ? -INFINITY : m[hh] * kLn2 + logf(x);
+    } else {
+      const int64_t pi = row * part.ns + split;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<float2 *>(part.o + pi * kD)[4 * i + tig] =
-              make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
-        if (tig == 0) part.ml[pi] = make_float2(m[hh], x);
-      }
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<float2 *>(part.o + pi * kD)[4 * i + tig] =
+            make_float2(o[i][2 * hh], o[i][2 * hh + 1]);
+      if (tig == 0) part.ml[pi] = make_float2(m[hh], x);
     }
+  }
 }
 
 // ---------------------------------------------------------------------------

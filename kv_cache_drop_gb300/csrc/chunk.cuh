@@ -27,8 +27,9 @@ struct ChunkReq {
   }
 };
 
-// Lengths are held to the bounds the call was given, so that no index can
-// leave the buffers whatever the index arrays hold.
+// Rows and lengths are held to the bounds the call was given, so that no row
+// of q, out or a workspace outside them is touched (kv_indptr itself is
+// trusted, as by the decode calls).
 __device__ __forceinline__ ChunkReq chunk_req(const ChunkBatch &a, int b) {
   ChunkReq r;
   r.q0 = max(0, a.q_indptr[b]);

@@ -145,8 +145,8 @@ def check_chunk(bt, out, lse, fill=7.0):
             g = _host(lse)[r]
             none = np.isneginf(wl)
             assert np.array_equal(np.isneginf(g), none)
-            assert np.all(np.abs(g - wl)[~none] <= tl[~none]), float(
-                (np.abs(g - wl)[~none] / tl[~none]).max())
+            err = np.abs(g[~none] - wl[~none])
+            assert np.all(err <= tl[~none]), float((err / tl[~none]).max())
     assert np.all(o[bt.q_ptr[-1]:] == fill)  # rows of no request
     if lse is not None:
         assert np.all(_host(lse)[bt.q_ptr[-1]:] == fill)
@@ -214,6 +214,111 @@ def test_chunk_other_groups(Hq, Hkv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [([1, 1], [20000, 700]), ([6], [9000]), ([10, 3], [6000, 5999]),
+                                 ([40, 30], [9001, 130]), ([300, 2], [9000, 8000])])
+def test_chunk_long_lists(m, n, dtype):
+    """Few rows over long lists: the lists are cut into splits (for 16 query
+    heads over 4 KV heads, every form of the kernels), some rows' entries
+    within one split and some over several, and the mass of an entry shared
+    by several CTAs."""
+    torch = _torch()
+    bt = Batch(13, m, n, 16, 4, dtype)
+    d = bt.device()
+    out, lse = run_chunk(bt, d)
+    check_chunk(bt, out, lse)
+    again, lse2 = run_chunk(bt, d)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)  # no order of atomics in it
+    got, got2 = (torch.zeros(bt.B, bt.max_kv, device="cuda") for _ in range(2))
+    run_mass(bt, d, lse, None, 1.0, got)
+    check_mass(bt, lse, None, 1.0, got, 0.0)
+    run_mass(bt, d, lse, None, 1.0, got2)
+    assert torch.equal(got, got2)
+
+
+def test_chunk_many_requests():
+    """300 requests of a few rows each, every seventh without any."""
+    rng = np.random.default_rng(14)
+    m = [0 if b % 7 == 3 else int(rng.integers(1, 4)) for b in range(300)]
+    n = [int(rng.integers(0, 60)) for _ in range(300)]
+    torch = _torch()
+    for shift in (0, 30):  # 30: chunks long enough for the other kernels
+        bt = Batch(15, [x + shift if x else 0 for x in m], [x + shift for x in n], 8, 2, "bf16")
+        d = bt.device()
+        out, lse = run_chunk(bt, d)
+        check_chunk(bt, out, lse)
+        got = torch.zeros(bt.B, bt.max_kv, device="cuda")
+        run_mass(bt, d, lse, None, 1.0, got)
+        check_mass(bt, lse, None, 1.0, got, 0.0)
+
+
+def test_no_wait_gave_up():
+    """The status word that the tensor-core kernels' bounded waits would set
+    reads 0 after a call, whatever the workspace held before."""
+    torch = _torch()
+    bt = Batch(16, [40, 150], [300, 700], 16, 4, "bf16")
+    d = bt.device()
+    out, lse = torch.empty_like(d["q"]), torch.empty(bt.rows, 16, device="cuda")
+    ws = torch.full((akv.akv_chunk_workspace(bt.shp, 2, bt.rows, 150, 700),), 255, dtype=torch.uint8,
+                    device="cuda")
+    akv.akv_chunk_attention(bt.shp, 2, d["q_ptr"], d["q"], d["k"], d["v"], d["kv_ptr"], d["idx"], 150,
+                            700, out, lse, ws)
+    assert akv.akv_workspace_status(ws) == 0
+    check_chunk(bt, out, lse)
+    ws = torch.full((akv.akv_attention_mass_workspace(bt.shp, 2, bt.rows, 150, 700),), 255,
+                    dtype=torch.uint8, device="cuda")
+    got = torch.zeros(2, 700, device="cuda")
+    akv.akv_attention_mass(bt.shp, 2, d["q_ptr"], d["q"], d["k"], d["kv_ptr"], d["idx"], 150, 700, lse,
+                           1.0, None, got, ws)
+    assert akv.akv_workspace_status(ws) == 0
+    check_mass(bt, lse, None, 1.0, got, 0.0)
+
+
+def test_no_lists_at_all():
+    """max_kv = 0 with no pool: rows get zeros and -inf."""
+    torch = _torch()
+    for dtype in ("bf16", "f32"):
+        for m in (1, 40, 300):
+            shp = akv.shape(16, 4, 64, dtype)
+            q = akv.to_device(_rand(np.random.default_rng(1), (m, 16, 64), dtype), dtype)
+            pool = q.new_zeros(0, 4, 64)
+            out, lse = torch.full_like(q, 7.0), torch.zeros(m, 16, device="cuda")
+            ws = torch.empty(akv.akv_chunk_workspace(shp, 1, m, m, 0), dtype=torch.uint8, device="cuda")
+            akv.akv_chunk_attention(shp, 1, akv.i32_device([0, m]), q, pool, pool, akv.i32_device([0, 0]),
+                                    akv.i32_device([]), m, 0, out, lse, ws)
+            torch.cuda.synchronize()
+            assert not out.any() and bool(torch.isneginf(lse).all())
+
+
+def test_mass_of_a_long_chunk():
+    """Each entry's mass is the sum of 24,000 weights (1,500 rows of 16 heads
+    over 2,000 entries, against 64 bits on the GPU): the sums' roundings stay
+    within the bound that holds for short ones, and the total is the number
+    of (row, head) pairs."""
+    torch = _torch()
+    bt = Batch(17, [1500], [2000], 16, 4, "bf16")
+    d = bt.device()
+    _, lse = run_chunk(bt, d)
+    got = torch.zeros(1, 2000, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, got)
+    idx = d["idx"].long()
+    want = torch.zeros(2000, dtype=torch.float64, device="cuda")
+    E = 0.0
+    seen = 501 + torch.arange(1500, device="cuda")
+    for h in range(16):
+        K, q = d["k"][idx, h // 4].double(), d["q"][:, h].double()
+        s = (q @ K.T / 8).masked_fill(torch.arange(2000, device="cuda") >= seen[:, None], -float("inf"))
+        want += torch.exp(s - lse[:, h].double()[:, None]).sum(0)
+        E = max(E, float((q.abs() @ K.abs().T).max()) / 8 * 2.0 ** -18)
+    err = (got[0].double() - want).abs()
+    assert bool((err <= (2 * E + 2.0 ** -18) * want).all())
+    # the rounding of 24,000 additions in one fp32 chain would be about
+    # sqrt(24000) 2^-25 = 5e-6; a score's own error is 2^-24 of its size times
+    # a few, 1e-6 of a weight here
+    assert float(err.norm() / want.norm()) < 2e-6
+    assert abs(float(got.double().sum()) / (1500 * 16) - 1) < 2e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("m", [1, 4, 300])
 def test_chunk_peaky_scores(m, dtype):
     """Scores of standard deviation 16: sharp rows, running maxima that rise."""
@@ -224,13 +329,14 @@ def test_chunk_peaky_scores(m, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("m", [2, 40, 300])
-def test_hidden_entries_do_not_reach_a_row(m, dtype):
+@pytest.mark.parametrize("more", [500, 4000])
+@pytest.mark.parametrize("m", [2, 10, 40, 300])
+def test_hidden_entries_do_not_reach_a_row(m, more, dtype):
     """NaN and infinities in the value and key of a chunk's later tokens, and
     in pool rows that no list names (row 0 among them): earlier rows keep
     their values, and rows that see such an entry show it."""
     torch = _torch()
-    n = m + 500
+    n = m + more
     bt = Batch(9, [m, m], [n, m], 16, 4, dtype, spare=50)
     clean = Batch(9, [m, m], [n, m], 16, 4, dtype, spare=50)
     d = bt.device()
@@ -495,7 +601,8 @@ def _run_evict(lens, mass, keep, n_first, n_recent, with_pos=True, max_kv=None, 
 
 
 @pytest.mark.parametrize("lens", [[1], [0, 0], [1, 2, 3, 0, 31, 32, 33], [127, 128, 129, 4095],
-                                  [20000, 5, 70001], [300_000]])
+                                  [16384, 16383], [16385, 1], [20000, 5, 70001], [131_072, 131_071],
+                                  [131_073], [300_000], [140_000] + [7] * 9, [3] * 200])
 def test_evict_sizes(lens):
     rng = np.random.default_rng(sum(lens))
     mass = np.exp(2 * rng.standard_normal((len(lens), max(max(lens), 1)))).astype(np.float32)
