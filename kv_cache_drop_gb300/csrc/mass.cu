@@ -94,15 +94,24 @@ __global__ void __launch_bounds__(kFThreads, 2)
     const int last = min(rq.n, j0 + kFKeys) - 1;  // sees the fewest rows
     const bool plain = r0 >= (int64_t)max(0, last - old) * grp && r0 + kFRows <= rows;
     float x[4] = {};
+    if (plain) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int r = r0 + ty + 16 * p;
-      const float v = sm.lse[buf][ty + 16 * p];
-      const int lim = plain ? INT32_MAX : r < rows && v != INFINITY ? rq.limit(r / grp) : 0;
+      for (int p = 0; p < 8; ++p) {
+        const float v = sm.lse[buf][ty + 16 * p];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float w = exp2f(fmaf(s[p][q], 0.125f, -v) * kLog2e);
-        x[q] += j0 + tx + 16 * q < lim ? w : 0.f;
+        for (int q = 0; q < 4; ++q) x[q] += ptx::ex2(fmaf(s[p][q], 0.125f, -v) * kLog2e);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int r = r0 + ty + 16 * p;
+        const float v = sm.lse[buf][ty + 16 * p];
+        const int lim = r < rows && v != INFINITY ? rq.limit(r / grp) : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float w = ptx::ex2(fmaf(s[p][q], 0.125f, -v) * kLog2e);
+          x[q] += j0 + tx + 16 * q < lim ? w : 0.f;
+        }
       }
     }
 #pragma unroll
