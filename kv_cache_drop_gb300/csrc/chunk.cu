@@ -544,8 +544,7 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // one type and the pool is bf16; the row sums are taken by the softmax
 // threads from the unrounded weights, so that the log-sum-exp is good to fp32.
 // Per window the MMA thread issues O_0 += P_0 V, S_0 of the next window, then
-// the same for tile 1: one tile's softmax runs beside the other's MMAs.  The
-// running maximum is raised (and O rescaled) only when it grows by 2^8.
+// the same for tile 1: one tile's softmax runs beside the other's MMAs.
 //
 // Hidden entries.  Windows from the first tile's limit on are masked per row.
 // There a weight of 0 would still turn a hidden infinity or NaN of V into
@@ -558,7 +557,9 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // return.
 // ---------------------------------------------------------------------------
 constexpr int kBarP = 3;         // hardware barriers kBarP + i (0 is __syncthreads)
-constexpr float kRescale = 8.f;  // log2 units
+constexpr float kRescale = 8.f;       // log2 units by which a maximum may pass the reference
+constexpr float kRaise = 65536.f;     // the row sum that raises it
+constexpr float kHuge = 1.0995116e12f;  // 2^40: a window's sum that was computed too far above it
 
 constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 5; }
 // Warps: the softmax groups (a warpgroup each), then the producers and the MMA
@@ -814,72 +815,86 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       filled();
       ptx::named_bar_sync(kBarP + i, kBarPCount);
       const float2 scale2 = make_float2(kScale, kScale);
-      float m_run = -INFINITY;
-      // row sum: four chains, so that no addition waits for the one before
-      float2 l4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
+      // Weights are 2^(score - m_run) with m_run any reference, not the running
+      // maximum: the first window's maximum, raised by l's exponent whenever l
+      // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference that is
+      // 40 below the maximum costs nothing, and the windows after the first
+      // need no maximum (9,210 -> @@ us for 2 x 4,096 rows over 50k-70k
+      // entries).  A window whose weights sum to 2^40 or more, or that has
+      // hidden entries, is done over with its maximum: its scores stay in TMEM
+      // until the weights are known to be good.
+      float m_run = -INFINITY, l = 0.f;
       for (int n = 0; n < n_win; ++n) {
         wait(&sm.bar_s[i], n & 1);
         ptx::tc_fence_after();
-        uint32_t sr[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
-        ptx::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
-        if (n >= w_ragged) {
-          const int seen = min(lim, c1) - (c0 + n * kTcKeys);
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= seen) sr[c] = 0xff800000u;  // -inf
+        float alpha = 1.f;  // what the sums so far are scaled by
+        if (l > kRaise && l < INFINITY) {
+          const int e = (int)(__float_as_uint(l) >> 23) - 127;
+          m_run += (float)e;
+          alpha = __uint_as_float((uint32_t)(127 - e) << 23);
         }
-        float mx8[8];
+        uint32_t sr[128], pw[64];
+        float lw;
+        // pw: word k holds keys 2 k, 2 k + 1 as bf16; lw: their sum, unrounded,
+        // in four chains so that no addition waits for the one before
+        auto load = [&] {
 #pragma unroll
-        for (int k8 = 0; k8 < 8; ++k8)
-          mx8[k8] = ptx::max3(__uint_as_float(sr[k8]), __uint_as_float(sr[8 + k8]),
-                              __uint_as_float(sr[16 + k8]));
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
+          ptx::tmem_wait_ld();
 #pragma unroll
-        for (int c = 24; c + 16 <= 120; c += 16)
+          for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+        };
+        auto weigh = [&](float ref) {
+          const float2 neg2 = make_float2(-ref, -ref);
+          float2 l4[4];
 #pragma unroll
-          for (int k8 = 0; k8 < 8; ++k8)
-            mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
+          for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = fmaxf(mx8[k8], __uint_as_float(sr[120 + k8]));
-        const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
-                               fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_new = fmaxf(m_run, mx * kScale);
-        const bool need = m_new > m_run + kRescale;
-        const bool any = __any_sync(0xffffffffu, need);
-        float alpha = 1.f;
-        if (need) {
-          alpha = ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
-          m_run = m_new;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            l4[k].x *= alpha;
-            l4[k].y *= alpha;
-          }
-        }
-        const float mref = m_run == -INFINITY ? 0.f : m_run;
-        const float2 neg2 = make_float2(-mref, -mref);
-        // weights in fp32 (summed as they are), rounded to bf16 pairs: word k
-        // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
-#pragma unroll
-        for (int qtr = 0; qtr < 4; ++qtr) {
-          uint32_t pw[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int c = 2 * (16 * qtr + k);
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                                        scale2, neg2);
+          for (int k = 0; k < 64; ++k) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), scale2, neg2);
             const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             l4[k & 3] = __fadd2_rn(l4[k & 3], p);
             pw[k] = pack2(p.x, p.y);
           }
-          ptx::tmem_st16(tS + 16 * qtr, pw);
+          const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+          lw = la.x + la.y;
+        };
+        bool good = n < w_ragged && !__any_sync(0xffffffffu, m_run == -INFINITY);
+        if (good) {
+          load();
+          weigh(m_run);
+          good = !__any_sync(0xffffffffu, !(lw < kHuge));
         }
-        if (n > 0 && any) {
+        if (!good) {
+          load();
+          if (n >= w_ragged) {
+            const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= seen) sr[c] = 0xff800000u;  // -inf
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 16)
+#pragma unroll
+            for (int k8 = 0; k8 < 8; ++k8)
+              mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
+          const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
+                                 fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          const float m_new = fmaxf(m_run, mx * kScale);
+          if (m_new > m_run + kRescale) {
+            alpha *= ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
+            m_run = m_new;
+          }
+          weigh(m_run == -INFINITY ? 0.f : m_run);
+        }
+        l = fmaf(l, alpha, lw);
+#pragma unroll
+        for (int qtr = 0; qtr < 4; ++qtr) ptx::tmem_st16(tS + 16 * qtr, pw + 16 * qtr);
+        if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
 #pragma unroll
           for (int hlf = 0; hlf < 2; ++hlf) {
@@ -942,8 +957,6 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           }
         }
       }
-      const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
-      const float l = la.x + la.y;
       const bool direct = part.direct(lim);
       if (valid && direct && split == 0) {
         const bool none = lim == 0;
