@@ -557,9 +557,10 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // return.
 // ---------------------------------------------------------------------------
 constexpr int kBarP = 3;         // hardware barriers kBarP + i (0 is __syncthreads)
+constexpr int kBarAll = 2;       // all warps, after a pass
 constexpr float kRescale = 8.f;       // log2 units by which a maximum may pass the reference
 constexpr float kRaise = 65536.f;     // the row sum that raises it
-constexpr float kHuge = 1.0995116e12f;  // 2^40: a window's sum that was computed too far above it
+constexpr float kHuge = 1.2089258e24f;  // 2^80: a window's sum that was computed too far above it
 
 constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 5; }
 // Warps: the softmax groups (a warpgroup each), then the producers and the MMA
@@ -582,6 +583,7 @@ struct __align__(1024) TcSmem {
   uint32_t tmem_base;
   uint32_t gave_up;  // a wait of this CTA ran out
   uint32_t odd;      // V windows held an infinity or NaN beside hidden entries
+  uint32_t again;    // weights were computed too far above their reference
 };
 
 template <int kTiles>
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) ptx::mbar_init(&sm.bar_s[s], 1);
     ptx::mbar_init(&sm.bar_done, 1);
-    sm.gave_up = sm.odd = 0u;
+    sm.gave_up = sm.odd = sm.again = 0u;
     ptx::fence_barrier_init();
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(&sm.tmem_base, kCols);
@@ -680,6 +682,13 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     if (!ptx::mbar_wait_grid(bar, parity, &sm.gave_up, 1u, kTcWaitBudget))
       atomicOr(status, kStatusWaitTimeout);
+  };
+
+  // Every warp, after a pass: whether there is another.  All copies and MMAs of
+  // the pass are done when the barrier opens.
+  auto run_again = [&](int pass) {
+    ptx::named_bar_sync(kBarAll, tc_threads(kTiles));
+    return pass == 0 && *(volatile uint32_t *)&sm.again != 0u;
   };
 
   if (warp >= kProdWarp) {
@@ -705,7 +714,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           row[s] = s0 + s < 32 && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
         }
       };
-      auto copy = [&](int n, const int *row) {
+      auto copy = [&](int n, const int *row, bool commit = true) {
         if (n < n_win) {
           const uint32_t at = (n % kSt) * kTcTileBytes;
 #pragma unroll
@@ -718,7 +727,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
             }
           }
         }
-        asm volatile("cp.async.commit_group;\n" ::: "memory");
+        if (commit) asm volatile("cp.async.commit_group;\n" ::: "memory");
       };
       // every window but the newest `pending` has landed and is visible to the
       // tensor core
@@ -734,20 +743,27 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
 #pragma unroll
         for (int n = kFill; n < kSt; ++n) copy(n, first[n - kFill]);
       }
-      slots(kSt, nx);
-      landed(std::integral_constant<int, kSt - kFill>());  // windows 0 .. kFill - 1
-      ptx::named_bar_sync(kBarP, kBarPCount);
-      if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-      for (int n = 0; n < n_win; ++n) {
-        if (n + 1 >= kFill) landed(std::integral_constant<int, kSt - 3>());  // window n + 1
+      for (int pass = 0;; ++pass) {
+        slots(kSt, nx);
+        landed(std::integral_constant<int, kSt - kFill>());  // windows 0 .. kFill - 1
         ptx::named_bar_sync(kBarP, kBarPCount);
         if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-        if (n >= 1) {
-          int cur[kSteps];
+        for (int n = 0; n < n_win; ++n) {
+          if (n + 1 >= kFill) landed(std::integral_constant<int, kSt - 3>());  // window n + 1
+          ptx::named_bar_sync(kBarP, kBarPCount);
+          if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+          if (n >= 1) {
+            int cur[kSteps];
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
-          slots(n + kSt, nx);
-          copy(n - 1 + kSt, cur);
+            for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
+            slots(n + kSt, nx);
+            copy(n - 1 + kSt, cur);
+          }
+        }
+        if (!run_again(pass)) break;
+        for (int n = 0; n < kSt; ++n) {  // the ring's first fill once more, by the producers alone
+          slots(n, nx);
+          copy(n, nx, n >= kFill - 1);
         }
       }
       asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -774,38 +790,46 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           ptx::mma_f16_ts(tmem + kColO + 64 * t, tmem + 128 * t + 8 * kk, dv + st * kTileStep + 128 * kk,
                           idO, (acc || kk > 0) ? 1u : 0u);
       };
-      ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
-      if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-      ptx::tc_fence_after();
-      if (n_win > 0) {
-        issue_s(0, 0);
-        if (two) issue_s(1, 0);
-      }
-      for (int n = 0; n < n_win; ++n) {
-        const int st = n % kSt, st1 = (n + 1) % kSt;
-        ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
+      for (int pass = 0;; ++pass) {
+        ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
+        if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
         ptx::tc_fence_after();
-        issue_o(0, st, n > 0);
-        if (n + 1 < n_win) issue_s(0, st1);
-        if (kTiles == 2) {
-          ptx::named_bar_sync(kBarP + 1, kBarPCount);
+        if (n_win > 0) {
+          issue_s(0, 0);
+          if (two) issue_s(1, 0);
+        }
+        for (int n = 0; n < n_win; ++n) {
+          const int st = n % kSt, st1 = (n + 1) % kSt;
+          ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
           ptx::tc_fence_after();
-          if (two) {
-            issue_o(1, st, n > 0);
-            if (n + 1 < n_win) issue_s(1, st1);
+          issue_o(0, st, n > 0);
+          if (n + 1 < n_win) issue_s(0, st1);
+          if (kTiles == 2) {
+            ptx::named_bar_sync(kBarP + 1, kBarPCount);
+            ptx::tc_fence_after();
+            if (two) {
+              issue_o(1, st, n > 0);
+              if (n + 1 < n_win) issue_s(1, st1);
+            }
           }
         }
+        if (leader) ptx::mma_commit(&sm.bar_done);
+        wait(&sm.bar_done, pass & 1);
+        if (!run_again(pass)) break;
       }
-      if (leader) ptx::mma_commit(&sm.bar_done);
-      wait(&sm.bar_done, 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     if (i == 1 && !two) {
       // no row in this tile: only the barriers
       filled();
-      for (int n = 0; n <= n_win; ++n) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-      wait(&sm.bar_done, 0);
+      ptx::named_bar_sync(kBarP + 1, kBarPCount);
+      for (int pass = 0;; ++pass) {
+        for (int n = 0; n < n_win; ++n) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+        wait(&sm.bar_done, pass & 1);
+        if (!run_again(pass)) break;
+        ptx::named_bar_sync(kBarP + 1, kBarPCount);
+      }
     } else {
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + 64 * i;
@@ -817,115 +841,117 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       const float2 scale2 = make_float2(kScale, kScale);
       // Weights are 2^(score - m_run) with m_run any reference, not the running
       // maximum: the first window's maximum, raised by l's exponent whenever l
-      // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference that is
-      // 40 below the maximum costs nothing, and the windows after the first
-      // need no maximum (9,210 -> @@ us for 2 x 4,096 rows over 50k-70k
-      // entries).  A window whose weights sum to 2^40 or more, or that has
-      // hidden entries, is done over with its maximum: its scores stay in TMEM
-      // until the weights are known to be good.
+      // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference far
+      // below the maximum costs nothing, and the windows after the first need
+      // no maximum (9,210 -> @@ us for 2 x 4,096 rows over 50k-70k entries).
+      // If a window's weights sum to 2^80 or more (its scores jump by 55 over
+      // all before it), the whole CTA runs once more with exact maxima.
       float m_run = -INFINITY, l = 0.f;
-      for (int n = 0; n < n_win; ++n) {
-        wait(&sm.bar_s[i], n & 1);
-        ptx::tc_fence_after();
-        float alpha = 1.f;  // what the sums so far are scaled by
-        if (l > kRaise && l < INFINITY) {
-          const int e = (int)(__float_as_uint(l) >> 23) - 127;
-          m_run += (float)e;
-          alpha = __uint_as_float((uint32_t)(127 - e) << 23);
-        }
-        uint32_t sr[128], pw[64];
-        float lw;
-        // pw: word k holds keys 2 k, 2 k + 1 as bf16; lw: their sum, unrounded,
-        // in four chains so that no addition waits for the one before
-        auto load = [&] {
+      for (int pass = 0;; ++pass) {
+        bool huge = false;
+        for (int n = 0; n < n_win; ++n) {
+          wait(&sm.bar_s[i], (pass * n_win + n) & 1);
+          ptx::tc_fence_after();
+          float alpha = 1.f;  // what the sums so far are scaled by
+          if (l > kRaise) {
+            const int e = min(127, (int)(__float_as_uint(l) >> 23) - 127);
+            m_run += (float)e;
+            alpha = __uint_as_float((uint32_t)(127 - e) << 23);
+          }
+          uint32_t sr[128];
 #pragma unroll
           for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
-        };
-        auto weigh = [&](float ref) {
-          const float2 neg2 = make_float2(-ref, -ref);
+          if (pass > 0 || n >= w_ragged || __any_sync(0xffffffffu, m_run == -INFINITY)) {
+            if (n >= w_ragged) {
+              const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (c >= seen) sr[c] = 0xff800000u;  // -inf
+            }
+            float mx8[8];
+#pragma unroll
+            for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; c += 16)
+#pragma unroll
+              for (int k8 = 0; k8 < 8; ++k8)
+                mx8[k8] =
+                    ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
+            const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
+                                   fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+            const float m_new = fmaxf(m_run, mx * kScale);
+            if (m_new > m_run + kRescale) {
+              alpha *= ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
+              m_run = m_new;
+            }
+          }
+          const float mref = m_run == -INFINITY ? 0.f : m_run;
+          const float2 neg2 = make_float2(-mref, -mref);
+          // weights in fp32, summed as they are (in four chains, so that no
+          // addition waits for the one before), rounded to bf16 pairs: word k
+          // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
           float2 l4[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float2 x = __ffma2_rn(
-                make_float2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), scale2, neg2);
-            const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-            l4[k & 3] = __fadd2_rn(l4[k & 3], p);
-            pw[k] = pack2(p.x, p.y);
+          for (int qtr = 0; qtr < 4; ++qtr) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int c = 2 * (16 * qtr + k);
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), scale2, neg2);
+              const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
+              l4[k & 3] = __fadd2_rn(l4[k & 3], p);
+              pw[k] = pack2(p.x, p.y);
+            }
+            ptx::tmem_st16(tS + 16 * qtr, pw);
           }
           const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
-          lw = la.x + la.y;
-        };
-        bool good = n < w_ragged && !__any_sync(0xffffffffu, m_run == -INFINITY);
-        if (good) {
-          load();
-          weigh(m_run);
-          good = !__any_sync(0xffffffffu, !(lw < kHuge));
-        }
-        if (!good) {
-          load();
-          if (n >= w_ragged) {
-            const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+          const float lw = la.x + la.y;
+          huge |= !(lw < kHuge);
+          l = fmaf(l, alpha, lw);
+          if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= seen) sr[c] = 0xff800000u;  // -inf
-          }
-          float mx8[8];
+            for (int hlf = 0; hlf < 2; ++hlf) {
+              uint32_t o[32];
+              ptx::tmem_ld32(tO + 32 * hlf, o);
+              ptx::tmem_wait_ld();
+              ptx::reg_fence32(o);
 #pragma unroll
-          for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 128; c += 16)
-#pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8)
-              mx8[k8] = ptx::max3(mx8[k8], __uint_as_float(sr[c + k8]), __uint_as_float(sr[c + 8 + k8]));
-          const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
-                                 fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-          const float m_new = fmaxf(m_run, mx * kScale);
-          if (m_new > m_run + kRescale) {
-            alpha *= ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
-            m_run = m_new;
-          }
-          weigh(m_run == -INFINITY ? 0.f : m_run);
-        }
-        l = fmaf(l, alpha, lw);
-#pragma unroll
-        for (int qtr = 0; qtr < 4; ++qtr) ptx::tmem_st16(tS + 16 * qtr, pw + 16 * qtr);
-        if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
-#pragma unroll
-          for (int hlf = 0; hlf < 2; ++hlf) {
-            uint32_t o[32];
-            ptx::tmem_ld32(tO + 32 * hlf, o);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence32(o);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            ptx::tmem_st32(tO + 32 * hlf, o);
-          }
-        }
-        if (n >= w_ragged) {
-          uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
-          for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
-            const uint4 x = v4[c];
-            const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
-                                       finite_or_zero(x.w));
-            if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-              *(volatile uint32_t *)&sm.odd = 1u;
-              __threadfence_block();
-              v4[c] = y;
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              ptx::tmem_st32(tO + 32 * hlf, o);
             }
           }
-          ptx::fence_proxy_async_smem();  // before the tensor core reads the window
+          if (n >= w_ragged) {
+            uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
+            for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
+              const uint4 x = v4[c];
+              const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
+                                         finite_or_zero(x.w));
+              if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+                *(volatile uint32_t *)&sm.odd = 1u;
+                __threadfence_block();
+                v4[c] = y;
+              }
+            }
+            ptx::fence_proxy_async_smem();  // before the tensor core reads the window
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::named_bar_sync(kBarP + i, kBarPCount);
         }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::named_bar_sync(kBarP + i, kBarPCount);
+        wait(&sm.bar_done, pass & 1);  // the last P.V
+        if (valid && huge && pass == 0) *(volatile uint32_t *)&sm.again = 1u;
+        if (!run_again(pass)) break;
+        m_run = -INFINITY;
+        l = 0.f;
+        ptx::named_bar_sync(kBarP + i, kBarPCount);  // window 0 landed again
       }
-      wait(&sm.bar_done, 0);  // the last P.V
       ptx::tc_fence_after();
       uint32_t o[64];
       if (n_win > 0) {

@@ -14,7 +14,8 @@ weight's relative error is that of its score.
 * lse: E + 2^-21 (1 + |lse|): the score's error, and the rounding of the
   maximum, of the sum (relative, so absolute in the logarithm) and of the
   result, a few 2^-24 each.
-* mass: (2 E + 2^-18) times the mass: every term is positive.
+* mass: (2 E + 2^-18) times the mass: every term is positive.  A weight below
+  2^-126 is no normal fp32 number and counts as 0: 2^-126 per term.
 * prepared rows: u |y| + 2^-20 |row's largest pair|: angles are good to 4e-7
   and the norm and rotation to a few 2^-24.
 """
@@ -110,7 +111,7 @@ class Batch:
         with np.errstate(invalid="ignore"):
             w = np.where(np.isneginf(s) | np.isneginf(l64)[..., None], 0, np.exp(s - l64[..., None]))
         got = w.sum((0, 1))
-        tol = (2 * E.max(initial=0) + 2.0 ** -18) * got
+        tol = (2 * E.max(initial=0) + 2.0 ** -18) * got + 2.0 ** -126 * self.m[b] * self.Hq
         if mass_in is not None:
             old = decay * mass_in[:max(0, self.n[b] - self.m[b])].astype(np.float64)
             got[:len(old)] += old
@@ -326,6 +327,43 @@ def test_chunk_peaky_scores(m, dtype):
     d = bt.device()
     out, lse = run_chunk(bt, d)
     check_chunk(bt, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 10, 40, 300])
+def test_chunk_scores_that_jump(m, dtype):
+    """Scores that rise by 60 to 190 within one window after hundreds of low
+    ones, rise in steps, or fall from the first entry on: weights relative to
+    anything but the running maximum would overflow or vanish."""
+    n = 1500
+    for case in ("one peak", "late peak", "steps", "sink", "two levels"):
+        bt = Batch(18, [m], [n], 16, 4, dtype)
+        level = np.zeros(n)
+        if case == "one peak":
+            level[:] = -3
+            level[700] = 3
+        elif case == "late peak":
+            level[:] = -3
+            level[n - m] = 3          # every row sees it
+            level[1100:1110] = 1
+        elif case == "steps":
+            level = -3 + np.floor(np.arange(n) / 100) * 0.4
+        elif case == "sink":
+            level[0] = 3
+        else:
+            level[:400], level[400:] = -2, 2
+        rng = np.random.default_rng(19)
+        k = (level[:, None, None] + 0.05 * rng.standard_normal((n, 4, 64))).astype(np.float32)
+        q = (4 + 0.05 * rng.standard_normal((m, 16, 64))).astype(np.float32)  # scores 32 x level
+        pool = np.zeros((bt.S, 4, 64), np.float32)
+        pool[bt.idx] = k
+        bt.q, bt.k = (workloads.bf16_bits(x) if dtype == "bf16" else x for x in (q, pool))
+        d = bt.device()
+        out, lse = run_chunk(bt, d)
+        check_chunk(bt, out, lse)
+        got = _torch().zeros(1, n, device="cuda")
+        run_mass(bt, d, lse, None, 1.0, got)
+        check_mass(bt, lse, None, 1.0, got, 0.0)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
