@@ -497,6 +497,11 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
  * lengths; longer ones are cut to them.  A pool index outside [0, S) reads
  * pool row 0.  All index data stays on the device, so the calls can be
  * captured in a CUDA graph and replayed with other lengths within the bounds.
+ * A workspace serves one call at a time: calls that may overlap on the GPU
+ * (two streams, two captured graphs) need one each.  Workspaces start with the
+ * status word read by akv_workspace_status (cleared by each call).  Outputs must
+ * not overlap inputs unless a call says so.  Make the first call of each kind
+ * outside a stream capture (it loads the kernels).
  * Limits: B <= 65535, max_kv <= 2^30, Hq <= 65535, and grids within CUDA's
  * limits (AKV_ERR_UNSUPPORTED otherwise). */
 
@@ -527,8 +532,8 @@ akv_status akv_qk_norm_append(const akv_shape *shape, int32_t n, const void *q, 
  * log(sum_j exp(s_j)) of the scaled scores.  A row that sees nothing gets
  * zeros, and -inf.  k_pool, v_pool [S, Hkv, D].  Values in hidden entries
  * (NaN, infinities) do not reach a row.  workspace: device, 256-byte
- * aligned, akv_chunk_workspace() bytes for the same arguments (0: may be
- * NULL): split-KV partials.  bf16: the weights are rounded to bf16 for the
+ * aligned, akv_chunk_workspace() bytes for the same arguments: the status word
+ * and split-KV partials.  bf16: the weights are rounded to bf16 for the
  * P x V product; their sum and the scores are fp32. */
 size_t akv_chunk_workspace(const akv_shape *shape, int32_t B, int32_t n_rows, int32_t max_q,
                            int32_t max_kv);

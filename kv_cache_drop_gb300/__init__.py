@@ -653,7 +653,7 @@ def akv_chunk_attention(shp: Shape, B: int, q_indptr, q, k_pool, v_pool, kv_indp
         _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), max_kv,
         _typed("out", out, dt, dev, (n, shp.Hq, D)),
         _typed("lse", lse, torch.float32, dev, (n, shp.Hq)),
-        None if workspace is None else workspace.data_ptr(),
+        _typed("workspace", workspace, torch.uint8, dev),
         0 if workspace is None else workspace.numel(), st))
 
 
@@ -677,7 +677,7 @@ def akv_attention_mass(shp: Shape, B: int, q_indptr, q, k_pool, kv_indptr, kv_in
         _typed("lse", lse, torch.float32, dev, (n, shp.Hq)), decay,
         _typed("mass_in", mass_in, torch.float32, dev, tuple(mass_out.shape)),
         _typed("mass_out", mass_out, torch.float32, dev, (B, None)), mass_out.shape[1],
-        None if workspace is None else workspace.data_ptr(),
+        _typed("workspace", workspace, torch.uint8, dev),
         0 if workspace is None else workspace.numel(), st))
 
 

@@ -50,10 +50,12 @@ struct F32Smem {
 };
 
 __global__ void __launch_bounds__(kFThreads, 1)
-    chunk_f32_kernel(const ChunkBatch a, float *out, float *lse, const ChunkParts part) {
+    chunk_f32_kernel(const ChunkBatch a, float *out, float *lse, const ChunkParts part,
+                     uint32_t *status) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   F32Smem &sm = *reinterpret_cast<F32Smem *>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  clear_status(status);
   const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
   const int64_t r0 = (int64_t)(blockIdx.x / part.ns) * kFRows;
   const ChunkReq rq = chunk_req(a, b);
@@ -321,10 +323,12 @@ __global__ void __launch_bounds__(kMergeThreads)
 constexpr int kSSt = 3;  // K and V tiles per warp
 
 __global__ void __launch_bounds__(kSHeads * 32, 2)
-    chunk_small_kernel(const ChunkBatch a, __nv_bfloat16 *out, float *lse, const ChunkParts part) {
+    chunk_small_kernel(const ChunkBatch a, __nv_bfloat16 *out, float *lse, const ChunkParts part,
+                       uint32_t *status) {
   constexpr int kSt = kSSt;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  clear_status(status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int split = blockIdx.x, b = blockIdx.y, g = blockIdx.z * kSHeads + warp;
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   TcSmem<kTiles> &sm = *reinterpret_cast<TcSmem<kTiles> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0u;
+  clear_status(status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the last row tiles see the most: they come first
   const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
@@ -843,7 +847,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       // maximum: the first window's maximum, raised by l's exponent whenever l
       // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference far
       // below the maximum costs nothing, and the windows after the first need
-      // no maximum (9,210 -> @@ us for 2 x 4,096 rows over 50k-70k entries).
+      // no maximum (9,210 -> 8,604 us for 2 x 4,096 rows over 50k-70k entries).
       // If a window's weights sum to 2^80 or more (its scores jump by 55 over
       // all before it), the whole CTA runs once more with exact maxima.
       float m_run = -INFINITY, l = 0.f;
@@ -1049,12 +1053,14 @@ void split_keys(ChunkPlan *p, int64_t ctas, int64_t want, int64_t resident, int 
 // us for 128 keys beside its neighbours, 6 us to start and end, and the
 // partials written and read at 5 TB/s.  The count that ends first when every
 // list is max_kv long: the splits then fill whole waves of CTAs (448 CTAs of
-// 196 windows instead of 896 of 128 and fewer: 1,078 -> @@ us for 14 chunks of
+// 196 windows instead of 896 of 128 and fewer: 1,078 -> 990 us for 14 chunks of
 // 64 over 50,000 entries).
 void split_windows(ChunkPlan *p, int64_t ctas, int64_t slots, double window, double row_bytes,
                    int max_kv) {
   const int windows = std::max(1, (max_kv + kTcKeys - 1) / kTcKeys);
-  const int most = std::min(kMaxSplit, std::max(1, windows / 4));
+  // at most eight waves, and four windows each
+  const int most = (int)std::max<int64_t>(
+      1, std::min<int64_t>(std::min(kMaxSplit, windows / 4), 8 * slots / std::max<int64_t>(1, ctas)));
   double best = 0;
   p->ns = 1;
   for (int ns = 1; ns <= most; ++ns) {
@@ -1097,24 +1103,24 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, i
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 cudaError_t launch_f32(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
-                       int64_t tiles, cudaStream_t s) {
+                       int64_t tiles, uint32_t *status, cudaStream_t s) {
   const int smem = (int)sizeof(F32Smem);
   cudaError_t e =
       cudaFuncSetAttribute(chunk_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   chunk_f32_kernel<<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kFThreads, smem, s>>>(
-      a, (float *)out, lse, part);
+      a, (float *)out, lse, part, status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
-                         cudaStream_t s) {
+                         uint32_t *status, cudaStream_t s) {
   const int warps = std::min(a.Hkv, kSHeads), smem = warps * kSSt * 2 * kSTile;
   cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   chunk_small_kernel<<<dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads), warps * 32, smem, s>>>(
-      a, (__nv_bfloat16 *)out, lse, part);
+      a, (__nv_bfloat16 *)out, lse, part, status);
   return cudaGetLastError();
 }
 
@@ -1182,8 +1188,8 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   cudaError_t e;
   if (p.kind == kTcKind) e = launch_tc<1>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
   else if (p.kind == kTcKind + 1) e = launch_tc<2>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
-  else if (p.kind == kSmallKind) e = launch_small(a, out, lse, part, s);
-  else e = launch_f32(a, out, lse, part, p.tiles, s);
+  else if (p.kind == kSmallKind) e = launch_small(a, out, lse, part, (uint32_t *)ws, s);
+  else e = launch_f32(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
   if (e != cudaSuccess || p.ns == 1) return e;
   return dtype == AKV_BF16 ? launch_merge<__nv_bfloat16>(a, out, lse, part, s)
                            : launch_merge<float>(a, out, lse, part, s);

@@ -45,6 +45,12 @@ __device__ __forceinline__ int64_t chunk_slot(const ChunkBatch &a, const ChunkRe
   return (unsigned)s < (unsigned)a.S ? s : 0;
 }
 
+// The call's status word starts at 0: written by one thread of every kernel
+// that opens a call (a wait that gives up sets its bit half a second later).
+__device__ __forceinline__ void clear_status(uint32_t *status) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0u;
+}
+
 // ---- tensor cores: 128 packed rows x 128 keys ----
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = 128;

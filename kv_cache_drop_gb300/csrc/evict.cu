@@ -20,6 +20,8 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 namespace cg = cooperative_groups;
 
 namespace akv {
@@ -322,10 +324,10 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
 // CTAs per request: enough for the lists to stay in registers, up to 8, or 16
 // where the device takes such clusters and the requests leave SMs idle.
 bool takes_16() {
-  static int known[64];  // 0 not asked, 1 no, 2 yes
+  static std::atomic<int> known[64];  // per device: 0 not asked, 1 no, 2 yes
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  if (known[dev] == 0) {
+  if (known[dev].load() == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kMaxCluster);
     cfg.blockDim = dim3(kEvThreads);
@@ -343,9 +345,9 @@ bool takes_16() {
                     cudaOccupancyMaxActiveClusters(&clusters, evict_kernel<false>, &cfg) == cudaSuccess &&
                     clusters > 0;
     if (!ok) (void)cudaGetLastError();
-    known[dev] = ok ? 2 : 1;
+    known[dev].store(ok ? 2 : 1);
   }
-  return known[dev] == 2;
+  return known[dev].load() == 2;
 }
 
 }  // namespace

@@ -44,7 +44,9 @@ struct MassF32Smem {
 };
 
 __global__ void __launch_bounds__(kFThreads, 2)
-    mass_f32_kernel(const ChunkBatch a, const MassArgs ma, int parts, float *partial) {
+    mass_f32_kernel(const ChunkBatch a, const MassArgs ma, int parts, float *partial,
+                    uint32_t *status) {
+  clear_status(status);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   MassF32Smem &sm = *reinterpret_cast<MassF32Smem *>(smem_raw);
   const int part = blockIdx.x % parts, b = blockIdx.y;
@@ -152,7 +154,8 @@ constexpr int mass_ctas(int rt) { return rt == 1 ? 4 : rt == 2 ? 3 : 2; }
 
 template <int kRT>
 __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
-    mass_small_kernel(const ChunkBatch a, const MassArgs ma, int chunk) {
+    mass_small_kernel(const ChunkBatch a, const MassArgs ma, int chunk, uint32_t *status) {
+  clear_status(status);
   constexpr int kMSt = mass_stages(kRT);
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   MassTcSmem &sm = *reinterpret_cast<MassTcSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                    ~uintptr_t(1023));
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0u;
+  clear_status(status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x % parts, b = blockIdx.y;
   const int j0 = (int)(blockIdx.x / parts) * kMBlock;
@@ -713,14 +716,15 @@ MassPlan mass_plan(int dtype, int B, int Hq, int Hkv, int max_q, int max_kv) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <int kRT>
-cudaError_t launch_small(const ChunkBatch &a, const MassArgs &ma, int chunk, cudaStream_t s) {
+cudaError_t launch_small(const ChunkBatch &a, const MassArgs &ma, int chunk, uint32_t *status,
+                         cudaStream_t s) {
   const int warps = std::min(a.Hkv, kSHeads);
   const int smem = warps * (mass_stages(kRT) * kSTile + chunk * (int)sizeof(float));
   cudaError_t e = cudaFuncSetAttribute(mass_small_kernel<kRT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   mass_small_kernel<kRT><<<dim3((unsigned)((a.max_kv + chunk - 1) / chunk), a.B), warps * 32, smem, s>>>(
-      a, ma, chunk);
+      a, ma, chunk, status);
   return cudaGetLastError();
 }
 
@@ -742,15 +746,16 @@ cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
   const MassPlan p = mass_plan(dtype, B, Hq, Hkv, max_q, max_kv);
   float *const partial = (float *)((char *)ws + kTcStatusBytes);
   cudaError_t e;
-  if (p.kind == 1) return launch_small<1>(a, ma, p.chunk, s);
-  if (p.kind == 2) return launch_small<2>(a, ma, p.chunk, s);
-  if (p.kind == 4) return launch_small<4>(a, ma, p.chunk, s);
+  if (p.kind == 1) return launch_small<1>(a, ma, p.chunk, (uint32_t *)ws, s);
+  if (p.kind == 2) return launch_small<2>(a, ma, p.chunk, (uint32_t *)ws, s);
+  if (p.kind == 4) return launch_small<4>(a, ma, p.chunk, (uint32_t *)ws, s);
   if (p.kind == 0) {
     const int smem = (int)sizeof(MassF32Smem);
     e = cudaFuncSetAttribute(mass_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (max_kv + kFKeys - 1) / kFKeys;
-    mass_f32_kernel<<<dim3((unsigned)(blocks * p.parts), B), kFThreads, smem, s>>>(a, ma, p.parts, partial);
+    mass_f32_kernel<<<dim3((unsigned)(blocks * p.parts), B), kFThreads, smem, s>>>(a, ma, p.parts, partial,
+                                                                                (uint32_t *)ws);
   } else {
     const int smem = (int)sizeof(MassTcSmem) + 1024;
     e = cudaFuncSetAttribute(mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
