@@ -541,12 +541,17 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 //        the MMA reads.  (TMA gathers of four rows deliver one 128-byte row
 //        per 24 clocks: 353 TFLOP/s at 1,024 rows over 16,384 entries.)
 //   then the MMA warp: TMEM allocation, one thread issuing tcgen05.mma
-// TMEM columns: S_i [128 i, + 128), O_i [128 kTiles + 64 i, + 64), Q_i
-// [192 kTiles + 32 i, + 32).  Q_i (bf16 pairs) is the A operand of S_i = Q_i
+// TMEM columns: S_i [128 i, + 128), O_i [128 kTiles + 80 i, + 80), Q_i
+// [208 kTiles + 32 i, + 32).  Q_i (bf16 pairs) is the A operand of S_i = Q_i
 // K^T; P_i overwrites the first 64 columns of S_i as bf16 pairs and is the A
 // operand of O_i += P_i V.  bf16 throughout, because A and B of one MMA have
-// one type and the pool is bf16; the row sums are taken by the softmax
-// threads from the unrounded weights, so that the log-sum-exp is good to fp32.
+// one type and the pool is bf16.  Two row sums: the softmax threads add the
+// unrounded weights, so that the log-sum-exp is good to fp32, and V has 16 more
+// columns of ones (a 2 KB tile that every window's last columns point at), so
+// that the MMA adds the rounded ones.  The output is divided by that second
+// sum: an average of V rows whose weights sum to 1, so that where few entries
+// carry a row the rounding of their weights hardly shows (error against 64 bits
+// 2.3e-3 -> 1.8e-3 on a mixed batch, of which the output's own rounding is 1.6e-3).
 // Per window the MMA thread issues O_0 += P_0 V, S_0 of the next window, then
 // the same for tile 1: one tile's softmax runs beside the other's MMAs.
 //
@@ -566,6 +571,9 @@ constexpr float kRescale = 8.f;       // log2 units by which a maximum may pass 
 constexpr float kRaise = 65536.f;     // the row sum that raises it
 constexpr float kHuge = 1.2089258e24f;  // 2^80: a window's sum that was computed too far above it
 
+constexpr uint32_t kOnesBytes = 16 * kD * 2;
+constexpr uint32_t kOCols = kD + 16;  // V's columns and the ones
+
 constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 5; }
 // Warps: the softmax groups (a warpgroup each), then the producers and the MMA
 // warp.  A softmax thread holds a row of 128 scores, so registers move from
@@ -583,6 +591,7 @@ template <int kTiles>
 struct __align__(1024) TcSmem {
   uint8_t k[tc_stages(kTiles)][kTcTileBytes];
   uint8_t v[tc_stages(kTiles)][kTcTileBytes];
+  uint8_t ones[kOnesBytes];  // 16 keys
   uint64_t bar_s[2], bar_done;
   uint32_t tmem_base;
   uint32_t gave_up;  // a wait of this CTA ran out
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   // a softmax group, the producers, the MMA warp
   constexpr int kBarPCount = 128 + 32 * kProducers + 32;
   constexpr uint32_t kCols = kTiles == 1 ? 256 : 512;
-  constexpr uint32_t kColO = 128 * kTiles, kColQ = 192 * kTiles;
+  constexpr uint32_t kColO = 128 * kTiles, kColQ = (128 + kOCols) * kTiles;
   extern __shared__ uint8_t smem_raw[];
   TcSmem<kTiles> &sm = *reinterpret_cast<TcSmem<kTiles> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -646,7 +655,9 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   }
-  // this warp's copies of those windows, before its first barrier
+  for (int c = threadIdx.x; c < (int)kOnesBytes / 4; c += tc_threads(kTiles))
+    reinterpret_cast<uint32_t *>(sm.ones)[c] = 0x3f803f80u;
+  // this warp's copies of those windows (and its ones), before its first barrier
   auto filled = [] {
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     ptx::fence_proxy_async_smem();
@@ -773,14 +784,18 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     } else {
       constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
-      constexpr uint32_t idO = ptx::idesc_bf16(128, 64, true);
+      constexpr uint32_t idO = ptx::idesc_bf16(128, kOCols, true);
       constexpr uint64_t kTileStep = kTcTileBytes >> 4;
+      // B of P V: 16 keys of V, and its columns 64 .. 79 at an offset (LBO) that
+      // leads to the ones from any window and key step: as the address grows,
+      // the offset shrinks
+      constexpr uint64_t kVUnit = 1 - ((uint64_t)1 << 16);
       const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0]));
-      const uint64_t dv = ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]));
-      const bool leader = lane == 0;
+      const uint64_t dv =
+          ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]), ptx::smem_addr(sm.ones) - ptx::smem_addr(sm.v[0]));
       filled();
       auto issue_s = [&](int t, int st) {
-        if (!leader) return;
+        if (!ptx::elect_one()) return;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           ptx::mma_f16_ts(tmem + 128 * t, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk,
@@ -788,11 +803,11 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         ptx::mma_commit(&sm.bar_s[t]);
       };
       auto issue_o = [&](int t, int st, bool acc) {
-        if (!leader) return;
+        if (!ptx::elect_one()) return;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_f16_ts(tmem + kColO + 64 * t, tmem + 128 * t + 8 * kk, dv + st * kTileStep + 128 * kk,
-                          idO, (acc || kk > 0) ? 1u : 0u);
+          ptx::mma_f16_ts(tmem + kColO + kOCols * t, tmem + 128 * t + 8 * kk,
+                          dv + (st * kTileStep + 128 * kk) * kVUnit, idO, (acc || kk > 0) ? 1u : 0u);
       };
       for (int pass = 0;; ++pass) {
         ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
@@ -817,7 +832,8 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
             }
           }
         }
-        if (leader) ptx::mma_commit(&sm.bar_done);
+        if (ptx::elect_one()) ptx::mma_commit(&sm.bar_done);
+        __syncwarp();
         wait(&sm.bar_done, pass & 1);
         if (!run_again(pass)) break;
       }
@@ -836,7 +852,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       }
     } else {
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + 64 * i;
+      const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + kOCols * i;
       ptx::tmem_st32(tmem + lane_base + kColQ + 32 * i, qw);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -930,6 +946,13 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
               for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
               ptx::tmem_st32(tO + 32 * hlf, o);
             }
+            uint32_t sum[16];  // of the rounded weights, in each column
+            ptx::tmem_ld16(tO + kD, sum);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence16(sum);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum[c] = __float_as_uint(__uint_as_float(sum[c]) * alpha);
+            ptx::tmem_st16(tO + kD, sum);
           }
           if (n >= w_ragged) {
             uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
@@ -958,12 +981,17 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       }
       ptx::tc_fence_after();
       uint32_t o[64];
+      float l_rounded = 0.f;
       if (n_win > 0) {
+        uint32_t sum[16];
         ptx::tmem_ld32(tO, o);
         ptx::tmem_ld32(tO + 32, o + 32);
+        ptx::tmem_ld16(tO + kD, sum);
         ptx::tmem_wait_ld();
         ptx::reg_fence32(o);
         ptx::reg_fence32(o + 32);
+        ptx::reg_fence16(sum);
+        l_rounded = __uint_as_float(sum[0]);
       } else {
 #pragma unroll
         for (int c = 0; c < 64; ++c) o[c] = 0u;
@@ -990,7 +1018,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       const bool direct = part.direct(lim);
       if (valid && direct && split == 0) {
         const bool none = lim == 0;
-        const float inv = none ? 0.f : 1.f / l;
+        const float inv = none ? 0.f : 1.f / l_rounded;
         uint4 *dst = reinterpret_cast<uint4 *>(out + row * kD);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -1005,10 +1033,12 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       } else if (valid && !direct) {
         const int64_t pi = row * part.ns + split;
         float4 *dst = reinterpret_cast<float4 *>(part.o + pi * kD);
+        const float to_l = l_rounded > 0.f ? l / l_rounded : 1.f;  // the merge divides by l
 #pragma unroll
         for (int c = 0; c < 16; ++c)
-          dst[c] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                               __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+          dst[c] = make_float4(__uint_as_float(o[4 * c]) * to_l, __uint_as_float(o[4 * c + 1]) * to_l,
+                               __uint_as_float(o[4 * c + 2]) * to_l,
+                               __uint_as_float(o[4 * c + 3]) * to_l);
         part.ml[pi] = make_float2(m_run, l);
       }
     }

@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
     int kn = 0, t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the next head
-        if (kn > 0 && lane == 0) ptx::mma_commit(&sm.k_free[(kn - 1) % kKBuf]);
+        if (kn > 0 && ptx::elect_one()) ptx::mma_commit(&sm.k_free[(kn - 1) % kKBuf]);
+        __syncwarp();
         wait(&sm.k_full[kn % kKBuf], (kn / kKBuf) & 1);
         ++kn;
       }
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
         const int buf = hseq & 1;
         if (hseq >= 2) wait(&sm.s_free[buf], ((hseq >> 1) - 1) & 1);
         ptx::tc_fence_after();
-        if (lane == 0) {
+        if (ptx::elect_one()) {
           const uint64_t ak = dk + ((kn - 1) % kKBuf) * 2 * kTileStep, bq = dq + (st * 2 + hf) * kTileStep;
 #pragma unroll
           for (int i = 0; i < 2; ++i)

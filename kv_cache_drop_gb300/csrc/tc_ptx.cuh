@@ -133,6 +133,17 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
                : "memory");
 }
 
+// One lane of a converged warp, the same every time.  The compiler knows that a
+// branch on it holds one thread and passes an MMA's operands on as they are; in
+// a branch on lane == 0 it must first make them uniform, and an MMA takes 56 to
+// 60 clocks to issue however small it is (measured: M 128, N 64, K 16 back to
+// back 36 clocks instead of 60; N 128 bound by the tensor core either way, 68).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\nselp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- MMA (one thread) ----
 // D[tmem] (+)= A[smem] * B[smem], kind::f16 (bf16/fp16 inputs, fp32 accumulate)
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
