@@ -536,24 +536,33 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // bf16, more rows: tcgen05.  CTA = kTiles tiles of 128 packed rows of one KV
 // head (both read the same K/V windows) x one key split.
 //   warps 4 i .. 4 i + 3  softmax of tile i (thread = packed row = TMEM lane)
-//   then the producer warps: 128-key K and V windows through a ring of stages,
-//        gathered by 16-byte cp.async into the 128-byte-swizzled layout that
-//        the MMA reads.  (TMA gathers of four rows deliver one 128-byte row
-//        per 24 clocks: 353 TFLOP/s at 1,024 rows over 16,384 entries.)
+//   then the producer warps: K and V windows of 96 keys through a ring of
+//        stages, gathered by 16-byte cp.async into the 128-byte-swizzled layout
+//        that the MMA reads.  (TMA gathers of four rows deliver one 128-byte
+//        row per 24 clocks: 353 TFLOP/s at 1,024 rows over 16,384 entries.)
 //   then the MMA warp: TMEM allocation, one thread issuing tcgen05.mma
-// TMEM columns: S_i [128 i, + 128), O_i [128 kTiles + 80 i, + 80), Q_i
-// [208 kTiles + 32 i, + 32).  Q_i (bf16 pairs) is the A operand of S_i = Q_i
-// K^T; P_i overwrites the first 64 columns of S_i as bf16 pairs and is the A
-// operand of O_i += P_i V.  bf16 throughout, because A and B of one MMA have
-// one type and the pool is bf16.  Two row sums: the softmax threads add the
-// unrounded weights, so that the log-sum-exp is good to fp32, and V has 16 more
-// columns of ones (a 2 KB tile that every window's last columns point at), so
-// that the MMA adds the rounded ones.  The output is divided by that second
-// sum: an average of V rows whose weights sum to 1, so that where few entries
-// carry a row the rounding of their weights hardly shows (error against 64 bits
-// 2.3e-3 -> 1.8e-3 on a mixed batch, of which the output's own rounding is 1.6e-3).
-// Per window the MMA thread issues O_0 += P_0 V, S_0 of the next window, then
-// the same for tile 1: one tile's softmax runs beside the other's MMAs.
+// TMEM columns: three (one tile: one) score buffers of 96, then O_i (80 each),
+// then Q_i (32 each).  Q_i (bf16 pairs) is the A operand of S_i = Q_i K^T; P_i
+// overwrites the first 48 columns of its S_i as bf16 pairs and is the A operand
+// of O_i += P_i V.  bf16 throughout, because A and B of one MMA have one type
+// and the pool is bf16.  Two row sums: the softmax threads add the unrounded
+// weights, so that the log-sum-exp is good to fp32, and V has 16 more columns of
+// ones (a 2 KB tile that every window's last columns point at), so that the MMA
+// adds the rounded ones.  The output is divided by that second sum: an average
+// of V rows whose weights sum to 1, so that where few entries carry a row the
+// rounding of their weights hardly shows (error against 64 bits 2.3e-3 ->
+// 1.8e-3 on a mixed batch, of which the output's own rounding is 1.6e-3).
+//
+// With two tiles the MMA thread issues, per window, O_0 += P_0 V, S_1 of the
+// next window, O_1 += P_1 V, S_0 of the window after that: the third score
+// buffer lets a tile's scores be ready before its softmax asks for them, and 96
+// is the window that three buffers, two O and two Q leave room for in 512
+// columns (with 128 keys, two buffers and scores that wait for P V: 7.71
+// instead of 7.52 ms at 2 x 4,096 rows over 50k-70k entries, a mixed batch 185
+// instead of 170 us).  With copies, weights and most MMAs taken out in turn the
+// kernel ran at 5.0 ms (copies alone), 6.4 ms (no copies) and 4.1 ms (barriers,
+// TMEM loads and stores): what bounds it at 6.84 ms is the softmax threads'
+// chain of TMEM load, weights, TMEM store and barrier, lengthened by the copies.
 //
 // Hidden entries.  Windows from the first tile's limit on are masked per row.
 // There a weight of 0 would still turn a hidden infinity or NaN of V into
@@ -574,25 +583,34 @@ constexpr float kHuge = 1.2089258e24f;  // 2^80: a window's sum that was compute
 constexpr uint32_t kOnesBytes = 16 * kD * 2;
 constexpr uint32_t kOCols = kD + 16;  // V's columns and the ones
 
-constexpr int tc_stages(int tiles) { return tiles == 1 ? 3 : 5; }
-// Warps: the softmax groups (a warpgroup each), then the producers and the MMA
-// warp.  A softmax thread holds a row of 128 scores, so registers move from
-// the other warpgroups to these (setmaxnreg): with one tile 128 x 200 + 128 x
-// 56 = 256 x 128 launched, two CTAs per SM; with two tiles twice that, one CTA.
-// A warp's copies in flight are few (about 4 bytes per clock and warp), so all
-// warps that are left over are producers, and every warp takes part in the
-// first windows' copies.
-constexpr int tc_producers(int tiles) { return tiles == 1 ? 3 : 7; }
-constexpr int tc_threads(int tiles) { return 256 * tiles; }
-constexpr int kTcLaunchRegs = 128, kSoftmaxRegs = 200, kOtherRegs = 56;
-static_assert(kSoftmaxRegs + kOtherRegs == 2 * kTcLaunchRegs, "the shares add up to the launch's");
+constexpr int kWin = 96;                        // keys of a window
+constexpr uint32_t kWinBytes = kWin * kD * 2;   // of K, and of V
+constexpr int tc_stages(int tiles) { return tiles == 1 ? 4 : 6; }
+constexpr int tc_bufs(int tiles) { return tiles == 1 ? 1 : 3; }  // of scores
+// Warps: the softmax groups (a warpgroup each), then a warpgroup of three
+// producers and the MMA warp.  A softmax thread holds a row of 96 scores, so
+// registers move to these (setmaxnreg): with one tile 200 + 56 of 2 x 128
+// launched, two CTAs per SM; with two tiles 2 x 224 + 56 of 3 x 168, one CTA.
+// Three producers keep up, since they wait for no load (seven, and every
+// barrier with more warps: 7.14 instead of 6.87 ms for 2 x 4,096 rows over
+// 50k-70k entries, 360 instead of 351 us for 14 chunks of 32 over 50,000); the
+// first windows are copied by all warps.
+constexpr int kProducers = 3;
+constexpr int tc_threads(int tiles) { return 128 * tiles + 128; }
+constexpr int tc_launch_regs(int tiles) { return tiles == 1 ? 128 : 168; }
+constexpr int tc_softmax_regs(int tiles) { return tiles == 1 ? 200 : 224; }
+constexpr int kOtherRegs = 56;
+static_assert(tc_softmax_regs(1) + kOtherRegs == 2 * tc_launch_regs(1) &&
+                  2 * tc_softmax_regs(2) + kOtherRegs == 3 * tc_launch_regs(2),
+              "the shares add up to the launch's");
 
 template <int kTiles>
 struct __align__(1024) TcSmem {
-  uint8_t k[tc_stages(kTiles)][kTcTileBytes];
-  uint8_t v[tc_stages(kTiles)][kTcTileBytes];
+  uint8_t k[tc_stages(kTiles)][kWinBytes];
+  uint8_t v[tc_stages(kTiles)][kWinBytes];
   uint8_t ones[kOnesBytes];  // 16 keys
-  uint64_t bar_s[2], bar_done;
+  int idx[2 * tc_stages(kTiles)][kWin];  // list entries of windows to come
+  uint64_t bar_s[kTiles][2], bar_o[kTiles], bar_done;
   uint32_t tmem_base;
   uint32_t gave_up;  // a wait of this CTA ran out
   uint32_t odd;      // V windows held an infinity or NaN beside hidden entries
@@ -604,12 +622,13 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     chunk_tc_kernel(const ChunkBatch a, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
                     const ChunkParts part, uint32_t *status) {
   constexpr int kSt = tc_stages(kTiles), kFill = kTiles;
-  constexpr int kProducers = tc_producers(kTiles);
   constexpr int kProdWarp = 4 * kTiles, kMmaWarp = kProdWarp + kProducers;
   // a softmax group, the producers, the MMA warp
   constexpr int kBarPCount = 128 + 32 * kProducers + 32;
   constexpr uint32_t kCols = kTiles == 1 ? 256 : 512;
-  constexpr uint32_t kColO = 128 * kTiles, kColQ = (128 + kOCols) * kTiles;
+  constexpr int kBufs = tc_bufs(kTiles);
+  constexpr uint32_t kColO = kWin * kBufs, kColQ = kColO + kOCols * kTiles;
+  static_assert(kColQ + 32 * kTiles <= kCols, "TMEM columns");
   extern __shared__ uint8_t smem_raw[];
   TcSmem<kTiles> &sm = *reinterpret_cast<TcSmem<kTiles> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -627,18 +646,63 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   const int c0 = split * part.chunk;
   const int c1 = min(rq.limit((int)((r1 - 1) / grp)), c0 + part.chunk);
   if (split > 0 && c0 >= c1) return;  // the merge reads only splits with visible entries
-  const int n_win = c1 > c0 ? (c1 - c0 + kTcKeys - 1) / kTcKeys : 0;
+  const int n_win = c1 > c0 ? (c1 - c0 + kWin - 1) / kWin : 0;
   // first window with an entry hidden from a row of this CTA (or past c1)
-  const int w_ragged = max(0, min(rq.limit((int)(r0 / grp)), c1) - c0) / kTcKeys;
+  const int w_ragged = max(0, min(rq.limit((int)(r0 / grp)), c1) - c0) / kWin;
 
-  // Windows 0 .. kFill - 1, by all warps: step u of the 32 kFill steps is
-  // entries 4 (u % 32) .. + 3 of window u / 32, eight lanes each.
-  constexpr int kWarps = tc_threads(kTiles) / 32, kFillSteps = 32 * kFill / kWarps;
+  // this thread's packed row
+  const int i = warp >> 2;
+  const int64_t r = r0 + threadIdx.x;
+  const bool valid = warp < kProdWarp && r < r1;
+  const int lim = valid ? rq.limit((int)(r / grp)) : 0;
+  const int64_t row = valid ? (int64_t)(rq.q0 + (int)(r / grp)) * a.Hq + g * grp + (int)(r % grp) : 0;
+  uint32_t qw[32];  // read before copies are queued
+  if (warp < kProdWarp) {
+    const uint4 *src = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + row * kD);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      qw[4 * c] = x.x;
+      qw[4 * c + 1] = x.y;
+      qw[4 * c + 2] = x.z;
+      qw[4 * c + 3] = x.w;
+    }
+  }
+
+  // Windows 0 .. kFill - 1, by all warps: a step is four entries, eight lanes
+  // each.
+  constexpr int kWarps = tc_threads(kTiles) / 32, kFillSteps = kWin / 4 * kFill / kWarps;
+  static_assert(kFillSteps * kWarps * 4 == kWin * kFill, "whole steps");
   const int64_t pitch = (int64_t)a.Hkv * kD * 2;
   const int ch = lane & 7;
+  // A step of the producers' copies is four entries; this one takes kSteps from
+  // s0 on of every window (the other warps none).  It fetches their list entries
+  // itself, a ring of stages before the rows, by cp.async too: a plain load
+  // returns only after all copies queued before it, which held the copies to 2
+  // bytes per clock and warp instead of 12 (8.2 -> 7.7 ms with loads two windows
+  // ahead, 7.5 -> 7.2 ms without loads).
+  constexpr int kAll = kWin / 4, kSteps = (kAll + kProducers - 1) / kProducers, kRing = 2 * kSt;
+  static_assert(4 * kSteps <= 32, "a lane fetches one entry");
+  const int s0 = (warp - kProdWarp) * kSteps;
+  auto fetch = [&](int n) {
+    const int x = 4 * s0 + lane, j = c0 + n * kWin + x;
+    if (lane < 4 * kSteps && x < kWin && n < n_win && j < c1)
+      cp_async4(ptx::smem_addr(&sm.idx[n % kRing][x]), a.kv_indices + (int64_t)rq.beg + j);
+  };
   const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
   const char *vg = (const char *)a.v + (g * kD + ch * 8) * 2;
   {
+    // the producers' entries of the other stages: loads too, as no copies are
+    // queued yet
+    const bool producer = warp >= kProdWarp && warp < kMmaWarp;
+    const int own = 4 * s0 + lane;
+    int stage[kSt - kFill];
+    if (producer)
+#pragma unroll
+      for (int n = kFill; n < kSt; ++n) {
+        const int j = c0 + n * kWin + own;
+        stage[n - kFill] = own < kWin && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : 0;
+      }
     int fill[kFillSteps];
 #pragma unroll
     for (int e = 0; e < kFillSteps; ++e) {
@@ -653,6 +717,12 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       cp_async16(ptx::smem_addr(sm.k[0]) + to, kg + off, fill[e] >= 0);  // past the end: zeros
       cp_async16(ptx::smem_addr(sm.v[0]) + to, vg + off, fill[e] >= 0);
     }
+    if (producer) {
+#pragma unroll
+      for (int n = kFill; n < kSt; ++n)
+        if (lane < 4 * kSteps && own < kWin) sm.idx[n][own] = stage[n - kFill];
+      for (int n = kSt; n < kRing; ++n) fetch(n);
+    }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   }
   for (int c = threadIdx.x; c < (int)kOnesBytes / 4; c += tc_threads(kTiles))
@@ -664,26 +734,12 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     __syncwarp();
   };
 
-  // this thread's packed row
-  const int i = warp >> 2;
-  const int64_t r = r0 + threadIdx.x;
-  const bool valid = warp < kProdWarp && r < r1;
-  const int lim = valid ? rq.limit((int)(r / grp)) : 0;
-  const int64_t row = valid ? (int64_t)(rq.q0 + (int)(r / grp)) * a.Hq + g * grp + (int)(r % grp) : 0;
-  uint32_t qw[32];
-  if (warp < kProdWarp) {
-    const uint4 *src = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + row * kD);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      qw[4 * c] = x.x;
-      qw[4 * c + 1] = x.y;
-      qw[4 * c + 2] = x.z;
-      qw[4 * c + 3] = x.w;
-    }
-  }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) ptx::mbar_init(&sm.bar_s[s], 1);
+    for (int x = 0; x < kTiles; ++x) {
+      ptx::mbar_init(&sm.bar_s[x][0], 1);
+      ptx::mbar_init(&sm.bar_s[x][1], 1);
+      ptx::mbar_init(&sm.bar_o[x], 1);
+    }
     ptx::mbar_init(&sm.bar_done, 1);
     sm.gave_up = sm.odd = sm.again = 0u;
     ptx::fence_barrier_init();
@@ -709,41 +765,36 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   if (warp >= kProdWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp < kMmaWarp) {
-      // A window is 128 rows of K and of V, 16 bytes per lane and copy: step s
-      // copies entries 4 s .. 4 s + 3, eight lanes each, and producer warp p
-      // takes steps kSteps p .. of every window.  A lane's pool rows are loaded
-      // a window ahead.  A stage is refilled without a wait: generation n + 1 of
-      // the last tile's barrier completes only after its softmax has seen S(n),
-      // whose commit tracks P.V(n - 1), the last reader of that stage.  Each
-      // window is one group of copies (empty past the end), so that "window
-      // n + 1 has landed" is a count of groups still in flight.
-      constexpr int kSteps = (32 + kProducers - 1) / kProducers;
-      const int s0 = (warp - kProdWarp) * kSteps, key0 = 4 * s0 + (lane >> 3);
-      const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kTcTileBytes;
+      // A window is kWin rows of K and of V, 16 bytes per lane and copy, eight
+      // lanes a row.  A stage is refilled without a wait: when tile 0's barrier of
+      // window n opens, its softmax has seen S_0(n), whose commit tracks
+      // P.V(n - 1) of both tiles, the last readers of that window.  Each window is
+      // one group of copies (empty past the end), with the list entries of the
+      // window kSt further on, so that "window w has landed" is a count of
+      // groups still in flight.
+      const int key0 = 4 * s0 + (lane >> 3);
+      const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kWinBytes;
       const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
-      int nx[kSteps];
-      auto slots = [&](int n, int *row) {
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const int j = c0 + n * kTcKeys + key0 + 4 * s;
-          row[s] = s0 + s < 32 && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : -1;
-        }
-      };
-      auto copy = [&](int n, const int *row, bool commit = true) {
+      // steps [from, to) of window n
+      auto copy = [&](int n, int from, int to) {
         if (n < n_win) {
-          const uint32_t at = (n % kSt) * kTcTileBytes;
+          const uint32_t at = (n % kSt) * kWinBytes;
+          const int *entry = sm.idx[n % kRing] + key0;
+          const int left = c1 - (c0 + n * kWin + key0);
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
-            if (s0 + s < 32) {
-              const int64_t off = max(row[s], 0) * pitch;
-              const uint32_t to = at + s * 512 + (s & 1 ? sw1 : sw0);
-              cp_async16(kd + to, kg + off, row[s] >= 0);
-              cp_async16(vd + to, vg + off, row[s] >= 0);
+            if (s >= from && s < to && s0 + s < kAll) {
+              const bool listed = 4 * s < left;
+              const int slot = listed ? entry[4 * s] : 0;
+              const int64_t off = ((unsigned)slot < (unsigned)a.S ? slot : 0) * pitch;
+              const uint32_t to_ = at + s * 512 + (s & 1 ? sw1 : sw0);
+              cp_async16(kd + to_, kg + off, listed);
+              cp_async16(vd + to_, vg + off, listed);
             }
           }
         }
-        if (commit) asm volatile("cp.async.commit_group;\n" ::: "memory");
       };
+      auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
       // every window but the newest `pending` has landed and is visible to the
       // tensor core
       auto landed = [&](auto pending) {
@@ -751,41 +802,67 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         ptx::fence_proxy_async_smem();
         __syncwarp();
       };
-      {
-        int first[kSt - kFill][kSteps];
-#pragma unroll
-        for (int n = kFill; n < kSt; ++n) slots(n, first[n - kFill]);
-#pragma unroll
-        for (int n = kFill; n < kSt; ++n) copy(n, first[n - kFill]);
+      // the first pass's other stages: two before the first barrier, the rest
+      // behind it
+      constexpr int kEarly = kFill + 2;
+#pragma unroll 1
+      for (int n = kFill; n < kEarly; ++n) {
+        copy(n, 0, kSteps);
+        commit();
       }
       for (int pass = 0;; ++pass) {
-        slots(kSt, nx);
-        landed(std::integral_constant<int, kSt - kFill>());  // windows 0 .. kFill - 1
+        landed(std::integral_constant<int, kEarly - kFill>());  // windows 0 .. kFill - 1
         ptx::named_bar_sync(kBarP, kBarPCount);
         if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
+#pragma unroll 1
+        for (int n = kEarly; n < kSt; ++n) {
+          copy(n, 0, kSteps);
+          commit();
+        }
         for (int n = 0; n < n_win; ++n) {
-          if (n + 1 >= kFill) landed(std::integral_constant<int, kSt - 3>());  // window n + 1
-          ptx::named_bar_sync(kBarP, kBarPCount);
-          if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
-          if (n >= 1) {
-            int cur[kSteps];
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) cur[s] = nx[s];
-            slots(n + kSt, nx);
-            copy(n - 1 + kSt, cur);
+          if constexpr (kTiles == 1) {
+            landed(std::integral_constant<int, kSt - 3>());  // window n + 1
+            ptx::named_bar_sync(kBarP, kBarPCount);
+            if (n >= 1) {
+              copy(n - 1 + kSt, 0, kSteps);
+              fetch(n - 1 + 2 * kSt);
+              commit();
+            }
+          } else {
+            // a window's copies are issued in two parts, so that neither tile's
+            // barrier waits for all of them
+            constexpr int kPart = (kSteps + 1) / 2;
+            ptx::named_bar_sync(kBarP, kBarPCount);
+            if (n >= 2) copy(n - 2 + kSt, 0, kPart);
+            // window n + 2; the newest group is window max(kSt - 1, n - 3 + kSt)
+            if (n == 0) landed(std::integral_constant<int, kSt - 3>());
+            else if (n == 1) landed(std::integral_constant<int, kSt - 4>());
+            else landed(std::integral_constant<int, kSt - 5>());
+            ptx::named_bar_sync(kBarP + 1, kBarPCount);
+            if (n >= 2) {
+              copy(n - 2 + kSt, kPart, kSteps);
+              fetch(n - 2 + 2 * kSt);
+              commit();
+            }
           }
         }
         if (!run_again(pass)) break;
-        for (int n = 0; n < kSt; ++n) {  // the ring's first fill once more, by the producers alone
-          slots(n, nx);
-          copy(n, nx, n >= kFill - 1);
+        // the ring's first fill once more, by the producers alone
+#pragma unroll 1
+        for (int n = 0; n < kRing; ++n) fetch(n);
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        __syncwarp();
+#pragma unroll 1
+        for (int n = 0; n < kEarly; ++n) {
+          copy(n, 0, kSteps);
+          if (n >= kFill - 1) commit();
         }
       }
       asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     } else {
-      constexpr uint32_t idS = ptx::idesc_bf16(128, 128, false);
+      constexpr uint32_t idS = ptx::idesc_bf16(128, kWin, false);
       constexpr uint32_t idO = ptx::idesc_bf16(128, kOCols, true);
-      constexpr uint64_t kTileStep = kTcTileBytes >> 4;
+      constexpr uint64_t kTileStep = kWinBytes >> 4;
       // B of P V: 16 keys of V, and its columns 64 .. 79 at an offset (LBO) that
       // leads to the ones from any window and key step: as the address grows,
       // the offset shrinks
@@ -794,42 +871,46 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       const uint64_t dv =
           ptx::sdesc_sw128(ptx::smem_addr(sm.v[0]), ptx::smem_addr(sm.ones) - ptx::smem_addr(sm.v[0]));
       filled();
-      auto issue_s = [&](int t, int st) {
+      auto buf = [&](int t, int n) { return tmem + kWin * ((kTiles * n + t) % kBufs); };
+      auto issue_s = [&](int t, int n, int seq) {
+        const uint32_t s = buf(t, n), st = n % kSt;
         if (!ptx::elect_one()) return;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_ts(tmem + 128 * t, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk,
-                          idS, kk > 0);
-        ptx::mma_commit(&sm.bar_s[t]);
+          ptx::mma_f16_ts(s, tmem + kColQ + 32 * t + 8 * kk, dk + st * kTileStep + 2 * kk, idS, kk > 0);
+        ptx::mma_commit(&sm.bar_s[t][seq & 1]);
       };
-      auto issue_o = [&](int t, int st, bool acc) {
+      auto issue_o = [&](int t, int n) {
+        const uint32_t p = buf(t, n), st = n % kSt;
         if (!ptx::elect_one()) return;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_f16_ts(tmem + kColO + kOCols * t, tmem + 128 * t + 8 * kk,
-                          dv + (st * kTileStep + 128 * kk) * kVUnit, idO, (acc || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < kWin / 16; ++kk)
+          ptx::mma_f16_ts(tmem + kColO + kOCols * t, p + 8 * kk,
+                          dv + (st * kTileStep + 128 * kk) * kVUnit, idO, (n > 0 || kk > 0) ? 1u : 0u);
+        ptx::mma_commit(&sm.bar_o[t]);
       };
       for (int pass = 0;; ++pass) {
-        ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, window 0 landed
+        const int seq = pass * n_win;  // of window 0
+        ptx::named_bar_sync(kBarP, kBarPCount);  // Q_0 in TMEM, the first windows landed
         if (kTiles == 2) ptx::named_bar_sync(kBarP + 1, kBarPCount);
         ptx::tc_fence_after();
         if (n_win > 0) {
-          issue_s(0, 0);
-          if (two) issue_s(1, 0);
+          issue_s(0, 0, seq);
+          if (two) issue_s(kTiles - 1, 0, seq);
+          if (kTiles == 2 && n_win > 1) issue_s(0, 1, seq + 1);
         }
         for (int n = 0; n < n_win; ++n) {
-          const int st = n % kSt, st1 = (n + 1) % kSt;
-          ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM, window n + 1 landed
+          ptx::named_bar_sync(kBarP, kBarPCount);  // P_0(n) in TMEM
           ptx::tc_fence_after();
-          issue_o(0, st, n > 0);
-          if (n + 1 < n_win) issue_s(0, st1);
-          if (kTiles == 2) {
-            ptx::named_bar_sync(kBarP + 1, kBarPCount);
+          issue_o(0, n);
+          if (kTiles == 1) {
+            if (n + 1 < n_win) issue_s(0, n + 1, seq + n + 1);
+          } else {
+            if (two && n + 1 < n_win) issue_s(kTiles - 1, n + 1, seq + n + 1);
+            ptx::named_bar_sync(kBarP + 1, kBarPCount);  // P_1(n) in TMEM, window n + 2 landed
             ptx::tc_fence_after();
-            if (two) {
-              issue_o(1, st, n > 0);
-              if (n + 1 < n_win) issue_s(1, st1);
-            }
+            if (two) issue_o(kTiles - 1, n);
+            if (n + 2 < n_win) issue_s(0, n + 2, seq + n + 2);
           }
         }
         if (ptx::elect_one()) ptx::mma_commit(&sm.bar_done);
@@ -839,7 +920,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(tc_softmax_regs(kTiles)));
     if (i == 1 && !two) {
       // no row in this tile: only the barriers
       filled();
@@ -852,7 +933,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       }
     } else {
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + lane_base + 128 * i, tO = tmem + lane_base + kColO + kOCols * i;
+      const uint32_t tS0 = tmem + lane_base, tO = tmem + lane_base + kColO + kOCols * i;
       ptx::tmem_st32(tmem + lane_base + kColQ + 32 * i, qw);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -863,39 +944,41 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       // maximum: the first window's maximum, raised by l's exponent whenever l
       // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference far
       // below the maximum costs nothing, and the windows after the first need
-      // no maximum (9,210 -> 8,604 us for 2 x 4,096 rows over 50k-70k entries).
+      // no maximum (9.2 -> 8.6 ms for 2 x 4,096 rows over 50k-70k entries).
       // If a window's weights sum to 2^80 or more (its scores jump by 55 over
       // all before it), the whole CTA runs once more with exact maxima.
       float m_run = -INFINITY, l = 0.f;
       for (int pass = 0;; ++pass) {
         bool huge = false;
         for (int n = 0; n < n_win; ++n) {
-          wait(&sm.bar_s[i], (pass * n_win + n) & 1);
+          const int seq = pass * n_win + n;
+          wait(&sm.bar_s[i][seq & 1], (seq >> 1) & 1);
           ptx::tc_fence_after();
+          const uint32_t tS = tS0 + kWin * ((kTiles * n + i) % kBufs);
           float alpha = 1.f;  // what the sums so far are scaled by
           if (l > kRaise) {
             const int e = min(127, (int)(__float_as_uint(l) >> 23) - 127);
             m_run += (float)e;
             alpha = __uint_as_float((uint32_t)(127 - e) << 23);
           }
-          uint32_t sr[128];
+          uint32_t sr[kWin];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
+          for (int c = 0; c < kWin / 32; ++c) ptx::tmem_ld32(tS + 32 * c, sr + 32 * c);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::reg_fence32(sr + 32 * c);
+          for (int c = 0; c < kWin / 32; ++c) ptx::reg_fence32(sr + 32 * c);
           if (pass > 0 || n >= w_ragged || __any_sync(0xffffffffu, m_run == -INFINITY)) {
             if (n >= w_ragged) {
-              const int seen = min(lim, c1) - (c0 + n * kTcKeys);
+              const int seen = min(lim, c1) - (c0 + n * kWin);
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
+              for (int c = 0; c < kWin; ++c)
                 if (c >= seen) sr[c] = 0xff800000u;  // -inf
             }
             float mx8[8];
 #pragma unroll
             for (int k8 = 0; k8 < 8; ++k8) mx8[k8] = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 128; c += 16)
+            for (int c = 0; c < kWin; c += 16)
 #pragma unroll
               for (int k8 = 0; k8 < 8; ++k8)
                 mx8[k8] =
@@ -917,7 +1000,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int qtr = 0; qtr < 4; ++qtr) {
+          for (int qtr = 0; qtr < kWin / 32; ++qtr) {
             uint32_t pw[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -935,7 +1018,8 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           huge |= !(lw < kHuge);
           l = fmaf(l, alpha, lw);
           if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // P.V(n - 1) has completed: the commit that signalled S(n) tracks it
+            wait(&sm.bar_o[i], (seq - 1) & 1);  // P.V(n - 1)
+            ptx::tc_fence_after();
 #pragma unroll
             for (int hlf = 0; hlf < 2; ++hlf) {
               uint32_t o[32];
@@ -956,7 +1040,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           }
           if (n >= w_ragged) {
             uint4 *v4 = reinterpret_cast<uint4 *>(sm.v[n % kSt]);
-            for (int c = threadIdx.x & 127; c < (int)(kTcTileBytes / 16); c += 128) {
+            for (int c = threadIdx.x & 127; c < (int)(kWinBytes / 16); c += 128) {
               const uint4 x = v4[c];
               const uint4 y = make_uint4(finite_or_zero(x.x), finite_or_zero(x.y), finite_or_zero(x.z),
                                          finite_or_zero(x.w));
@@ -997,7 +1081,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         for (int c = 0; c < 64; ++c) o[c] = 0u;
       }
       if (*(volatile uint32_t *)&sm.odd && valid) {
-        for (int j = c0 + w_ragged * kTcKeys; j < min(lim, c1); ++j) {
+        for (int j = c0 + w_ragged * kWin; j < min(lim, c1); ++j) {
           const uint4 *src = reinterpret_cast<const uint4 *>(
               (const __nv_bfloat16 *)a.v + (chunk_slot(a, rq, j) * a.Hkv + g) * kD);
 #pragma unroll
@@ -1080,14 +1164,14 @@ void split_keys(ChunkPlan *p, int64_t ctas, int64_t want, int64_t resident, int 
 }
 
 // Key splits of the tcgen05 kernels, from what their CTAs measured: `window`
-// us for 128 keys beside its neighbours, 6 us to start and end, and the
-// partials written and read at 5 TB/s.  The count that ends first when every
-// list is max_kv long: the splits then fill whole waves of CTAs (448 CTAs of
-// 196 windows instead of 896 of 128 and fewer: 1,078 -> 990 us for 14 chunks of
-// 64 over 50,000 entries).
+// us for 96 keys beside its neighbours, 8 us to start and end, and the partials
+// written and read at 5 TB/s in a merge of 6 us.  The count that ends first when
+// every list is max_kv long: the splits then fill whole waves of CTAs (448 CTAs
+// of 196 windows instead of 896 of 128 and fewer: 1,078 -> 990 us for 14 chunks
+// of 64 over 50,000 entries, at the time).
 void split_windows(ChunkPlan *p, int64_t ctas, int64_t slots, double window, double row_bytes,
                    int max_kv) {
-  const int windows = std::max(1, (max_kv + kTcKeys - 1) / kTcKeys);
+  const int windows = std::max(1, (max_kv + kWin - 1) / kWin);
   // at most eight waves, and four windows each
   const int most = (int)std::max<int64_t>(
       1, std::min<int64_t>(std::min(kMaxSplit, windows / 4), 8 * slots / std::max<int64_t>(1, ctas)));
@@ -1096,14 +1180,14 @@ void split_windows(ChunkPlan *p, int64_t ctas, int64_t slots, double window, dou
   for (int ns = 1; ns <= most; ++ns) {
     const int per = (windows + ns - 1) / ns;
     if (ns > 1 && per * (ns - 1) >= windows) continue;  // a split would be empty
-    const double t = (double)((ctas * ns + slots - 1) / slots) * (per * window + 6) +
-                     (ns > 1 ? 4 + ns * row_bytes / 5e6 : 0);
+    const double t = (double)((ctas * ns + slots - 1) / slots) * (per * window + 8) +
+                     (ns > 1 ? 6 + ns * row_bytes / 5e6 : 0);
     if (ns == 1 || t < best) {
       best = t;
       p->ns = ns;
     }
   }
-  p->chunk = (windows + p->ns - 1) / p->ns * kTcKeys;
+  p->chunk = (windows + p->ns - 1) / p->ns * kWin;
 }
 
 ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
@@ -1120,7 +1204,7 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, i
     p.kind = rows <= kTcRows ? kTcKind : kTcKind + 1;
     const int per_sm = p.kind == kTcKind ? 2 : 1, tile = p.kind == kTcKind ? kTcRows : 2 * kTcRows;
     p.tiles = (rows + tile - 1) / tile;
-    split_windows(&p, p.tiles * B * Hkv, (int64_t)per_sm * sms, p.kind == kTcKind ? 2.0 : 1.44,
+    split_windows(&p, p.tiles * B * Hkv, (int64_t)per_sm * sms, p.kind == kTcKind ? 1.4 : 0.8,
                   (double)n_rows * Hq * 528, max_kv);
   } else {
     p.kind = kF32Kind;
@@ -1157,12 +1241,12 @@ cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const Chunk
 template <int kTiles>
 cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                       int64_t tiles, uint32_t *status, cudaStream_t s) {
-  // the register shares hold for the launch's 128 only: an inc beyond them
-  // would wait forever
+  // the register shares hold for the launch's only: an inc beyond them would
+  // wait forever
   static const bool regs_ok = [] {
     cudaFuncAttributes at;
     return cudaFuncGetAttributes(&at, chunk_tc_kernel<kTiles>) == cudaSuccess &&
-           at.numRegs == kTcLaunchRegs;
+           at.numRegs == tc_launch_regs(kTiles);
   }();
   if (!regs_ok) return cudaErrorInvalidConfiguration;
   const int smem = (int)sizeof(TcSmem<kTiles>) + 1024;
