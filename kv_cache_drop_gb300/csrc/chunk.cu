@@ -309,7 +309,6 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (lse && threadIdx.x == 0) lse[w] = M * kLn2 + logf(L);
 }
 
-
 // ---------------------------------------------------------------------------
 // bf16, few rows (decode steps, short verification chunks): up to 16
 // packed rows per KV head.  CTA = key split x request, a warp per KV head (up
@@ -317,8 +316,9 @@ __global__ void __launch_bounds__(kMergeThreads)
 // values are gathered 16 rows at a time by 16-byte cp.async into an
 // XOR-swizzled tile, several tiles in flight; the packed rows are the rows of
 // m16n8k16 tiles: S = Q K^T with K as the B operand, P reused from the S
-// registers for P V.  Bound by the gather from HBM; tcgen05 would spend a
-// 128-row tile on 8 rows.
+// registers for P V.  Bound by the gather from HBM (14 decode steps over 20,000
+// to 90,000 entries, 64 / 8 heads: 236 us, 0.94 of the floor); tcgen05 would
+// spend a 128-row tile on 8 rows.
 // ---------------------------------------------------------------------------
 constexpr int kSSt = 3;  // K and V tiles per warp
 
@@ -339,37 +339,39 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   if (split > 0 && c0 >= c1) return;
   const int nk = max(0, c1 - c0), n_tiles = (nk + kSKeys - 1) / kSKeys;
   const uint32_t wsm = ptx::smem_addr(smem_raw) + warp * kSt * 2 * kSTile;
+  int *const idx = reinterpret_cast<int *>(smem_raw + (blockDim.x >> 5) * kSt * 2 * kSTile) +
+                   warp * 2 * kSt * kSKeys;
   uint8_t *const wsm_g = smem_raw + warp * kSt * 2 * kSTile;
 
-  // pool row of key `lane` of tile t, loaded a tile ahead of its use
-  auto load_slot = [&](int t) {
+  // List entries travel by cp.async too, a ring of stages before their rows: a
+  // plain load returns only after all copies queued before it (251 -> 236 us).
+  auto fetch = [&](int t) {
     const int k = t * kSKeys + lane;
-    return lane < kSKeys && k < nk ? (int)chunk_slot(a, rq, c0 + k) : 0;
+    if (lane < kSKeys && k < nk)
+      cp_async4(ptx::smem_addr(idx + t % (2 * kSt) * kSKeys + lane),
+                a.kv_indices + (int64_t)rq.beg + c0 + k);
   };
   const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + g * kD;
   const __nv_bfloat16 *vp = (const __nv_bfloat16 *)a.v + g * kD;
-  auto issue = [&](int t, int slot) {
+  auto issue = [&](int t) {
     if (t < n_tiles) {
       const uint32_t at = wsm + (t % kSt) * 2 * kSTile;
+      const int *entry = idx + t % (2 * kSt) * kSKeys;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = (lane >> 3) + 4 * i, ch = lane & 7;
-        const int sl = __shfl_sync(0xffffffffu, slot, key);
         const bool valid = t * kSKeys + key < nk;
-        const int64_t off = (int64_t)sl * a.Hkv * kD + ch * 8;
+        const int sl = valid ? entry[key] : 0;
+        const int64_t off = (int64_t)((unsigned)sl < (unsigned)a.S ? sl : 0) * a.Hkv * kD + ch * 8;
         cp_async16(at + tile_at(key, ch), kp + off, valid);
         cp_async16(at + kSTile + tile_at(key, ch), vp + off, valid);
       }
+      fetch(t + kSt);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
-  int slot_nx = load_slot(0);
 #pragma unroll
-  for (int t = 0; t < kSt - 1; ++t) {
-    const int sl = slot_nx;
-    slot_nx = load_slot(t + 1);
-    issue(t, sl);
-  }
+  for (int t = 0; t < kSt; ++t) fetch(t);
 
   // Q fragments and the rows' limits (relative to c0)
   uint32_t qa[4][4];
@@ -390,6 +392,11 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   }
   const int lim_min = rq.limit(0) - c0;  // the first token sees the least
 
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < kSt - 1; ++t) issue(t);
+
   float o[8][4], m[2], l[2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -397,9 +404,7 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   l[0] = l[1] = 0.f;
 
   for (int it = 0; it < n_tiles; ++it) {
-    const int sl = slot_nx;
-    slot_nx = load_slot(it + kSt);
-    issue(it + kSt - 1, sl);
+    issue(it + kSt - 1);
     asm volatile("cp.async.wait_group %0;\n" ::"n"(kSt - 1) : "memory");
     __syncwarp();
     const uint32_t kt = wsm + (it % kSt) * 2 * kSTile, vt = kt + kSTile;
@@ -1229,7 +1234,7 @@ cudaError_t launch_f32(const ChunkBatch &a, void *out, float *lse, const ChunkPa
 
 cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                          uint32_t *status, cudaStream_t s) {
-  const int warps = std::min(a.Hkv, kSHeads), smem = warps * kSSt * 2 * kSTile;
+  const int warps = std::min(a.Hkv, kSHeads), smem = warps * kSSt * 2 * (kSTile + kSKeys * 4);
   cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
