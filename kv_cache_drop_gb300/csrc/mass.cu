@@ -138,6 +138,18 @@ __global__ void __launch_bounds__(kFThreads, 2)
   }
 }
 
+// -lse in log2 units, for the tensor cores' scores; -inf for a row that counts
+// nothing.  The tensor core truncates its sums, which makes a score smaller by
+// 4.4e-8 of itself on average (measured at head dimension 64).  An lse from the
+// chunk's attention is smaller by as much, and the weights come out right; an lse
+// computed otherwise is not, and a weight near 1 loses 4.4e-8 of its score.  The
+// reference is lowered by half of that, so that neither is off by more than half
+// (an exact lse, 2 x 1,100-1,500 rows over 40k-56k entries: error against 64
+// bits 1.06e-6 -> 6.7e-7).
+__device__ __forceinline__ float log2_reference(float lse) {
+  return isinf(lse) ? -INFINITY : fmaf(-lse, kLog2e, lse * 3.17e-8f);
+}
+
 // ---------------------------------------------------------------------------
 // bf16, few rows (decode steps): up to 16 kRT packed rows per KV head.  CTA =
 // `chunk` list entries of a request and all KV heads, a warp per head (heads
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
           qa[rt][ks][2 + hh] = ok ? __ldg(src + ks * 8 + tig + 4) : 0u;
         }
         const float v = ok ? __ldg(ma.lse + row) : -INFINITY;
-        nl[rt][hh] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+        nl[rt][hh] = log2_reference(v);
         lim[rt][hh] = v == -INFINITY ? INT32_MIN : rq.limit(r / grp) - c0;
       }
     for (int it = 0; it < n_tiles; ++it) {
@@ -496,7 +508,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
       for (int u = 0; u < kLse; ++u) {
         const int x = 4 * qs0 + lane + 32 * u;
         if (lane + 32 * u < 4 * kQSteps && x < kQRows)
-          sm.nl[qn % kNlSt][x] = lse_nx[u] == -INFINITY ? -INFINITY : -lse_nx[u] * kLog2e;
+          sm.nl[qn % kNlSt][x] = log2_reference(lse_nx[u]);
       }
       landed(&sm.q_full[st]);
       if (++t == n_tiles) {
