@@ -357,6 +357,27 @@ def test_chunk_scores_that_jump(m, dtype):
         check_mass(bt, lse, None, 1.0, got, 0.0)
 
 
+@pytest.mark.parametrize("B,m,n", [(80, 30, 1500), (44, 40, 1500)])
+def test_chunk_scores_that_jump_late(B, m, n):
+    """A jump after a thousand entries of an unsplit list: the pass with exact
+    maxima starts over and walks the whole list again, every ring of copies
+    several times round."""
+    bt = Batch(20, [m] * B, [n] * B, 16, 4, "bf16")
+    rng = np.random.default_rng(21)
+    pool = np.zeros((bt.S, 4, 64), np.float32)
+    for b in range(B):
+        level = np.full(n, -3.0)
+        level[1200 + b % 97] = 2 + (b % 3) / 2
+        if b % 4 == 1:
+            level[: 200 + b] = -1.5
+        pool[bt.idx[bt.kv_ptr[b]:bt.kv_ptr[b + 1]]] = level[:, None, None] + 0.05 * rng.standard_normal((n, 4, 64))
+    q = (4 + 0.05 * rng.standard_normal((m * B, 16, 64))).astype(np.float32)
+    bt.q, bt.k = workloads.bf16_bits(q), workloads.bf16_bits(pool)
+    d = bt.device()
+    out, lse = run_chunk(bt, d)
+    check_chunk(bt, out, lse)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("more", [500, 4000])
 @pytest.mark.parametrize("m", [2, 10, 40, 300])
