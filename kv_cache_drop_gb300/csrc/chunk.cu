@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // instead of 7.52 ms at 2 x 4,096 rows over 50k-70k entries, a mixed batch 185
 // instead of 170 us).  With copies, weights and most MMAs taken out in turn the
 // kernel ran at 5.0 ms (copies alone), 6.4 ms (no copies) and 4.1 ms (barriers,
-// TMEM loads and stores): what bounds it at 6.84 ms is the softmax threads'
+// TMEM loads and stores): what bounds it, 6.4 ms now, is the softmax threads'
 // chain of TMEM load, weights, TMEM store and barrier, lengthened by the copies.
 //
 // Hidden entries.  Windows from the first tile's limit on are masked per row.
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   // each.
   constexpr int kWarps = tc_threads(kTiles) / 32, kFillSteps = kWin / 4 * kFill / kWarps;
   static_assert(kFillSteps * kWarps * 4 == kWin * kFill, "whole steps");
-  const int64_t pitch = (int64_t)a.Hkv * kD * 2;
+  const uint32_t pitch = (uint32_t)a.Hkv * kD * 2;
   const int ch = lane & 7;
   // A step of the producers' copies is four entries; this one takes kSteps from
   // s0 on of every window (the other warps none).  It fetches their list entries
@@ -686,12 +686,12 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   // returns only after all copies queued before it, which held the copies to 2
   // bytes per clock and warp instead of 12 (8.2 -> 7.7 ms with loads two windows
   // ahead, 7.5 -> 7.2 ms without loads).
-  constexpr int kAll = kWin / 4, kSteps = (kAll + kProducers - 1) / kProducers, kRing = 2 * kSt;
-  static_assert(4 * kSteps <= 32, "a lane fetches one entry");
+  constexpr int kSteps = kWin / 4 / kProducers, kRing = 2 * kSt;
+  static_assert(4 * kSteps * kProducers == kWin && 4 * kSteps <= 32, "a lane fetches one entry");
   const int s0 = (warp - kProdWarp) * kSteps;
   auto fetch = [&](int n) {
     const int x = 4 * s0 + lane, j = c0 + n * kWin + x;
-    if (lane < 4 * kSteps && x < kWin && n < n_win && j < c1)
+    if (lane < 4 * kSteps && n < n_win && j < c1)
       cp_async4(ptx::smem_addr(&sm.idx[n % kRing][x]), a.kv_indices + (int64_t)rq.beg + j);
   };
   const char *kg = (const char *)a.k + (g * kD + ch * 8) * 2;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
 #pragma unroll
       for (int n = kFill; n < kSt; ++n) {
         const int j = c0 + n * kWin + own;
-        stage[n - kFill] = own < kWin && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : 0;
+        stage[n - kFill] = lane < 4 * kSteps && n < n_win && j < c1 ? (int)chunk_slot(a, rq, j) : 0;
       }
     int fill[kFillSteps];
 #pragma unroll
@@ -718,14 +718,14 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     for (int e = 0; e < kFillSteps; ++e) {
       const int x = 4 * (warp * kFillSteps + e) + (lane >> 3);  // row of the windows, one after the other
       const uint32_t to = x * 128 + ((ch ^ (x & 7)) << 4);
-      const int64_t off = max(fill[e], 0) * pitch;
+      const uint64_t off = (uint64_t)max(fill[e], 0) * pitch;
       cp_async16(ptx::smem_addr(sm.k[0]) + to, kg + off, fill[e] >= 0);  // past the end: zeros
       cp_async16(ptx::smem_addr(sm.v[0]) + to, vg + off, fill[e] >= 0);
     }
     if (producer) {
 #pragma unroll
       for (int n = kFill; n < kSt; ++n)
-        if (lane < 4 * kSteps && own < kWin) sm.idx[n][own] = stage[n - kFill];
+        if (lane < 4 * kSteps) sm.idx[n][own] = stage[n - kFill];
       for (int n = kSt; n < kRing; ++n) fetch(n);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -778,26 +778,32 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       // window kSt further on, so that "window w has landed" is a count of
       // groups still in flight.
       const int key0 = 4 * s0 + (lane >> 3);
-      const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128, vd = kd + kSt * kWinBytes;
+      const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128;
       const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
       // steps [from, to) of window n
       auto copy = [&](int n, int from, int to) {
-        if (n < n_win) {
-          const uint32_t at = (n % kSt) * kWinBytes;
-          const int *entry = sm.idx[n % kRing] + key0;
-          const int left = c1 - (c0 + n * kWin + key0);
+        if (n >= n_win) return;
+        const uint32_t at = (n % kSt) * kWinBytes, k0 = kd + at + sw0, k1 = kd + at + sw1;
+        const int *entry = sm.idx[n % kRing] + key0;
+        const int left = c1 - (c0 + n * kWin + key0);
+        // whole windows without the tests of a last one, and rows at 32 x 32-bit
+        // products: the producers' instructions compete with the softmax warps'
+        // (6.88 -> 6.39 ms for 2 x 4,096 rows over 50k-70k entries)
+        auto steps = [&](auto whole) {
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
-            if (s >= from && s < to && s0 + s < kAll) {
-              const bool listed = 4 * s < left;
-              const int slot = listed ? entry[4 * s] : 0;
-              const int64_t off = ((unsigned)slot < (unsigned)a.S ? slot : 0) * pitch;
-              const uint32_t to_ = at + s * 512 + (s & 1 ? sw1 : sw0);
-              cp_async16(kd + to_, kg + off, listed);
-              cp_async16(vd + to_, vg + off, listed);
+            if (s >= from && s < to) {
+              const bool listed = decltype(whole)::value || 4 * s < left;
+              const uint32_t slot = listed ? entry[4 * s] : 0;
+              const uint64_t off = (uint64_t)(slot < (uint32_t)a.S ? slot : 0u) * pitch;
+              const uint32_t dst = (s & 1 ? k1 : k0) + s * 512;
+              cp_async16(dst, kg + off, listed);
+              cp_async16(dst + kSt * kWinBytes, vg + off, listed);
             }
           }
-        }
+        };
+        if (c0 + (n + 1) * kWin <= c1) steps(std::true_type());
+        else steps(std::false_type());
       };
       auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
       // every window but the newest `pending` has landed and is visible to the
@@ -952,19 +958,26 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       // no maximum (9.2 -> 8.6 ms for 2 x 4,096 rows over 50k-70k entries).
       // If a window's weights sum to 2^80 or more (its scores jump by 55 over
       // all before it), the whole CTA runs once more with exact maxima.
-      float m_run = -INFINITY, l = 0.f;
+      float m_run = -INFINITY, l = 0.f, neg = 0.f;  // neg: -m_run, 0 while there is none
       for (int pass = 0;; ++pass) {
-        bool huge = false;
+        uint32_t s_col = kWin * i;
+        bool huge = false, fresh = true;  // rows that have no reference yet
         for (int n = 0; n < n_win; ++n) {
           const int seq = pass * n_win + n;
           wait(&sm.bar_s[i][seq & 1], (seq >> 1) & 1);
           ptx::tc_fence_after();
-          const uint32_t tS = tS0 + kWin * ((kTiles * n + i) % kBufs);
+          const uint32_t tS = tS0 + s_col;
+          if (kBufs > 1) s_col = s_col == 0 ? 2 * kWin : s_col - kWin;  // buffer (2 n + i) % 3
           float alpha = 1.f;  // what the sums so far are scaled by
-          if (l > kRaise) {
-            const int e = min(127, (int)(__float_as_uint(l) >> 23) - 127);
-            m_run += (float)e;
-            alpha = __uint_as_float((uint32_t)(127 - e) << 23);
+          bool scaled = false;
+          if (__any_sync(0xffffffffu, l > kRaise)) {
+            if (l > kRaise) {
+              const int e = min(127, (int)(__float_as_uint(l) >> 23) - 127);
+              m_run += (float)e;
+              alpha = __uint_as_float((uint32_t)(127 - e) << 23);
+            }
+            neg = m_run == -INFINITY ? 0.f : -m_run;
+            scaled = true;
           }
           uint32_t sr[kWin];
 #pragma unroll
@@ -972,7 +985,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < kWin / 32; ++c) ptx::reg_fence32(sr + 32 * c);
-          if (pass > 0 || n >= w_ragged || __any_sync(0xffffffffu, m_run == -INFINITY)) {
+          if (fresh || n >= w_ragged) {
             if (n >= w_ragged) {
               const int seen = min(lim, c1) - (c0 + n * kWin);
 #pragma unroll
@@ -995,15 +1008,15 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
               alpha *= ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
               m_run = m_new;
             }
+            fresh = pass > 0 || __any_sync(0xffffffffu, m_run == -INFINITY);
+            neg = m_run == -INFINITY ? 0.f : -m_run;
+            scaled |= __any_sync(0xffffffffu, alpha != 1.f) != 0;
           }
-          const float mref = m_run == -INFINITY ? 0.f : m_run;
-          const float2 neg2 = make_float2(-mref, -mref);
-          // weights in fp32, summed as they are (in four chains, so that no
+          const float2 neg2 = make_float2(neg, neg);
+          // weights in fp32, summed as they are (in two chains, so that no
           // addition waits for the one before), rounded to bf16 pairs: word k
           // holds keys 2 k, 2 k + 1 and overwrites score column k, already read
-          float2 l4[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) l4[k] = make_float2(0.f, 0.f);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int qtr = 0; qtr < kWin / 32; ++qtr) {
             uint32_t pw[16];
@@ -1013,16 +1026,16 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
               const float2 x = __ffma2_rn(
                   make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), scale2, neg2);
               const float2 p = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
-              l4[k & 3] = __fadd2_rn(l4[k & 3], p);
+              l2[k & 1] = __fadd2_rn(l2[k & 1], p);
               pw[k] = pack2(p.x, p.y);
             }
             ptx::tmem_st16(tS + 16 * qtr, pw);
           }
-          const float2 la = __fadd2_rn(__fadd2_rn(l4[0], l4[1]), __fadd2_rn(l4[2], l4[3]));
+          const float2 la = __fadd2_rn(l2[0], l2[1]);
           const float lw = la.x + la.y;
           huge |= !(lw < kHuge);
           l = fmaf(l, alpha, lw);
-          if (n > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (n > 0 && scaled) {
             wait(&sm.bar_o[i], (seq - 1) & 1);  // P.V(n - 1)
             ptx::tc_fence_after();
 #pragma unroll
@@ -1065,7 +1078,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         if (valid && huge && pass == 0) *(volatile uint32_t *)&sm.again = 1u;
         if (!run_again(pass)) break;
         m_run = -INFINITY;
-        l = 0.f;
+        l = neg = 0.f;
         ptx::named_bar_sync(kBarP + i, kBarPCount);  // window 0 landed again
       }
       ptx::tc_fence_after();
