@@ -625,9 +625,9 @@ def akv_qk_norm_append(shp: Shape, n: int, q, k, v, pos, slot, k_pool, v_pool, q
     pool = (S, Hkv, D)
     _check(lib().akv_qk_norm_append(
         ctypes.byref(shp), n,
-        _typed("q", q, dt, dev, (n, Hq, D), True), q.stride(0) if n > 1 else Hq * D,
-        _typed("k", k, dt, dev, rows, True), k.stride(0) if n > 1 else Hkv * D,
-        _typed("v", v, dt, dev, rows, True), v.stride(0) if n > 1 else Hkv * D,
+        _typed("q", q, dt, dev, (n, Hq, D), True), q.stride()[0] if n > 1 else Hq * D,
+        _typed("k", k, dt, dev, rows, True), k.stride()[0] if n > 1 else Hkv * D,
+        _typed("v", v, dt, dev, rows, True), v.stride()[0] if n > 1 else Hkv * D,
         _typed("q_weight", q_weight, f32, dev, (D,)), _typed("k_weight", k_weight, f32, dev, (D,)),
         eps, flags, _typed("pos", pos, i32, dev, (n,)), _typed("slot", slot, i32, dev, (n,)), S,
         _typed("q_out", q_out, dt, dev, (n, Hq, D)), _typed("k_pool", k_pool, dt, dev, pool),
