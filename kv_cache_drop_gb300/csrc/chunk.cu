@@ -44,7 +44,8 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *dst, const 
 // Tensor cores take no fp32 operands; this path is for single-precision
 // parity, bound by the fp32 pipes and their shared-memory operands.  One CTA
 // per SM: held to 128 registers for two, it spills and takes 257 us instead of
-// 232 (3 chunks of 116-301 rows over 1,050-4,000 entries).
+// 232 (3 chunks of 116-301 rows over 1,050-4,000 entries; 230 with the list
+// entries of a step loaded before the step's scores).
 struct F32Smem {
   float q[kFRows][kFPitch], p[kFRows][kFPitch], k[kFKeys][kFPitch], v[kFKeys][kFPitch];
 };
@@ -71,14 +72,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
   int lim[8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    const int64_t r = r0 + ty + 16 * p;
-    lim[p] = r < r1 ? rq.limit((int)(r / grp)) : 0;
+    const int r = (int)r0 + ty + 16 * p;
+    lim[p] = r < r1 ? rq.limit(r / grp) : 0;
   }
   const auto commit = [] { asm volatile("cp.async.commit_group;\n" ::: "memory"); };
+  int own[kFOwn];
+  f32_rows(own, a, rq, c0, c1);
   f32_load_q(sm.q, a, rq, g, r0);
-  f32_load_kv(sm.k, a.k, a, rq, g, c0, c1);
+  f32_load_kv(sm.k, a.k, a, g, own);
   commit();
-  f32_load_kv(sm.v, a.v, a, rq, g, c0, c1);
+  f32_load_kv(sm.v, a.v, a, g, own);
   commit();
   float o[8][4], m[8], l[8];
 #pragma unroll
@@ -89,10 +92,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
   for (int j0 = c0; j0 < c1; j0 += kFKeys) {
     asm volatile("cp.async.wait_group 1;\n" ::: "memory");
     __syncthreads();  // K (and Q) landed
+    f32_rows(own, a, rq, j0 + kFKeys, c1);
     float s[8][4];
     f32_scores(sm.q, sm.k, ty, tx, s);
     __syncthreads();  // K's readers are done
-    f32_load_kv(sm.k, a.k, a, rq, g, j0 + kFKeys, c1);
+    f32_load_kv(sm.k, a.k, a, g, own);
     commit();
     const bool ragged = j0 + kFKeys > min(first, c1);
 #pragma unroll
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       }
     }
     __syncthreads();  // V's and P's readers are done
-    f32_load_kv(sm.v, a.v, a, rq, g, j0 + kFKeys, c1);
+    f32_load_kv(sm.v, a.v, a, g, own);
     commit();
   }
   asm volatile("cp.async.wait_group 0;\n" ::: "memory");

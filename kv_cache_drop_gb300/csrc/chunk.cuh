@@ -131,29 +131,35 @@ constexpr int kFThreads = 256;
 __device__ __forceinline__ void f32_load_q(float (*dst)[kFPitch], const ChunkBatch &a,
                                            const ChunkReq &rq, int g, int64_t r0) {
   const int grp = a.Hq / a.Hkv, c = threadIdx.x % 16;
-  const int64_t rows = (int64_t)rq.m * grp;
+  const int rows = rq.m * grp;  // 2^30 at most
   for (int x = threadIdx.x / 16; x < kFRows; x += kFThreads / 16) {
-    const int64_t r = r0 + x;
+    const int r = (int)r0 + x;
     const bool ok = r < rows;
-    const int i = ok ? (int)(r / grp) : 0, h = ok ? (int)(r % grp) : 0;
+    const int i = ok ? r / grp : 0, h = ok ? r - i * grp : 0;
     cp_async16(ptx::smem_addr(&dst[x][4 * c]),
                (const float *)a.q + ((int64_t)(rq.q0 + i) * a.Hq + g * grp + h) * kD + 4 * c, ok);
   }
 }
-// list entries j0 .. of a pool, KV head g (entries from `end` on: zeros)
+// Pool rows of this thread's entries from j0 on (-1 from `end` on).  Loaded well
+// before the copies that use them: a load returns only after all copies that
+// were queued before it.
+constexpr int kFOwn = kFKeys / (kFThreads / 16);
+__device__ __forceinline__ void f32_rows(int *row, const ChunkBatch &a, const ChunkReq &rq, int j0,
+                                         int end) {
+#pragma unroll
+  for (int e = 0; e < kFOwn; ++e) {
+    const int j = j0 + threadIdx.x / 16 + e * (kFThreads / 16);
+    row[e] = j < end ? (int)chunk_slot(a, rq, j) : -1;
+  }
+}
+// those rows of a pool, KV head g (zeros for -1)
 __device__ __forceinline__ void f32_load_kv(float (*dst)[kFPitch], const void *pool,
-                                            const ChunkBatch &a, const ChunkReq &rq, int g, int j0,
-                                            int end) {
+                                            const ChunkBatch &a, int g, const int *row) {
   const int c = threadIdx.x % 16, x0 = threadIdx.x / 16;
-  constexpr int kStep = kFThreads / 16;
-  int64_t row[kFKeys / kStep];  // all indices before the first copy
 #pragma unroll
-  for (int e = 0; e < kFKeys / kStep; ++e)
-    row[e] = j0 + x0 + e * kStep < end ? chunk_slot(a, rq, j0 + x0 + e * kStep) : -1;
-#pragma unroll
-  for (int e = 0; e < kFKeys / kStep; ++e)
-    cp_async16(ptx::smem_addr(&dst[x0 + e * kStep][4 * c]),
-               (const float *)pool + (max(row[e], (int64_t)0) * a.Hkv + g) * kD + 4 * c, row[e] >= 0);
+  for (int e = 0; e < kFOwn; ++e)
+    cp_async16(ptx::smem_addr(&dst[x0 + e * (kFThreads / 16)][4 * c]),
+               (const float *)pool + ((int64_t)max(row[e], 0) * a.Hkv + g) * kD + 4 * c, row[e] >= 0);
 }
 
 // acc[p][q] = q row . k row, even and odd dimensions in packed pairs: half the

@@ -67,21 +67,21 @@ __global__ void __launch_bounds__(kFThreads, 2)
   auto load_rows = [&](int buf, int g, int t) {
     f32_load_q(sm.q[buf], a, rq, g, (int64_t)t * kFRows);
     if (threadIdx.x < kFRows) {
-      const int r = t * kFRows + threadIdx.x;
-      // +inf: a row that saw nothing, or no row, weighs 0
-      float v = INFINITY;
-      if (r < rows) {
-        v = __ldg(ma.lse + (int64_t)(rq.q0 + r / grp) * a.Hq + g * grp + r % grp);
-        if (v == -INFINITY) v = INFINITY;
-      }
-      sm.lse[buf][threadIdx.x] = v;
+      const int r = t * kFRows + threadIdx.x, i = r / grp;
+      if (r < rows)
+        cp_async4(ptx::smem_addr(&sm.lse[buf][threadIdx.x]),
+                  ma.lse + (int64_t)(rq.q0 + i) * a.Hq + g * grp + (r - i * grp));
     }
   };
   Total sum[4];
   if (mine) load_rows(0, g, t);
   for (int it = 0; it < mine; ++it) {
     const int r0 = t * kFRows, buf = it & 1;
-    if (it == 0 || t == t0) f32_load_kv(sm.k, a.k, a, rq, g, j0, rq.n);
+    if (it == 0 || t == t0) {
+      int own[kFOwn];
+      f32_rows(own, a, rq, j0, rq.n);
+      f32_load_kv(sm.k, a.k, a, g, own);
+    }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
     if (++t == n_tiles) {
       t = t0;
@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kFThreads, 2)
     if (plain) {
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        const float v = sm.lse[buf][ty + 16 * p];
+        float v = sm.lse[buf][ty + 16 * p];
+        if (v == -INFINITY) v = INFINITY;  // a row that saw nothing weighs 0
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[q] += ptx::ex2(fmaf(s[p][q], 0.125f, -v) * kLog2e);
       }
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
       for (int p = 0; p < 8; ++p) {
         const int r = r0 + ty + 16 * p;
         const float v = sm.lse[buf][ty + 16 * p];
-        const int lim = r < rows && v != INFINITY ? rq.limit(r / grp) : 0;
+        const int lim = r < rows && !isinf(v) ? rq.limit(r / grp) : 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float w = ptx::ex2(fmaf(s[p][q], 0.125f, -v) * kLog2e);
