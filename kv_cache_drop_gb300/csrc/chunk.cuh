@@ -51,7 +51,7 @@ __device__ __forceinline__ void clear_status(uint32_t *status) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *status = 0u;
 }
 
-// ---- tensor cores: 128 packed rows x 128 keys ----
+// ---- tensor cores: 128 packed rows, key tiles of 128 (the mass; the attention has windows of its own) ----
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = 128;
 constexpr uint32_t kTcTileBytes = kTcKeys * kD * 2;      // one K or V window of a KV head
