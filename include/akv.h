@@ -534,7 +534,8 @@ akv_status akv_qk_norm_append(const akv_shape *shape, int32_t n, const void *q, 
  * (NaN, infinities) do not reach a row.  workspace: device, 256-byte
  * aligned, akv_chunk_workspace() bytes for the same arguments: the status word
  * and split-KV partials.  bf16: the weights are rounded to bf16 for the
- * P x V product; their sum and the scores are fp32. */
+ * P x V product; their sum and the scores are fp32.  So is the sum of the
+ * weighted values before its division: |v| up to 2^96 never leaves its range. */
 size_t akv_chunk_workspace(const akv_shape *shape, int32_t B, int32_t n_rows, int32_t max_q,
                            int32_t max_kv);
 akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t *q_indptr,

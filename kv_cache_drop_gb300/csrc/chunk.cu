@@ -588,6 +588,7 @@ constexpr int kBarAll = 2;       // all warps, after a pass
 constexpr float kRescale = 8.f;       // log2 units by which a maximum may pass the reference
 constexpr float kRaise = 65536.f;     // the row sum that raises it
 constexpr float kHuge = 1.2089258e24f;  // 2^80: a window's sum that was computed too far above it
+constexpr uint32_t kFar = 0x71800000u;  // 2^100's bits: an output sum that was
 
 constexpr uint32_t kOnesBytes = 16 * kD * 2;
 constexpr uint32_t kOCols = kD + 16;  // V's columns and the ones
@@ -958,12 +959,17 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
       // Weights are 2^(score - m_run) with m_run any reference, not the running
       // maximum: the first window's maximum, raised by l's exponent whenever l
       // has passed 2^16.  fp32 and bf16 hold 2^(+-126), so a reference far
-      // below the maximum costs nothing, and the windows after the first need
-      // no maximum (9.2 -> 8.6 ms for 2 x 4,096 rows over 50k-70k entries).
+      // below the maximum costs no precision, and the windows after the first
+      // need no maximum (9.2 -> 8.6 ms for 2 x 4,096 rows over 50k-70k entries).
       // If a window's weights sum to 2^80 or more (its scores jump by 55 over
-      // all before it), the whole CTA runs once more with exact maxima.
+      // all before it), or a row's output sums end at 2^100 or more, infinite
+      // or NaN (a smaller jump, but large values: their product left fp32's
+      // range, or would in the merge), the whole CTA runs once more with exact
+      // maxima.  No weight is above 1 then, and no sum above 2^17 values.
       float m_run = -INFINITY, l = 0.f, neg = 0.f;  // neg: -m_run, 0 while there is none
+      uint32_t o[64];  // output sums, after a pass
       for (int pass = 0;; ++pass) {
+        const float slack = pass > 0 ? 0.f : kRescale;
         uint32_t s_col = kWin * i;
         bool huge = false, fresh = true;  // rows that have no reference yet
         for (int n = 0; n < n_win; ++n) {
@@ -1008,7 +1014,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
             const float mx = fmaxf(ptx::max3(mx8[0], mx8[1], mx8[2]),
                                    fmaxf(ptx::max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
             const float m_new = fmaxf(m_run, mx * kScale);
-            if (m_new > m_run + kRescale) {
+            if (m_new > m_run + slack) {
               alpha *= ptx::ex2(m_run - m_new);  // 0 on the first raise from -inf
               m_run = m_new;
             }
@@ -1079,28 +1085,36 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
           ptx::named_bar_sync(kBarP + i, kBarPCount);
         }
         wait(&sm.bar_done, pass & 1);  // the last P.V
+        ptx::tc_fence_after();
+        if (n_win > 0) {
+          ptx::tmem_ld32(tO, o);
+          ptx::tmem_ld32(tO + 32, o + 32);
+          ptx::tmem_wait_ld();
+          ptx::reg_fence32(o);
+          ptx::reg_fence32(o + 32);
+          uint32_t top = 0u;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) top = max(top, o[c] & 0x7fffffffu);
+          huge |= top >= kFar;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) o[c] = 0u;
+        }
         if (valid && huge && pass == 0) *(volatile uint32_t *)&sm.again = 1u;
+        ptx::tc_fence_before();
         if (!run_again(pass)) break;
         m_run = -INFINITY;
         l = neg = 0.f;
         ptx::named_bar_sync(kBarP + i, kBarPCount);  // window 0 landed again
       }
       ptx::tc_fence_after();
-      uint32_t o[64];
       float l_rounded = 0.f;
       if (n_win > 0) {
         uint32_t sum[16];
-        ptx::tmem_ld32(tO, o);
-        ptx::tmem_ld32(tO + 32, o + 32);
         ptx::tmem_ld16(tO + kD, sum);
         ptx::tmem_wait_ld();
-        ptx::reg_fence32(o);
-        ptx::reg_fence32(o + 32);
         ptx::reg_fence16(sum);
         l_rounded = __uint_as_float(sum[0]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 64; ++c) o[c] = 0u;
       }
       if (*(volatile uint32_t *)&sm.odd && valid) {
         for (int j = c0 + w_ragged * kWin; j < min(lim, c1); ++j) {
