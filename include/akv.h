@@ -577,7 +577,8 @@ akv_status akv_attention_mass(const akv_shape *shape, int32_t B, const int32_t *
  * and out_pos hold, dropped_capacity: those of dropped (the length of
  * kv_indices always suffices); out_stride: masses that a row of out_mass
  * holds.  What would go past them is not written; the index pointers count it
- * all the same.  Outputs must not overlap inputs. */
+ * all the same; an output of no entries may be NULL.  Outputs must not overlap
+ * inputs. */
 akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t *kv_indices,
                              const int32_t *kv_pos, int32_t max_kv, const float *mass,
                              int64_t mass_stride, const int32_t *keep, int32_t n_first,

@@ -1423,10 +1423,12 @@ akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t 
   if (out_stride < 0 || out_capacity < 0 || dropped_capacity < 0)
     return fail(AKV_ERR_INVALID, "negative size");
   if (B == 0) return AKV_OK;
+  // an output of no entries may be NULL: nothing is written past its capacity
   if (!kv_indptr || !keep || !out_indptr || !dropped_indptr ||
-      (max_kv > 0 && (!kv_indices || !mass || !out_indices || !out_mass || !dropped)))
+      (max_kv > 0 && (!kv_indices || !mass || (out_capacity > 0 && !out_indices) ||
+                      (out_stride > 0 && !out_mass) || (dropped_capacity > 0 && !dropped))))
     return fail(AKV_ERR_INVALID, "NULL argument");
-  if (max_kv > 0 && (kv_pos == nullptr) != (out_pos == nullptr))
+  if (max_kv > 0 && (kv_pos ? out_capacity > 0 && !out_pos : out_pos != nullptr))
     return fail(AKV_ERR_INVALID, "kv_pos and out_pos are given together or not at all");
   if (max_kv > 0 && mass == out_mass)
     return fail(AKV_ERR_INVALID, "out_mass must not be mass");

@@ -74,3 +74,38 @@ def test_chunk_infinite_value_seen_by_all(m, dtype):
     rest = np.ones(o.shape, bool)
     rest[:, 4:8, 9] = rest[:, 8:12, 11] = False
     assert np.all((np.abs(o - want) <= tol)[rest])
+
+
+@pytest.mark.parametrize("lens", [[1], [700, 0, 33], [20000, 5]])
+def test_evict_exactly_sized_outputs(lens):
+    """Buffers of exactly the kept and dropped entries, the empty ones among
+    them (an empty tensor has no address)."""
+    torch = _torch()
+    rng = np.random.default_rng(67)
+    B, ptr = len(lens), np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    nnz, wide = int(ptr[-1]), max(lens)
+    idx, pos = (rng.permutation(nnz).astype(np.int32) for _ in range(2))
+    mass = rng.random((B, wide)).astype(np.float32)
+    i32 = lambda n: torch.full((n,), -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    for keep in (0, wide, wide // 3):
+        for with_pos in (True, False):
+            kept = [_evict_ref(mass[b], n, keep, 1, 1) for b, n in enumerate(lens)]
+            n_kept, width = sum(map(len, kept)), max(map(len, kept))
+            o_ptr, o_idx, d_ptr, drop = i32(B + 1), i32(n_kept), i32(B + 1), i32(nnz - n_kept)
+            o_pos = i32(n_kept) if with_pos else None
+            o_mass = torch.full((B, width), -9.0, device="cuda")
+            akv.akv_evict_by_mass(B, akv.i32_device(ptr), akv.i32_device(idx),
+                                  akv.i32_device(pos) if with_pos else None, wide,
+                                  torch.from_numpy(mass).cuda(), akv.i32_device([keep] * B), 1, 1, o_ptr,
+                                  o_idx, o_pos, o_mass, d_ptr, drop)
+            torch.cuda.synchronize()
+            at = np.concatenate([ptr[b] + k for b, k in enumerate(kept)]).astype(np.int64)
+            gone = np.concatenate([ptr[b] + np.setdiff1d(np.arange(lens[b]), k) for b, k in enumerate(kept)])
+            np.testing.assert_array_equal(o_idx.cpu().numpy(), idx[at])
+            np.testing.assert_array_equal(drop.cpu().numpy(), idx[gone.astype(np.int64)])
+            if with_pos:
+                np.testing.assert_array_equal(o_pos.cpu().numpy(), pos[at])
+            for b, k in enumerate(kept):
+                np.testing.assert_array_equal(o_mass[b, :len(k)].cpu().numpy(), mass[b, k])
+            assert o_ptr.tolist() == np.concatenate([[0], np.cumsum([len(k) for k in kept])]).tolist()
+            assert int(d_ptr[-1]) == nnz - n_kept
