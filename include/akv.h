@@ -494,8 +494,8 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
  * to no request are neither read nor written.  Row i of a chunk of m rows sees
  * the first n - m + i + 1 of the list's n entries (none if that is not
  * positive).  max_q, max_kv: host, upper bounds on the chunks' and lists'
- * lengths; longer ones are cut to them.  A pool index outside [0, S) reads
- * pool row 0.  All index data stays on the device, so the calls can be
+ * lengths; longer ones are cut to them.  kv_indices and the pools may be NULL
+ * where max_kv is 0.  A pool index outside [0, S) reads pool row 0.  All index data stays on the device, so the calls can be
  * captured in a CUDA graph and replayed with other lengths within the bounds.
  * A workspace serves one call at a time: calls that may overlap on the GPU
  * (two streams, two captured graphs) need one each.  Workspaces start with the

@@ -605,6 +605,12 @@ def _run_on(stream):
     return dev, stream.cuda_stream
 
 
+def _list_bound(kv_indices, max_kv: int) -> int:
+    """max_kv; 0 where no list has an entry, as an empty tensor has no address
+    to pass on."""
+    return max_kv if kv_indices.shape[0] else 0
+
+
 def _torch_dtype(shp: Shape):
     import torch
     return torch.bfloat16 if shp.dtype == AKV_BF16 else torch.float32
@@ -650,7 +656,7 @@ def akv_chunk_attention(shp: Shape, B: int, q_indptr, q, k_pool, v_pool, kv_indp
         _typed("q", q, dt, dev, (n, shp.Hq, D)), _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
         _typed("v_pool", v_pool, dt, dev, (S, shp.Hkv, D)), S,
         _typed("kv_indptr", kv_indptr, torch.int32, dev, (B + 1,)),
-        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), max_kv,
+        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), _list_bound(kv_indices, max_kv),
         _typed("out", out, dt, dev, (n, shp.Hq, D)),
         _typed("lse", lse, torch.float32, dev, (n, shp.Hq)),
         _typed("workspace", workspace, torch.uint8, dev),
@@ -673,7 +679,7 @@ def akv_attention_mass(shp: Shape, B: int, q_indptr, q, k_pool, kv_indptr, kv_in
         ctypes.byref(shp), B, _typed("q_indptr", q_indptr, torch.int32, dev, (B + 1,)), n, max_q,
         _typed("q", q, dt, dev, (n, shp.Hq, D)), _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
         S, _typed("kv_indptr", kv_indptr, torch.int32, dev, (B + 1,)),
-        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), max_kv,
+        _typed("kv_indices", kv_indices, torch.int32, dev, (None,)), _list_bound(kv_indices, max_kv),
         _typed("lse", lse, torch.float32, dev, (n, shp.Hq)), decay,
         _typed("mass_in", mass_in, torch.float32, dev, tuple(mass_out.shape)),
         _typed("mass_out", mass_out, torch.float32, dev, (B, None)), mass_out.shape[1],
@@ -693,7 +699,7 @@ def akv_evict_by_mass(B: int, kv_indptr, kv_indices, kv_pos, max_kv: int, mass, 
     _check(lib().akv_evict_by_mass(
         B, _typed("kv_indptr", kv_indptr, i32, dev, (B + 1,)),
         _typed("kv_indices", kv_indices, i32, dev, (None,)),
-        _typed("kv_pos", kv_pos, i32, dev, tuple(kv_indices.shape)), max_kv,
+        _typed("kv_pos", kv_pos, i32, dev, tuple(kv_indices.shape)), _list_bound(kv_indices, max_kv),
         _typed("mass", mass, f32, dev, (B, None)), mass.shape[1],
         _typed("keep", keep, i32, dev, (B,)), n_first, n_recent,
         _typed("out_indptr", out_indptr, i32, dev, (B + 1,)),

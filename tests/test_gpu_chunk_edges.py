@@ -109,3 +109,30 @@ def test_evict_exactly_sized_outputs(lens):
                 np.testing.assert_array_equal(o_mass[b, :len(k)].cpu().numpy(), mass[b, k])
             assert o_ptr.tolist() == np.concatenate([[0], np.cumsum([len(k) for k in kept])]).tolist()
             assert int(d_ptr[-1]) == nnz - n_kept
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 10, 40, 300])
+@pytest.mark.parametrize("S", [0, 5])
+def test_lists_without_entries_under_a_bound(S, m, dtype):
+    """kv_indices of no entries while max_kv allows some: rows see nothing,
+    nothing gains mass, nothing is kept or dropped."""
+    torch = _torch()
+    shp = akv.shape(16, 4, 64, dtype)
+    q = akv.to_device(_rand(np.random.default_rng(1), (2 * m, 16, 64), dtype), dtype)
+    pool, ptr, none = q.new_zeros(S, 4, 64), akv.i32_device([0, 0, 0]), akv.i32_device([])
+    qp = akv.i32_device([0, m, 2 * m])
+    out, lse = torch.full_like(q, 7.0), torch.zeros(2 * m, 16, device="cuda")
+    ws = torch.empty(akv.akv_chunk_workspace(shp, 2, 2 * m, m, 5000), dtype=torch.uint8, device="cuda")
+    akv.akv_chunk_attention(shp, 2, qp, q, pool, pool, ptr, none, m, 5000, out, lse, ws)
+    torch.cuda.synchronize()
+    assert not out.any() and bool(torch.isneginf(lse).all())
+    ws = torch.empty(akv.akv_attention_mass_workspace(shp, 2, 2 * m, m, 5000), dtype=torch.uint8,
+                     device="cuda")
+    mass = torch.full((2, 5000), -3.0, device="cuda")
+    akv.akv_attention_mass(shp, 2, qp, q, pool, ptr, none, m, 5000, lse, 0.5, mass, mass, ws)
+    o_ptr, d_ptr = (torch.full((3,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    akv.akv_evict_by_mass(2, ptr, none, none, 5000, mass, akv.i32_device([10, 0]), 1, 1, o_ptr, none, none,
+                          mass.clone(), d_ptr, none)
+    torch.cuda.synchronize()
+    assert bool((mass == -3).all()) and not o_ptr.any() and not d_ptr.any()
