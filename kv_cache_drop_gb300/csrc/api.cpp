@@ -1316,7 +1316,8 @@ akv_status akv_qk_norm_append(const akv_shape *shape, int32_t n, const void *q, 
     return fail(AKV_ERR_INVALID, "unknown flags 0x%x", (unsigned)flags);
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(AKV_ERR_INVALID, "eps must be finite and >= 0");
   if (n == 0) return AKV_OK;
-  if (!q || !k || !v || !slot || !q_out || !k_pool || !v_pool ||
+  // a pool of no slots may be NULL: every token is padding
+  if (!q || !k || !v || !slot || !q_out || (S > 0 && (!k_pool || !v_pool)) ||
       ((flags & (AKV_ROPE_Q | AKV_ROPE_K)) && !pos))
     return fail(AKV_ERR_INVALID, "NULL argument");
   const int64_t q_row = (int64_t)shape->Hq * shape->D, k_row = (int64_t)shape->Hkv * shape->D;

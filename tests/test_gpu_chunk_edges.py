@@ -136,3 +136,15 @@ def test_lists_without_entries_under_a_bound(S, m, dtype):
                           mass.clone(), d_ptr, none)
     torch.cuda.synchronize()
     assert bool((mass == -3).all()) and not o_ptr.any() and not d_ptr.any()
+
+
+def test_append_to_a_pool_without_slots():
+    """S = 0: every token is padding."""
+    torch = _torch()
+    shp = akv.shape(16, 4, 64, "bf16")
+    x = torch.ones(3, 24, 64, dtype=torch.bfloat16, device="cuda")
+    pool, qo = x.new_zeros(0, 4, 64), torch.full((3, 16, 64), 7.0, dtype=x.dtype, device="cuda")
+    akv.akv_qk_norm_append(shp, 3, x[:, :16], x[:, 16:20], x[:, 20:], akv.i32_device([0, 1, 2]),
+                           akv.i32_device([0, -1, 5]), pool, pool, qo)
+    torch.cuda.synchronize()
+    assert bool((qo == 7).all())
