@@ -141,14 +141,12 @@ __global__ void __launch_bounds__(kFThreads, 2)
 
 // -lse in log2 units, for the tensor cores' scores; -inf for a row that counts
 // nothing.  The tensor core truncates its sums, which makes a score smaller by
-// 4.4e-8 of itself on average (measured at head dimension 64).  An lse from the
-// chunk's attention is smaller by as much, and the weights come out right; an lse
-// computed otherwise is not, and a weight near 1 loses 4.4e-8 of its score.  The
-// reference is lowered by half of that, so that neither is off by more than half
-// (an exact lse, 2 x 1,100-1,500 rows over 40k-56k entries: error against 64
-// bits 1.06e-6 -> 6.7e-7).
+// 4.4e-8 of itself on average (measured at head dimension 64, N(0, 1) operands).
+// An lse from the chunk's attention is smaller by as much, and the weights come
+// out right (2 x 700-900 rows over 10k-14k entries: error against 64 bits
+// 9e-8); with an exact lse a weight near 1 loses 4.4e-8 of its score (8.1e-7).
 __device__ __forceinline__ float log2_reference(float lse) {
-  return isinf(lse) ? -INFINITY : fmaf(-lse, kLog2e, lse * 3.17e-8f);
+  return isinf(lse) ? -INFINITY : -lse * kLog2e;
 }
 
 // ---------------------------------------------------------------------------

@@ -148,3 +148,44 @@ def test_append_to_a_pool_without_slots():
                            akv.i32_device([0, -1, 5]), pool, pool, qo)
     torch.cuda.synchronize()
     assert bool((qo == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [4, 6, 12, 40])
+def test_mass_has_no_bias(m, dtype):
+    """Weights exp(L - L) = 1 for some 120 values of L between 45 and 88, with
+    q . k exact (one product): each is off by the rounding of L's product with
+    log2 e, half a step of [64, 128) either way, which averages out.  Mean of
+    N = 121 roundings, uniform over a step of 2^-17, times ln 2: a standard
+    deviation of 1.4e-7; four of these, and 2^-22 for the exponential, are
+    8e-7."""
+    torch = _torch()
+    L = np.concatenate([np.arange(45, 64, 0.25), np.arange(64, 86.5, 0.5)])
+    B, n = len(L), m + 260
+    bt = Batch(63, [m] * B, [n] * B, 16, 4, dtype)
+    q, k = np.zeros((bt.rows, 16, 64), np.float32), np.zeros((bt.S, 4, 64), np.float32)
+    q[..., 0] = 8
+    for b in range(B):
+        k[bt.idx[bt.kv_ptr[b]:bt.kv_ptr[b + 1]], :, 0] = L[b]
+    bt.q, bt.k = (workloads.bf16_bits(x) if dtype == "bf16" else x for x in (q, k))
+    d = bt.device()
+    lse = torch.from_numpy(np.repeat(L, m).astype(np.float32)).cuda()[:, None].repeat(1, 16)
+    got = torch.zeros(B, n, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, got)
+    check_mass(bt, lse, None, 1.0, got, 0.0)
+    w = _host(got)[:, :256] / (16 * m)  # entries that every row sees
+    assert abs(w.mean() - 1) < 8e-7, w.mean() - 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 6, 14, 40, 300])
+def test_mass_of_an_exact_lse(m, dtype):
+    """A log-sum-exp that is not the library's own but the definition's,
+    rounded to fp32."""
+    torch = _torch()
+    bt = Batch(64, [m, m], [900, m + 1], 16, 4, dtype, scale=3.0)
+    d = bt.device()
+    lse = torch.from_numpy(np.concatenate([bt.attend(b)[1] for b in range(2)]).astype(np.float32)).cuda()
+    got = torch.zeros(2, 900, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, got)
+    check_mass(bt, lse, None, 1.0, got, 0.0)
