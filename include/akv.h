@@ -553,7 +553,9 @@ akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t 
  * in the list, not its slot, carries its mass, so slots shared by several
  * requests have one mass in each.  mass_in may be NULL or mass_out.
  * mass_stride >= max_kv.  Entries from n on are left as they are.  lse: device
- * fp32 [n_rows, Hq] from akv_chunk_attention; a row with -inf counts nothing.
+ * fp32 [n_rows, Hq] from akv_chunk_attention; a row with -inf counts nothing,
+ * whatever its q holds (a key that is not finite makes its own entry's mass
+ * undefined, if a row sees it).
  * workspace: as above, akv_attention_mass_workspace() bytes. */
 size_t akv_attention_mass_workspace(const akv_shape *shape, int32_t B, int32_t n_rows,
                                     int32_t max_q, int32_t max_kv);

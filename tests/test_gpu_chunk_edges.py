@@ -189,3 +189,25 @@ def test_mass_of_an_exact_lse(m, dtype):
     got = torch.zeros(2, 900, device="cuda")
     run_mass(bt, d, lse, None, 1.0, got)
     check_mass(bt, lse, None, 1.0, got, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [2, 6, 14, 40, 300])
+def test_mass_rows_that_count_nothing(m, dtype):
+    """Rows whose log-sum-exp is -inf count nothing, whatever they hold: NaN,
+    infinities, zeros."""
+    torch = _torch()
+    bt = Batch(65, [m, m], [900, m + 70], 16, 4, dtype)
+    d = bt.device()
+    _, lse = run_chunk(bt, d)
+    out_rows = np.arange(0, 2 * m, 2)
+    at = torch.from_numpy(out_rows).cuda()
+    lse[at] = -math.inf
+    want = torch.zeros(2, 900, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, want)
+    check_mass(bt, lse, None, 1.0, want, 0.0)
+    for bad in (math.nan, math.inf, -math.inf, 0.0):
+        d["q"][at] = bad
+        got = torch.zeros(2, 900, device="cuda")
+        run_mass(bt, d, lse, None, 1.0, got)
+        assert torch.equal(got, want), bad
