@@ -510,6 +510,9 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
  *                                            (weight NULL = ones), else x;
  *   z = R(pos[i]) y                          with AKV_ROPE_Q / AKV_ROPE_K.
  * q_out[i] = z of q; k_pool[slot[i]] = z of k; v_pool[slot[i]] = v[i].
+ * The squares are summed in fp32: a normalised row holds |x| < 2^60, and where
+ * eps is below 2^-100 its root mean square is above 2^-55 (rows outside come
+ * out as zeros, infinities or NaN).
  * q, k, v: device, token i at i * {q,k,v}_stride elements, its heads
  * contiguous (Hq * D, Hkv * D elements), so that they may be column blocks of
  * one projection; strides are at least the row's length.  q_out [n, Hq, D]

@@ -4,7 +4,9 @@
 //   y = x * rsqrt(mean(x^2) + eps) * w,   z = R(pos) y,
 //   q_out = z_q,  k_pool[slot] = z_k,  v_pool[slot] = v,
 // norm and rotation each optional for q and k.  All arithmetic is fp32 and
-// every output is rounded once.
+// every output is rounded once.  (Rows whose squares leave fp32's range could be
+// scaled first; any test for them between the unrolled rows' sums cost every
+// call 4 %: 60.3 -> 62.7 us for 16,384 tokens of 64 / 8 heads.)
 //
 // Bound by HBM: each row is read once and written once.  A head row of 64
 // takes kLanes lanes, each holding the 16-byte chunks c and c + kLanes, which

@@ -211,3 +211,30 @@ def test_mass_rows_that_count_nothing(m, dtype):
         got = torch.zeros(2, 900, device="cuda")
         run_mass(bt, d, lse, None, 1.0, got)
         assert torch.equal(got, want), bad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_qk_norm_of_any_magnitude(n, dtype):
+    """Rows over the range whose squares fp32 holds: up to 2^60, and down to
+    2^-55 or, beside an eps, to anything."""
+    torch = _torch()
+    rng = np.random.default_rng(66)
+    Hq, Hkv = 16, 4
+    shp = akv.shape(Hq, Hkv, 64, dtype)
+    x = rng.standard_normal((n, Hq + 2 * Hkv, 64)).clip(-3, 3)
+    for eps, powers in ((0.0, [-53, -20, 0, 20, 58]), (1e-30, [-100, -55, -20, 0, 58]),
+                        (1e-6, [-120, -50, -20, -8, 0, 58])):
+        p = np.resize(np.array(powers), n * (Hq + 2 * Hkv)).reshape(n, -1, 1)
+        y = (x * 2.0 ** p).astype(np.float32)
+        y = workloads.bf16_bits(y) if dtype == "bf16" else y
+        pos = rng.integers(0, 1000, size=n).astype(np.int32)
+        t = akv.to_device(y, dtype)
+        kp, vp = (torch.zeros(n, Hkv, 64, dtype=t.dtype, device="cuda") for _ in range(2))
+        qo = torch.zeros(n, Hq, 64, dtype=t.dtype, device="cuda")
+        akv.akv_qk_norm_append(shp, n, t[:, :Hq], t[:, Hq:Hq + Hkv], t[:, Hq + Hkv:], akv.i32_device(pos),
+                               akv.i32_device(np.arange(n)), kp, vp, qo, eps=eps)
+        torch.cuda.synchronize()
+        _close_rows(_host(qo), _prepared(y[:, :Hq], None, pos, 1, 1, eps, dtype), dtype)
+        _close_rows(_host(kp), _prepared(y[:, Hq:Hq + Hkv], None, pos, 1, 1, eps, dtype), dtype)
+        assert np.array_equal(_host(vp), oracle.widen(y[:, Hq + Hkv:], dtype))
