@@ -238,3 +238,70 @@ def test_qk_norm_of_any_magnitude(n, dtype):
         _close_rows(_host(qo), _prepared(y[:, :Hq], None, pos, 1, 1, eps, dtype), dtype)
         _close_rows(_host(kp), _prepared(y[:, Hq:Hq + Hkv], None, pos, 1, 1, eps, dtype), dtype)
         assert np.array_equal(_host(vp), oracle.widen(y[:, Hq + Hkv:], dtype))
+
+
+class Led(Batch):
+    """A batch whose rows come after `lead` rows of q that belong to no
+    request."""
+
+    def __init__(self, *args, lead=0, tail=0, **kw):
+        super().__init__(*args, tail=lead + tail, **kw)
+        self.lead = lead
+        self.q_ptr = self.q_ptr + np.int32(lead)
+
+
+def _cut(bt, max_q, max_kv):
+    """The batch that a call with these bounds sees: each chunk's first max_q
+    rows over its list's first max_kv entries."""
+    c = copy.copy(bt)
+    c.m, c.n = [min(x, max_q) for x in bt.m], [min(x, max_kv) for x in bt.n]
+    c.q = np.concatenate([bt.q[p:p + x] for p, x in zip(bt.q_ptr, c.m)])
+    c.idx = np.concatenate([bt.idx[p:p + x] for p, x in zip(bt.kv_ptr, c.n)])
+    c.q_ptr = np.concatenate([[0], np.cumsum(c.m)]).astype(np.int32)
+    c.kv_ptr = np.concatenate([[0], np.cumsum(c.n)]).astype(np.int32)
+    c.rows = int(c.q_ptr[-1])
+    return c
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [([2, 0, 3], [5000, 10, 70]), ([10, 6, 0, 16], [3000, 3100, 8, 40]),
+                                 ([30, 20], [5000, 900]), ([100, 1, 51], [2500, 3000, 60])])
+def test_chunk_rows_and_bounds(m, n, dtype):
+    """Rows before the first request and after the last, and chunks and lists
+    longer than max_q and max_kv: cut to them, with every row and entry past
+    the cut left as it was."""
+    torch = _torch()
+    bt = Led(68, m, n, 16, 4, dtype, lead=5, tail=4)
+    d = bt.device()
+    mq, mk = max(m), max(n)
+    for max_q, max_kv in ((mq, mk), (mq + 9, mk + 900), (mq - 1, mk), (mq, mk - 7), ((mq + 1) // 2, mk // 2)):
+        c = _cut(bt, max_q, max_kv)
+        out, lse = run_chunk(bt, d, max_q=max_q, max_kv=max_kv)
+        torch.cuda.synchronize()
+        mine = np.concatenate([np.arange(p, p + x) for p, x in zip(bt.q_ptr, c.m)])
+        rest = np.setdiff1d(np.arange(bt.rows), mine)
+        at = torch.from_numpy(mine).cuda()
+        check_chunk(c, out[at], lse[at])
+        assert np.all(_host(out)[rest] == 7) and np.all(_host(lse)[rest] == 7)
+        mass_in = torch.rand(bt.B, mk + 900, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+        got = torch.full((bt.B, mk + 900), -3.0, device="cuda")
+        run_mass(bt, d, lse, mass_in, 0.5, got, max_q=max_q, max_kv=max_kv)
+        check_mass(c, lse[at], mass_in, 0.5, got, -3.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_long_chunk_among_single_tokens(dtype):
+    """A prefill chunk batched with decode steps: 13 single tokens and 260
+    rows over lists of 1 to 4,000 entries."""
+    torch = _torch()
+    rng = np.random.default_rng(69)
+    m = [1] * 6 + [260] + [1] * 7
+    n = [int(x) for x in rng.integers(1, 4000, size=14)]
+    n[6], n[0], n[13] = 1300, 4000, 1
+    bt = Batch(70, m, n, 16, 4, dtype)
+    d = bt.device()
+    out, lse = run_chunk(bt, d)
+    check_chunk(bt, out, lse)
+    got = torch.zeros(bt.B, bt.max_kv, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, got)
+    check_mass(bt, lse, None, 1.0, got, 0.0)
