@@ -485,7 +485,7 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
  *                        added to what it had;
  *   akv_evict_by_mass    each list cut to a budget, lowest mass first: the new
  *                        list for the next decode or chunk, and the slots
- *                        that became free.
+ *                        that left it.
  *
  * Common to the last three: lists are those of the decode calls (kv_indptr
  * [B+1], kv_indices, device int32, keys in the pool already rotated).  q_indptr
@@ -495,13 +495,16 @@ akv_status akv_append_kv(const akv_shape *shape, int32_t n, const void *k_new, c
  * the first n - m + i + 1 of the list's n entries (none if that is not
  * positive).  max_q, max_kv: host, upper bounds on the chunks' and lists'
  * lengths; longer ones are cut to them.  kv_indices and the pools may be NULL
- * where max_kv is 0.  A pool index outside [0, S) reads pool row 0.  All index data stays on the device, so the calls can be
- * captured in a CUDA graph and replayed with other lengths within the bounds.
+ * where max_kv is 0.  A pool index outside [0, S) reads pool row 0.  All index
+ * data stays on the device, so the calls can be captured in a CUDA graph and
+ * replayed with other lengths within the bounds.
  * A workspace serves one call at a time: calls that may overlap on the GPU
  * (two streams, two captured graphs) need one each.  Workspaces start with the
- * status word read by akv_workspace_status (cleared by each call).  Outputs must
- * not overlap inputs unless a call says so.  Make the first call of each kind
- * outside a stream capture (it loads the kernels).
+ * status word read by akv_workspace_status, cleared by each call that launches
+ * a kernel; a call without work (B, n_rows or max_q is 0 for the attention, B or
+ * max_kv for the mass) leaves its workspace as it is.  Outputs must not overlap
+ * inputs unless a call says so.  Make the first call of each kind outside a
+ * stream capture (it loads the kernels).
  * Limits: B <= 65535, max_kv <= 2^30, Hq <= 65535, and grids within CUDA's
  * limits (AKV_ERR_UNSUPPORTED otherwise). */
 
@@ -572,7 +575,10 @@ akv_status akv_attention_mass(const akv_shape *shape, int32_t B, const int32_t *
 /* Eviction by mass: drop(P) of section 3.3 with P chosen by weight.  Request
  * b keeps min(max(keep[b], 0), n) entries: those of the largest mass, ties to
  * the lowest list position.  The first n_first and last n_recent entries of a
- * list count as +inf, a NaN mass as -inf.  Outputs, in list order:
+ * list count as +inf, a NaN mass as -inf.  A slot that left one list may be in
+ * another request's: it is free once it is in none.  (akv_tree knows nothing of
+ * this call: the units of a history that it lists stay pinned with all their
+ * slots.)  Outputs, in list order:
  *   out_indptr [B+1], out_indices, out_pos   the kept lists (kv_pos and
  *       out_pos: both given or both NULL), for the next decode or chunk, or
  *       for akv_repos_rotate (src_idx = out_indices, pos_from = out_pos);
@@ -582,8 +588,9 @@ akv_status akv_attention_mass(const akv_shape *shape, int32_t B, const int32_t *
  * and out_pos hold, dropped_capacity: those of dropped (the length of
  * kv_indices always suffices); out_stride: masses that a row of out_mass
  * holds.  What would go past them is not written; the index pointers count it
- * all the same; an output of no entries may be NULL.  Outputs must not overlap
- * inputs. */
+ * all the same; an output of no entries may be NULL.  Entries past max_kv are
+ * neither kept nor dropped.  B = 0 writes nothing, the index pointers neither.
+ * Outputs must not overlap inputs. */
 akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t *kv_indices,
                              const int32_t *kv_pos, int32_t max_kv, const float *mass,
                              int64_t mass_stride, const int32_t *keep, int32_t n_first,
