@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 // XOR-swizzled tile, several tiles in flight; the packed rows are the rows of
 // m16n8k16 tiles: S = Q K^T with K as the B operand, P reused from the S
 // registers for P V.  Bound by the gather from HBM (14 decode steps over 20,000
-// to 90,000 entries, 64 / 8 heads: 236 us, 0.94 of the floor); tcgen05 would
+// to 90,000 entries, 64 / 8 heads: 235 us on the device, 0.94 of the floor, 243
+// for the call); tcgen05 would
 // spend a 128-row tile on 8 rows.
 // ---------------------------------------------------------------------------
 constexpr int kSSt = 3;  // K and V tiles per warp
@@ -570,8 +571,9 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
 // instead of 7.52 ms at 2 x 4,096 rows over 50k-70k entries, a mixed batch 185
 // instead of 170 us).  With copies, weights and most MMAs taken out in turn the
 // kernel ran at 5.0 ms (copies alone), 6.4 ms (no copies) and 4.1 ms (barriers,
-// TMEM loads and stores): what bounds it, 6.4 ms now, is the softmax threads'
-// chain of TMEM load, weights, TMEM store and barrier, lengthened by the copies.
+// TMEM loads and stores), from 7.5 to 6.9 ms in all: what bounds it, 6.5 to 6.6 ms
+// now, is the softmax threads' chain of TMEM load, weights, TMEM store and
+// barrier, lengthened by the copies.
 //
 // Hidden entries.  Windows from the first tile's limit on are masked per row.
 // There a weight of 0 would still turn a hidden infinity or NaN of V into
@@ -777,11 +779,14 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
     if (warp < kMmaWarp) {
       // A window is kWin rows of K and of V, 16 bytes per lane and copy, eight
       // lanes a row.  A stage is refilled without a wait: when tile 0's barrier of
-      // window n opens, its softmax has seen S_0(n), whose commit tracks
-      // P.V(n - 1) of both tiles, the last readers of that window.  Each window is
-      // one group of copies (empty past the end), with the list entries of the
-      // window kSt further on, so that "window w has landed" is a count of
-      // groups still in flight.
+      // window n opens, its softmax has seen S_0(n), whose commit tracks every MMA
+      // issued before it.  With one tile that is P.V(n - 1), the last reader of
+      // window n - 1, which is refilled; with two tiles S_0(n) was issued two
+      // windows ahead, right behind P.V(n - 2) of both, so that only window
+      // n - 2 may be (window n - 1 may still be read).  Each window is one group
+      // of copies (empty past the end), with the list entries of the window kSt
+      // further on, so that "window w has landed" is a count of groups still in
+      // flight.
       const int key0 = 4 * s0 + (lane >> 3);
       const uint32_t kd = ptx::smem_addr(sm.k[0]) + key0 * 128;
       const uint32_t sw0 = (ch ^ (key0 & 7)) << 4, sw1 = (ch ^ ((key0 + 4) & 7)) << 4;
@@ -793,7 +798,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
         const int left = c1 - (c0 + n * kWin + key0);
         // whole windows without the tests of a last one, and rows at 32 x 32-bit
         // products: the producers' instructions compete with the softmax warps'
-        // (6.88 -> 6.39 ms for 2 x 4,096 rows over 50k-70k entries)
+        // (7 % of the call for 2 x 4,096 rows over 50k-70k entries)
         auto steps = [&](auto whole) {
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {

@@ -1,5 +1,5 @@
 // Shared by the kernels over a chunk of new tokens and a page-size-1 pool
-// (chunk.cu, mass.cu): the batch, a request's view of it, and the 64 x 64
+// (chunk.cu, mass.cu): the batch, a request's view of it, and the 128 x 64
 // score tile on the CUDA cores.
 //
 // Rows.  The query rows of KV head g are packed (token, head of the group):

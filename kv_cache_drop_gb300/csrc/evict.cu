@@ -12,10 +12,13 @@
 // contiguous part of the list, the counts are scanned over warps and CTAs, and
 // the warp goes over its part again, writing kept and dropped entries in list
 // order by ballot prefix.  No atomics on global memory: the result does not
-// depend on timing.  Lists of up to 16,384 entries per CTA stay in registers
-// between the passes; longer ones are read again, from L2, eight loads in
-// flight per thread.  Bound by the latency of the passes and cluster barriers
-// (short lists) and by the L2 bandwidth of the cluster's SMs (long ones).
+// depend on timing.  Keys of up to 16,384 entries per CTA stay in registers
+// between the digits and the count; longer lists' masses are read again for
+// each, from L2, eight loads in flight per thread.  The last pass reads masses,
+// slots and positions from memory in either case.  14 lists of 20,000 to 90,000
+// entries take 17.8 us on the device, one of 1.5 million 81, of which the last
+// pass 34: bound by the latency of the passes and of five cluster barriers (short
+// lists), and by what one cluster's SMs read and write (long ones).
 #include "common.cuh"
 
 #include <cooperative_groups.h>

@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(kFThreads, 2)
 // 4.4e-8 of itself on average (measured at head dimension 64, N(0, 1) operands).
 // An lse from the chunk's attention is smaller by as much, and the weights come
 // out right (2 x 700-900 rows over 10k-14k entries: error against 64 bits
-// 9e-8); with an exact lse a weight near 1 loses 4.4e-8 of its score (8.1e-7).
+// 9e-8); with an exact lse a weight near 1 loses 4.4e-8 of its score (8.1e-7, and
+// 1.1e-6 for 2 x 1,100-1,500 rows over 40k-56k).
 __device__ __forceinline__ float log2_reference(float lse) {
   return isinf(lse) ? -INFINITY : -lse * kLog2e;
 }
