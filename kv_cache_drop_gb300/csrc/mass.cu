@@ -139,13 +139,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
   }
 }
 
-// -lse in log2 units, for the tensor cores' scores; -inf for a row that counts
-// nothing.  The tensor core truncates its sums, which makes a score smaller by
-// 4.4e-8 of itself on average (measured at head dimension 64, N(0, 1) operands).
-// An lse from the chunk's attention is smaller by as much, and the weights come
-// out right (2 x 700-900 rows over 10k-14k entries: error against 64 bits
-// 9e-8); with an exact lse a weight near 1 loses 4.4e-8 of its score (8.1e-7, and
-// 1.1e-6 for 2 x 1,100-1,500 rows over 40k-56k).
+// -lse in log2 units, for mma.sync's scores; -inf for a row that counts nothing
 __device__ __forceinline__ float log2_reference(float lse) {
   return isinf(lse) ? -INFINITY : -lse * kLog2e;
 }
@@ -294,11 +288,20 @@ __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
 // (two tiles of 128 keys) x a share of the (KV head, 256-row tile) items:
 //   warps 4 i .. 4 i + 3  every other 128-row half of the items: thread = TMEM
 //        lane = one key of each key tile, so that the sums over rows stay in
-//        the thread's registers, and one load of a row's lse serves two weights
+//        the thread's registers
 //   3 producer warps      K tiles (once per head), Q tiles and the rows' lse
 //        through a ring, by cp.async into the 128-byte-swizzled layout
-//   MMA warp              S^T = K Q^T, both operands from shared memory, two
-//        128 x 128 tiles per half, into the TMEM buffer of its warps
+//   MMA warp              S^T = K Q^T - 8 lse, both operands from shared memory,
+//        two 128 x 128 tiles per half, into the TMEM buffer of its warps
+// The log-sum-exp is a fifth K step (keys: ones; rows: -8 lse in three bf16
+// pieces) between the second and the third.  The tensor core truncates every
+// step's sum.  Summed to the end, a score came out smaller by 4.4e-8 of itself,
+// and with it the weights (error against 64 bits 8.1e-7 for 2 x 700-900 rows over
+// 10k-14k entries); now the two sums before the step are cut towards one side,
+// the two after it, of the other sign, towards the other, none is larger than
+// half the score, and the last is near 0: 1.1e-7, as the plain form in fp32.  The
+// step's MMA costs less than the rows' references did in the weights' loop
+// (1,629 -> 1,553 us for 2 x 1,100-1,500 rows over 40k-56k entries).
 // Scores are taken 16 rows at a time, the next 16 being loaded while a step's
 // weights are summed; the buffer is given back with the last load.  Each Q tile
 // serves both key tiles: 32 KB from L2 per 65,536 weights.
@@ -308,8 +311,6 @@ __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
 // ---------------------------------------------------------------------------
 constexpr int kQRows = 2 * kTcRows;
 constexpr int kQSt = 4, kKBuf = 2;
-constexpr int kNlSt = 8;
-static_assert(kNlSt >= kQSt + 2, "slots of the rows' lse");
 constexpr int kMProducers = 3;
 constexpr int kMThreads = 256 + 32 * kMProducers + 32;
 constexpr int kKSteps = (kTcKeys / 4 + kMProducers - 1) / kMProducers;  // 4-row copy steps, per warp
@@ -324,16 +325,26 @@ constexpr int kInFlight = 1;
 struct __align__(1024) MassTcSmem {
   uint8_t k[kKBuf][2][kTcTileBytes];  // [buffer][key tile]
   uint8_t q[kQSt][2 * kTcTileBytes];
-  // -lse in log2 units of an item's rows.  Item x's slot was item x - kNlSt's:
-  // the Q stage of x is free once the MMAs of x - kQSt are done, the last of
-  // which began when the scores two halves earlier were in registers.
-  float nl[kNlSt][kQRows];
+  // the K step of the log-sum-exp: the rows' columns 0 .. 7 (with Q's stage), the
+  // keys', and columns 8 .. 15 of either
+  uint4 lse[kQSt][kQRows], ones[kTcKeys], zeros[kTcKeys];
   uint64_t k_full[kKBuf], k_free[kKBuf], q_full[kQSt], q_free[kQSt];
   uint64_t s_full[2], s_free[2];  // per score buffer
   float join[kMBlock];            // sums of the odd halves
   uint32_t tmem_base;
   uint32_t gave_up;
 };
+
+// Columns 0 .. 7 of a row in the K step that takes its log-sum-exp off its scores:
+// -8 lse (scores are not divided by 8 yet) as three bf16 values, which hold all 24
+// bits.  A row that counts nothing gets -1e30, whose weight is 0.
+__device__ __forceinline__ uint4 reference(float lse) {
+  const float x = isinf(lse) ? -1e30f : -8.f * lse;
+  const float hi = __bfloat162float(__float2bfloat16_rn(x));
+  const float rest = isinf(hi) ? 0.f : x - hi;
+  const float mid = __bfloat162float(__float2bfloat16_rn(rest));
+  return make_uint4(pack2(hi, mid), pack2(rest - mid, 0.f), 0u, 0u);
+}
 
 // tokens that v packed rows from a token's first row on reach over; exact for
 // v < 512 + grp
@@ -385,6 +396,11 @@ __global__ void __launch_bounds__(kMThreads, 1)
     }
     sm.gave_up = 0u;
     ptx::fence_barrier_init();
+  }
+  if (threadIdx.x < kTcKeys) {
+    sm.ones[threadIdx.x] = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);  // one per piece of lse
+    sm.zeros[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
   }
   if (warp == 8 + kMProducers) ptx::tmem_alloc(&sm.tmem_base, 512);
   ptx::tc_fence_before();
@@ -508,11 +524,11 @@ __global__ void __launch_bounds__(kMThreads, 1)
       for (int u = 0; u < kLse; ++u) {
         const int x = 4 * qs0 + lane + 32 * u;
         if (lane + 32 * u < 4 * kQSteps && x < kQRows)
-          sm.nl[qn % kNlSt][x] = log2_reference(lse_nx[u]);
+          sm.lse[st][x] = reference(lse_nx[u]);
       }
-      // A row that counts nothing may hold anything, and its reference of -inf
-      // makes a weight of 0 of finite scores only: its copy becomes zeros.
-      // (Telling the warps that form the weights, 1.4 % of the call.)
+      // A row that counts nothing may hold anything, and its reference makes a
+      // weight of 0 of finite scores only: its copy becomes zeros.  (Telling the
+      // warps that form the weights, 1.4 % of the call.)
       static_assert(kLse == 3, "rows per lane");
       const bool none = fminf(fminf(lse_nx[0], lse_nx[1]), lse_nx[2]) == -INFINITY;
       if (__any_sync(0xffffffffu, none)) {
@@ -540,6 +556,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
     constexpr uint64_t kTileStep = kTcTileBytes >> 4;
     const uint64_t dk = ptx::sdesc_sw128(ptx::smem_addr(sm.k[0][0]));
     const uint64_t dq = ptx::sdesc_sw128(ptx::smem_addr(sm.q[0]));
+    const uint64_t d_ones =
+        ptx::sdesc_plain(ptx::smem_addr(sm.ones), ptx::smem_addr(sm.zeros) - ptx::smem_addr(sm.ones), 128);
     int kn = 0, t = tile0, hseq = 0;
     for (int qn = 0; qn < mine; ++qn) {
       if (qn == 0 || t == t0) {  // the next head
@@ -558,12 +576,16 @@ __global__ void __launch_bounds__(kMThreads, 1)
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint64_t ak = dk + ((kn - 1) % kKBuf) * 2 * kTileStep, bq = dq + (st * 2 + hf) * kTileStep;
+          const uint32_t at = ptx::smem_addr(sm.lse[st] + hf * kTcRows);
+          const uint64_t d_lse = ptx::sdesc_plain(at, ptx::smem_addr(sm.zeros) - at, 128);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_f16_ss(tmem + buf * 256 + i * 128, ak + i * kTileStep + 2 * kk, bq + 2 * kk, id,
-                              kk > 0);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t d = tmem + buf * 256 + i * 128;
+              if (kk == 2) ptx::mma_f16_ss(d, d_ones, d_lse, id, 1u);
+              ptx::mma_f16_ss(d, ak + i * kTileStep + 2 * kk, bq + 2 * kk, id, kk > 0);
+            }
           ptx::mma_commit(&sm.s_full[buf]);
           if (hf + 1 == halves) ptx::mma_commit(&sm.q_free[st]);
         }
@@ -591,7 +613,6 @@ __global__ void __launch_bounds__(kMThreads, 1)
       hseq += halves;
       if (hf >= halves) continue;
       const int r0 = r_tile + hf * kTcRows;
-      const float4 *nl4 = reinterpret_cast<const float4 *>(sm.nl[qn % kNlSt] + hf * kTcRows);
       float2 sum[2][2];  // of this half: [key][pair of rows]
 #pragma unroll
       for (int e = 0; e < 2; ++e) sum[e][0] = sum[e][1] = make_float2(0.f, 0.f);
@@ -620,15 +641,13 @@ __global__ void __launch_bounds__(kMThreads, 1)
           }
 #pragma unroll
           for (int q = 0; q < kStep / 4; ++q) {
-            const float4 v = nl4[c * (kStep / 4) + q];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
                 const int x = 4 * q + 2 * w;
-                const float2 y = __ffma2_rn(
-                    make_float2(__uint_as_float(s[e][x]), __uint_as_float(s[e][x + 1])), scale2,
-                    w ? make_float2(v.z, v.w) : make_float2(v.x, v.y));
+                const float2 y = __fmul2_rn(
+                    make_float2(__uint_as_float(s[e][x]), __uint_as_float(s[e][x + 1])), scale2);
                 sum[e][w] = __fadd2_rn(sum[e][w], make_float2(ptx::ex2(y.x), ptx::ex2(y.y)));
               }
           }
@@ -638,7 +657,6 @@ __global__ void __launch_bounds__(kMThreads, 1)
         const int lo0 = (int)min((int64_t)kTcRows, max((int64_t)0, r_min0 - r0));
         const int lo1 = (int)min((int64_t)kTcRows, max((int64_t)0, r_min1 - r0));
         const int hi = min(kTcRows, rows - r0);
-        const float *nl = reinterpret_cast<const float *>(nl4);
 #pragma unroll 1
         for (int c = 0; c < kTcRows; c += kStep) {
           uint32_t s[2][kStep];
@@ -650,8 +668,8 @@ __global__ void __launch_bounds__(kMThreads, 1)
           if (c + kStep == kTcRows) give_back();
 #pragma unroll
           for (int x = 0; x < kStep; ++x) {
-            const float p0 = ptx::ex2(fmaf(__uint_as_float(s[0][x]), kScale, nl[c + x]));
-            const float p1 = ptx::ex2(fmaf(__uint_as_float(s[1][x]), kScale, nl[c + x]));
+            const float p0 = ptx::ex2(__uint_as_float(s[0][x]) * kScale);
+            const float p1 = ptx::ex2(__uint_as_float(s[1][x]) * kScale);
             if (c + x >= lo0 && c + x < hi) sum[0][0].x += p0;
             if (c + x >= lo1 && c + x < hi) sum[1][0].x += p1;
           }

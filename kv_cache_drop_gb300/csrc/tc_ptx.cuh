@@ -192,6 +192,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// The same without swizzle, K-major: 8 rows x 16 bytes are one contiguous block
+// of 128 bytes; `k_step` bytes to the next block along K, `row_step` to the next
+// 8 rows.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t k_step, uint32_t row_step) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((k_step >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(row_step >> 4) << 32) | ((uint64_t)1 << 46);
+}
 
 // ---- TMEM <-> registers (one warp; its 32 lanes = rows lane_base..+31) ----
 #define AKV_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \

@@ -305,3 +305,25 @@ def test_one_long_chunk_among_single_tokens(dtype):
     got = torch.zeros(bt.B, bt.max_kv, device="cuda")
     run_mass(bt, d, lse, None, 1.0, got)
     check_mass(bt, lse, None, 1.0, got, 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 6, 14, 40, 300])
+@pytest.mark.parametrize("scale", [0.0, 1.0, 6.0])
+def test_mass_of_the_library_lse_sums_to_the_rows(scale, m, dtype):
+    """Attention's log-sum-exp into the mass: every row and head gives a mass
+    of 1.  Off by the lse's error and the weights': 2^-22 (1 + |lse|) for the
+    roundings of lse and of its products with ln 2 and log2 e, and nine steps of
+    a tensor core that cuts each sum (four in the attention, five in the mass),
+    each below 2^-23 of the sum of the products' sizes."""
+    torch = _torch()
+    bt = Batch(71, [m, m], [1200, m + 5], 16, 4, dtype, scale=scale)
+    d = bt.device()
+    _, lse = run_chunk(bt, d)
+    got = torch.zeros(2, 1200, device="cuda")
+    run_mass(bt, d, lse, None, 1.0, got)
+    total, l = _host(got).sum(1), np.abs(_host(lse))
+    for b in range(2):
+        _, E = bt.scores(b)  # 2^-18 of that size
+        tol = 2.0 ** -22 * (1 + l[bt.q_ptr[b]:bt.q_ptr[b + 1]].max()) + 9 * 2.0 ** -5 * E.max()
+        assert abs(total[b] / (16 * m) - 1) <= tol, (total[b] / (16 * m) - 1, tol)
