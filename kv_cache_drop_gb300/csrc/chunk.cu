@@ -321,8 +321,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 // XOR-swizzled tile, several tiles in flight; the packed rows are the rows of
 // m16n8k16 tiles: S = Q K^T with K as the B operand, P reused from the S
 // registers for P V.  Bound by the gather from HBM (14 decode steps over 20,000
-// to 90,000 entries, 64 / 8 heads: 235 us on the device, 0.94 of the floor, 243
-// for the call); tcgen05 would
+// to 90,000 entries, 64 / 8 heads: 235 us on the device, 0.94 of the floor, 239
+// to 243 for the call); tcgen05 would
 // spend a 128-row tile on 8 rows.
 // ---------------------------------------------------------------------------
 constexpr int kSSt = 3;  // K and V tiles per warp
