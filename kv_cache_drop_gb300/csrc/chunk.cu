@@ -590,7 +590,7 @@ constexpr int kBarAll = 2;       // all warps, after a pass
 constexpr float kRescale = 8.f;       // log2 units by which a maximum may pass the reference
 constexpr float kRaise = 65536.f;     // the row sum that raises it
 constexpr float kHuge = 1.2089258e24f;  // 2^80: a window's sum that was computed too far above it
-constexpr uint32_t kFar = 0x71800000u;  // 2^100's bits: an output sum that was
+constexpr uint32_t kFar = 0x71800000u;  // 2^100: an output sum that says so too (its bits)
 
 constexpr uint32_t kOnesBytes = 16 * kD * 2;
 constexpr uint32_t kOCols = kD + 16;  // V's columns and the ones

@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
 // and with it the weights (error against 64 bits 8.1e-7 for 2 x 700-900 rows over
 // 10k-14k entries); now the two sums before the step are cut towards one side,
 // the two after it, of the other sign, towards the other, none is larger than
-// half the score, and the last is near 0: 1.1e-7, as the plain form in fp32.  The
+// half the score, and the last is near 0: 1.1e-7, as plain fp32 arithmetic.  The
 // step's MMA costs less than the rows' references did in the weights' loop
 // (1,629 -> 1,553 us for 2 x 1,100-1,500 rows over 40k-56k entries).
 // Scores are taken 16 rows at a time, the next 16 being loaded while a step's
