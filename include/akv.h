@@ -550,6 +550,34 @@ akv_status akv_chunk_attention(const akv_shape *shape, int32_t B, const int32_t 
                                const int32_t *kv_indices, int32_t max_kv, void *out, float *lse,
                                void *workspace, size_t workspace_bytes, akv_stream_t stream);
 
+/* Attention of a batch whose requests share prefixes (the prefix sharing of
+ * akv_plan_create_shared, over the pool): as akv_chunk_attention, with a list of
+ * its own for each group of rows beside those of the requests.  Group g holds
+ * rows group_indptr[g] .. group_indptr[g+1]-1 of q (device int32 [n_groups+1],
+ * ascending; max_rows: host, an upper bound on a group's rows) and the prefix
+ * list prefix_indices[prefix_indptr[g] ..) (max_prefix: its upper bound).  A row
+ * sees its group's whole prefix, and of its request's own list what
+ * akv_chunk_attention lets it see; out and lse are over both together, so lse
+ * serves akv_attention_mass for the own lists.  A prefix is read once for all
+ * rows of its group.  A row may be in a group and no request, or the reverse;
+ * rows in neither are neither read nor written; one that sees nothing gets zeros,
+ * and -inf.  n_groups or B may be 0, with their lists NULL.  Rows and entries
+ * past the bounds max_rows, max_prefix, max_q, max_kv have no part in the lists
+ * these bound.  group_indptr need not follow the requests' limits.  Otherwise as
+ * akv_chunk_attention, n_groups as B.  workspace: akv_prefix_workspace() bytes
+ * for the same arguments. */
+size_t akv_prefix_workspace(const akv_shape *shape, int32_t n_groups, int32_t max_rows,
+                            int32_t max_prefix, int32_t B, int32_t n_rows, int32_t max_q,
+                            int32_t max_kv);
+akv_status akv_prefix_attention(const akv_shape *shape, int32_t n_groups,
+                                const int32_t *group_indptr, int32_t max_rows,
+                                const int32_t *prefix_indptr, const int32_t *prefix_indices,
+                                int32_t max_prefix, int32_t B, const int32_t *q_indptr,
+                                int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                                const void *v_pool, int32_t S, const int32_t *kv_indptr,
+                                const int32_t *kv_indices, int32_t max_kv, void *out, float *lse,
+                                void *workspace, size_t workspace_bytes, akv_stream_t stream);
+
 /* Attention mass.  For list entry j < n of request b:
  *   mass_out[b * mass_stride + j] = decay * mass_in[b * mass_stride + j]
  *     + sum over the chunk's rows i that see j, and heads h, of
@@ -598,6 +626,70 @@ akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t 
                              int32_t *out_pos, float *out_mass, int64_t out_stride,
                              int64_t out_capacity, int32_t *dropped_indptr, int32_t *dropped,
                              int64_t dropped_capacity, akv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A cache in 8 bits: half the bytes per entry, for the pool whose lists the
+ * decode calls read.  Pools: k_pool, v_pool [S, Hkv, D] e4m3 values (one byte,
+ * no infinity), k_scale, v_scale [S, Hkv] bytes, a power of two 2^(byte - 127)
+ * for each head row (e8m0).  A row stands for value * 2^s with the smallest s
+ * in -127 .. 127 for which the row's largest finite |x| is at most 448 * 2^s
+ * (-127 for a row of zeros); each value is rounded to the nearest, ties to
+ * even: at most 2^-4 of it off, or 2^-10 * 2^s where that is more.  What is not
+ * finite is kept as NaN.
+ * Keys are kept before RoPE and lists carry positions (as for
+ * akv_decode_attention_rope): a repos rewrites positions only, where stored
+ * rotated keys would be rounded to 8 bits again at every turn.
+ * k_pool, v_pool, rows of q, k, v and outputs must start at multiples of 16
+ * bytes (AKV_ERR_INVALID); the pools may be NULL where S is 0.
+ *
+ * akv_append_kv_q8: token i < n of k and v (device, raw, at i * {k,v}_stride
+ * elements, its heads contiguous, so that they may be column blocks of one
+ * projection; strides at least Hkv * D) goes to slot[i] (device int32 [n],
+ * distinct).  A token whose slot is outside [0, S) is padding: nothing of it is
+ * read or written.  n * Hkv < 2^31 (AKV_ERR_UNSUPPORTED).
+ *
+ * akv_read_kv_q8: for i < n, K_out[dst[i]] = R(pos[i]) K[src[i]] and
+ * V_out[dst[i]] = V[src[i]], rounded once to the shape's dtype.  src, pos, dst:
+ * device int32 [n]; pos NULL: keys as they are stored; dst NULL: dst[i] = i, else
+ * distinct.  k_out, v_out: device [R, Hkv, D]: with pos, a pool for
+ * akv_chunk_attention, akv_prefix_attention or akv_decode_attention (the keys
+ * rotated); without, one for akv_decode_attention_rope.  An entry whose src is
+ * outside [0, S) or whose dst is outside [0, R) writes nothing. */
+akv_status akv_append_kv_q8(const akv_shape *shape, int32_t n, const void *k, int64_t k_stride,
+                            const void *v, int64_t v_stride, const int32_t *slot, int32_t S,
+                            void *k_pool, void *v_pool, uint8_t *k_scale, uint8_t *v_scale,
+                            akv_stream_t stream);
+akv_status akv_read_kv_q8(const akv_shape *shape, int32_t n, const int32_t *src, const int32_t *pos,
+                          const int32_t *dst, const void *k_pool, const void *v_pool,
+                          const uint8_t *k_scale, const uint8_t *v_scale, int32_t S, void *k_out,
+                          void *v_out, int32_t R, akv_stream_t stream);
+
+/* Decode over an 8-bit cache with rotation on read: akv_decode_attention_rope
+ * with 8-bit pools.  q [B, Hq, D] raw, rotated at q_pos (device int32 [B]); entry
+ * j of request b's list kv_indices[kv_indptr[b] ..) is rotated at kv_pos[j].
+ * max_kv: host, an upper bound on the lists' lengths; longer ones are cut to it.
+ * An index outside [0, S) reads pool row 0.  kv_indices, kv_pos and the pools may
+ * be NULL where max_kv is 0.  out [B, Hq, D]; a request without entries gets
+ * zeros.  Fused append (k_new, v_new [B, Hkv, D] raw and contiguous, new_slot
+ * device int32 [B]; all three or none): the step's row of request b goes to
+ * new_slot[b], in 8 bits as akv_append_kv_q8 writes it, before the list is read;
+ * the list must end with new_slot[b] (its kv_pos entry is q_pos[b]) and no other
+ * entry of the batch may name that slot.  A request whose new_slot is outside
+ * [0, S) or whose list is empty appends nothing.
+ * Any number of query heads per KV head.  Limits: B <= 65535, Hq <= 65535, max_kv
+ * <= 2^30 (AKV_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned,
+ * akv_decode_q8_workspace() bytes (split-KV partials); it serves one call at a
+ * time.  All index data stays on the device, so the call can be captured in a
+ * CUDA graph and replayed with other lengths within max_kv; make the first call
+ * outside a capture (it loads the kernels). */
+size_t akv_decode_q8_workspace(const akv_shape *shape, int32_t B, int32_t max_kv);
+akv_status akv_decode_attention_q8(const akv_shape *shape, int32_t B, const void *q,
+                                   const int32_t *q_pos, const void *k_new, const void *v_new,
+                                   const int32_t *new_slot, void *k_pool, void *v_pool,
+                                   uint8_t *k_scale, uint8_t *v_scale, int32_t S,
+                                   const int32_t *kv_indptr, const int32_t *kv_indices,
+                                   const int32_t *kv_pos, int32_t max_kv, void *out,
+                                   void *workspace, size_t workspace_bytes, akv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Decoder layers of a single-prefill restoration (paper review page section

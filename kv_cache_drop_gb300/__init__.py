@@ -198,6 +198,24 @@ _SIGS = {
                           [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p] +
                           [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 4 + [ctypes.c_int64] * 2 +
                           [ctypes.c_void_p] * 2 + [ctypes.c_int64, ctypes.c_void_p]),
+    "akv_prefix_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] + [ctypes.c_int32] * 7),
+    "akv_prefix_attention": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32,
+                                            ctypes.c_void_p, ctypes.c_int32] +
+                             [ctypes.c_void_p] * 2 + [ctypes.c_int32] * 2 + [ctypes.c_void_p] +
+                             [ctypes.c_int32] * 2 + [ctypes.c_void_p] * 3 + [ctypes.c_int32] +
+                             [ctypes.c_void_p] * 2 + [ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                             [ctypes.c_size_t, ctypes.c_void_p]),
+    "akv_append_kv_q8": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
+                         [ctypes.c_void_p, ctypes.c_int64] * 2 + [ctypes.c_void_p, ctypes.c_int32] +
+                         [ctypes.c_void_p] * 5),
+    "akv_read_kv_q8": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
+                       [ctypes.c_void_p] * 7 + [ctypes.c_int32] + [ctypes.c_void_p] * 2 +
+                       [ctypes.c_int32, ctypes.c_void_p]),
+    "akv_decode_q8_workspace": (ctypes.c_size_t, [ctypes.POINTER(Shape)] + [ctypes.c_int32] * 2),
+    "akv_decode_attention_q8": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
+                                [ctypes.c_void_p] * 9 + [ctypes.c_int32] + [ctypes.c_void_p] * 3 +
+                                [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                 ctypes.c_size_t, ctypes.c_void_p]),
     "akv_append_kv": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.c_int32] +
                       [ctypes.c_void_p] * 6 + [ctypes.c_void_p]),
 }
@@ -663,6 +681,45 @@ def akv_chunk_attention(shp: Shape, B: int, q_indptr, q, k_pool, v_pool, kv_indp
         0 if workspace is None else workspace.numel(), st))
 
 
+def akv_prefix_workspace(shp: Shape, n_groups: int, B: int, n_rows: int, max_rows: int,
+                         max_prefix: int, max_q: int, max_kv: int) -> int:
+    return lib().akv_prefix_workspace(ctypes.byref(shp), n_groups, max_rows, max_prefix, B, n_rows,
+                                      max_q, max_kv)
+
+
+def akv_prefix_attention(shp: Shape, n_groups: int, group_indptr, prefix_indptr, prefix_indices,
+                         B: int, q_indptr, q, k_pool, v_pool, kv_indptr, kv_indices, max_rows: int,
+                         max_prefix: int, max_q: int, max_kv: int, out, lse, workspace,
+                         stream=None):
+    """Attention of each request's rows over their group's shared prefix, read
+    once for the whole group, and the request's own list; lse may be None."""
+    import torch
+    dev, st = _run_on(stream)
+    i32 = torch.int32
+    dt, D, n, S = _torch_dtype(shp), shp.D, q.shape[0], k_pool.shape[0]
+    if n_groups == 0:
+        max_prefix = 0
+    elif prefix_indices is not None:
+        max_prefix = _list_bound(prefix_indices, max_prefix)
+    if B == 0:
+        max_kv = 0
+    elif kv_indices is not None:
+        max_kv = _list_bound(kv_indices, max_kv)
+    _check(lib().akv_prefix_attention(
+        ctypes.byref(shp), n_groups, _typed("group_indptr", group_indptr, i32, dev, (n_groups + 1,)),
+        max_rows, _typed("prefix_indptr", prefix_indptr, i32, dev, (n_groups + 1,)),
+        _typed("prefix_indices", prefix_indices, i32, dev, (None,)), max_prefix, B,
+        _typed("q_indptr", q_indptr, i32, dev, (B + 1,)), n, max_q,
+        _typed("q", q, dt, dev, (n, shp.Hq, D)), _typed("k_pool", k_pool, dt, dev, (S, shp.Hkv, D)),
+        _typed("v_pool", v_pool, dt, dev, (S, shp.Hkv, D)), S,
+        _typed("kv_indptr", kv_indptr, i32, dev, (B + 1,)),
+        _typed("kv_indices", kv_indices, i32, dev, (None,)), max_kv,
+        _typed("out", out, dt, dev, (n, shp.Hq, D)),
+        _typed("lse", lse, torch.float32, dev, (n, shp.Hq)),
+        _typed("workspace", workspace, torch.uint8, dev),
+        0 if workspace is None else workspace.numel(), st))
+
+
 def akv_attention_mass_workspace(shp: Shape, B: int, n_rows: int, max_q: int,
                                  max_kv: int) -> int:
     return lib().akv_attention_mass_workspace(ctypes.byref(shp), B, n_rows, max_q, max_kv)
@@ -708,6 +765,71 @@ def akv_evict_by_mass(B: int, kv_indptr, kv_indices, kv_pos, max_kv: int, mass, 
         _typed("out_mass", out_mass, f32, dev, (B, None)), out_mass.shape[1], cap,
         _typed("dropped_indptr", dropped_indptr, i32, dev, (B + 1,)),
         _typed("dropped", dropped, i32, dev, (None,)), dropped.shape[0], st))
+
+
+def _pools8(shp: Shape, k_pool, v_pool, k_scale, v_scale, dev):
+    """Addresses of an 8-bit cache (e4m3 pools [S, Hkv, D], e8m0 scales [S, Hkv]) and S."""
+    import torch
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    S = k_pool.shape[0]
+    pool, scale = (S, shp.Hkv, shp.D), (S, shp.Hkv)
+    return (_typed("k_pool", k_pool, f8, dev, pool), _typed("v_pool", v_pool, f8, dev, pool),
+            _typed("k_scale", k_scale, e8, dev, scale), _typed("v_scale", v_scale, e8, dev, scale), S)
+
+
+def akv_append_kv_q8(shp: Shape, n: int, k, v, slot, k_pool, v_pool, k_scale, v_scale, stream=None):
+    """Rows k, v [n, Hkv, D] (raw, any stride between tokens) into their slots
+    of an 8-bit cache; slots outside the pool mark padding rows."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, D, Hkv = _torch_dtype(shp), shp.D, shp.Hkv
+    rows = (n, Hkv, D)
+    kp, vp, ks, vs, S = _pools8(shp, k_pool, v_pool, k_scale, v_scale, dev)
+    _check(lib().akv_append_kv_q8(
+        ctypes.byref(shp), n, _typed("k", k, dt, dev, rows, True), k.stride()[0] if n > 1 else Hkv * D,
+        _typed("v", v, dt, dev, rows, True), v.stride()[0] if n > 1 else Hkv * D,
+        _typed("slot", slot, torch.int32, dev, (n,)), S, kp, vp, ks, vs, st))
+
+
+def akv_read_kv_q8(shp: Shape, n: int, src, pos, dst, k_pool, v_pool, k_scale, v_scale, k_out,
+                   v_out, stream=None):
+    """Entries src of an 8-bit cache into rows dst (None: 0 .. n-1) of k_out,
+    v_out [R, Hkv, D], keys rotated at pos (None: as they are stored)."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, i32, R = _torch_dtype(shp), torch.int32, k_out.shape[0]
+    kp, vp, ks, vs, S = _pools8(shp, k_pool, v_pool, k_scale, v_scale, dev)
+    rows = (R, shp.Hkv, shp.D)
+    _check(lib().akv_read_kv_q8(
+        ctypes.byref(shp), n, _typed("src", src, i32, dev, (n,)), _typed("pos", pos, i32, dev, (n,)),
+        _typed("dst", dst, i32, dev, (n,)), kp, vp, ks, vs, S, _typed("k_out", k_out, dt, dev, rows),
+        _typed("v_out", v_out, dt, dev, rows), R, st))
+
+
+def akv_decode_q8_workspace(shp: Shape, B: int, max_kv: int) -> int:
+    return lib().akv_decode_q8_workspace(ctypes.byref(shp), B, max_kv)
+
+
+def akv_decode_attention_q8(shp: Shape, B: int, q, q_pos, k_new, v_new, new_slot, k_pool, v_pool,
+                            k_scale, v_scale, kv_indptr, kv_indices, kv_pos, max_kv: int, out,
+                            workspace, stream=None):
+    """Decode over an 8-bit cache of keys before RoPE, each entry rotated at
+    kv_pos as it is read; k_new/v_new/new_slot (or all None) append the step's
+    token first."""
+    import torch
+    dev, st = _run_on(stream)
+    dt, i32, D = _torch_dtype(shp), torch.int32, shp.D
+    kp, vp, ks, vs, S = _pools8(shp, k_pool, v_pool, k_scale, v_scale, dev)
+    heads, rows = (B, shp.Hq, D), (B, shp.Hkv, D)
+    _check(lib().akv_decode_attention_q8(
+        ctypes.byref(shp), B, _typed("q", q, dt, dev, heads), _typed("q_pos", q_pos, i32, dev, (B,)),
+        _typed("k_new", k_new, dt, dev, rows), _typed("v_new", v_new, dt, dev, rows),
+        _typed("new_slot", new_slot, i32, dev, (B,)), kp, vp, ks, vs, S,
+        _typed("kv_indptr", kv_indptr, i32, dev, (B + 1,)),
+        _typed("kv_indices", kv_indices, i32, dev, (None,)),
+        _typed("kv_pos", kv_pos, i32, dev, tuple(kv_indices.shape)), _list_bound(kv_indices, max_kv),
+        _typed("out", out, dt, dev, heads), _typed("workspace", workspace, torch.uint8, dev),
+        0 if workspace is None else workspace.numel(), st))
 
 
 def to_device(arr: np.ndarray, dtype: str, device="cuda"):

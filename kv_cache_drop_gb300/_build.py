@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libakv.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 SOURCES = ["api.cpp", "cache_tree.cpp", "prep.cu", "attn_simt.cu", "attn_tc.cu", "repos.cu", "compact.cu",
-           "decode.cu", "gemm.cu", "norm.cu", "qk_norm.cu", "chunk.cu", "mass.cu", "evict.cu"]
+           "decode.cu", "gemm.cu", "norm.cu", "qk_norm.cu", "chunk.cu", "mass.cu", "evict.cu",
+           "kv8.cu", "decode8.cu"]
 
 
 def _nvcc() -> str:

@@ -228,6 +228,18 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                          const int32_t *q_indptr, int max_q, const void *q, const void *k,
                          const void *v, const int32_t *kv_indptr, const int32_t *kv_indices,
                          int max_kv, void *out, float *lse, void *ws, cudaStream_t s);
+// The same over a prefix per group of rows and a list per request, joined.
+int64_t prefix_grid_x(int dtype, int Hq, int Hkv, int n_groups, int max_rows, int max_prefix, int B,
+                      int n_rows, int max_q, int max_kv);
+size_t prefix_workspace_bytes(int dtype, int Hq, int Hkv, int n_groups, int max_rows, int max_prefix,
+                              int B, int n_rows, int max_q, int max_kv);
+cudaError_t launch_prefix(int dtype, int Hq, int Hkv, int S, int n_groups,
+                          const int32_t *group_indptr, int max_rows, const int32_t *prefix_indptr,
+                          const int32_t *prefix_indices, int max_prefix, int B,
+                          const int32_t *q_indptr, int n_rows, int max_q, const void *q,
+                          const void *k, const void *v, const int32_t *kv_indptr,
+                          const int32_t *kv_indices, int max_kv, void *out, float *lse, void *ws,
+                          cudaStream_t s);
 size_t mass_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv);
 cudaError_t launch_mass(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                         const int32_t *q_indptr, int max_q, const void *q, const void *k,
@@ -240,5 +252,23 @@ cudaError_t launch_evict(int B, const int32_t *indptr, const int32_t *indices, c
                          int32_t *out_pos, float *out_mass, int64_t out_stride,
                          int64_t out_cap, int32_t *dropped_indptr, int32_t *dropped,
                          int64_t dropped_cap, cudaStream_t s);
+
+// A cache in 8 bits: rows written and read back (kv8.cu), decode (decode8.cu).
+struct Kv8Pool {
+  uint8_t *k, *v;              // [S][Hkv][kD] e4m3 values
+  uint8_t *k_scale, *v_scale;  // [S][Hkv] powers of two: exponent + 127
+  int S;
+};
+cudaError_t launch_append_q8(int dtype, int Hkv, int n, const void *k, int64_t ks, const void *v,
+                             int64_t vs, const int32_t *slot, const Kv8Pool &pool, cudaStream_t s);
+cudaError_t launch_read_q8(int dtype, int Hkv, int n, const int32_t *src, const int32_t *pos,
+                           const int32_t *dst, int R, const Kv8Pool &pool, void *k_out, void *v_out,
+                           const RopeTheta &th, cudaStream_t s);
+size_t decode_q8_workspace_bytes(int dtype, int B, int Hq, int Hkv, int max_kv);
+cudaError_t launch_decode_q8(int dtype, int B, int Hq, int Hkv, const void *q, const int32_t *qpos,
+                             const void *k_new, const void *v_new, const int32_t *new_slot,
+                             const Kv8Pool &pool, const int32_t *indptr, const int32_t *indices,
+                             const int32_t *kvpos, int max_kv, void *out, void *ws,
+                             const RopeTheta &th, cudaStream_t s);
 
 }  // namespace akv

@@ -1442,6 +1442,163 @@ akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t 
 }
 
 // ------------------------------------------------------------------------
+// A prefix that several requests share
+// ------------------------------------------------------------------------
+
+size_t akv_prefix_workspace(const akv_shape *shape, int32_t n_groups, int32_t max_rows,
+                            int32_t max_prefix, int32_t B, int32_t n_rows, int32_t max_q,
+                            int32_t max_kv) {
+  if (!shape || shape->Hq <= 0 || shape->Hkv <= 0 || shape->Hq % shape->Hkv || n_groups < 0 ||
+      max_rows < 0 || max_prefix < 0 || max_prefix > kMaxList || B < 0 || n_rows < 0 || max_q < 0 ||
+      max_kv < 0 || max_kv > kMaxList)
+    return 0;
+  return prefix_workspace_bytes(shape->dtype, shape->Hq, shape->Hkv, n_groups, max_rows, max_prefix,
+                                B, n_rows, max_q, max_kv);
+}
+
+akv_status akv_prefix_attention(const akv_shape *shape, int32_t n_groups,
+                                const int32_t *group_indptr, int32_t max_rows,
+                                const int32_t *prefix_indptr, const int32_t *prefix_indices,
+                                int32_t max_prefix, int32_t B, const int32_t *q_indptr,
+                                int32_t n_rows, int32_t max_q, const void *q, const void *k_pool,
+                                const void *v_pool, int32_t S, const int32_t *kv_indptr,
+                                const int32_t *kv_indices, int32_t max_kv, void *out, float *lse,
+                                void *workspace, size_t workspace_bytes, akv_stream_t stream) {
+  AKV_ENTRY("akv_prefix_attention");
+  const bool prefixes = n_groups > 0 && max_prefix > 0, lists = B > 0 && max_kv > 0;
+  if (akv_status st = check_chunk(shape, n_groups, n_rows, max_rows, S, max_prefix)) return st;
+  if (akv_status st = check_chunk(shape, B, n_rows, max_q, S, max_kv)) return st;
+  if (n_rows == 0 || (n_groups == 0 && B == 0)) return AKV_OK;
+  if (!q || !out || (n_groups > 0 && (!group_indptr || !prefix_indptr)) ||
+      (B > 0 && (!q_indptr || !kv_indptr)) || (prefixes && !prefix_indices) ||
+      (lists && !kv_indices) || ((prefixes || lists) && (!k_pool || !v_pool)))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if (misaligned(q) || misaligned(k_pool) || misaligned(v_pool) || misaligned(out))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  if (prefix_grid_x(shape->dtype, shape->Hq, shape->Hkv, n_groups, max_rows, max_prefix, B, n_rows,
+                    max_q, max_kv) > INT32_MAX ||
+      (int64_t)n_rows * shape->Hq > INT32_MAX)
+    return fail(AKV_ERR_UNSUPPORTED, "prefix attention: %d rows of %d heads exceed a grid", n_rows,
+                shape->Hq);
+  const size_t need = prefix_workspace_bytes(shape->dtype, shape->Hq, shape->Hkv, n_groups, max_rows,
+                                             max_prefix, B, n_rows, max_q, max_kv);
+  if (akv_status st = check_scratch("prefix attention", workspace, workspace_bytes, need)) return st;
+  cudaError_t e = launch_prefix(shape->dtype, shape->Hq, shape->Hkv, S, n_groups, group_indptr,
+                                max_rows, prefix_indptr, prefix_indices, max_prefix, B, q_indptr,
+                                n_rows, max_q, q, k_pool, v_pool, kv_indptr, kv_indices, max_kv, out,
+                                lse, workspace, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix attention");
+  return AKV_OK;
+}
+
+// ------------------------------------------------------------------------
+// A cache in 8 bits
+// ------------------------------------------------------------------------
+
+namespace {
+// the pools of an 8-bit cache: rows of codes at multiples of 16 bytes
+akv_status check_pool8(int32_t S, const void *k_pool, const void *v_pool, const uint8_t *k_scale,
+                       const uint8_t *v_scale) {
+  if (S > 0 && (!k_pool || !v_pool || !k_scale || !v_scale))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if (misaligned(k_pool) || misaligned(v_pool))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  return AKV_OK;
+}
+}  // namespace
+
+akv_status akv_append_kv_q8(const akv_shape *shape, int32_t n, const void *k, int64_t k_stride,
+                            const void *v, int64_t v_stride, const int32_t *slot, int32_t S,
+                            void *k_pool, void *v_pool, uint8_t *k_scale, uint8_t *v_scale,
+                            akv_stream_t stream) {
+  AKV_ENTRY("akv_append_kv_q8");
+  if (akv_status st = check_shape(shape)) return st;
+  if (n < 0 || S < 0) return fail(AKV_ERR_INVALID, "negative size");
+  if (n == 0) return AKV_OK;
+  if (!k || !v || !slot) return fail(AKV_ERR_INVALID, "NULL argument");
+  if (akv_status st = check_pool8(S, k_pool, v_pool, k_scale, v_scale)) return st;
+  const int64_t row = (int64_t)shape->Hkv * shape->D;
+  if (k_stride < row || v_stride < row)
+    return fail(AKV_ERR_INVALID, "row strides must be at least the rows' length (%lld)",
+                (long long)row);
+  const int64_t per16 = 16 / (int64_t)esize(shape->dtype);
+  if (k_stride % per16 || v_stride % per16 || misaligned(k) || misaligned(v))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  if ((int64_t)n * shape->Hkv > INT32_MAX)
+    return fail(AKV_ERR_UNSUPPORTED, "8-bit append supports n * Hkv < 2^31");
+  cudaError_t e = launch_append_q8(shape->dtype, shape->Hkv, n, k, k_stride, v, v_stride, slot,
+                                   Kv8Pool{(uint8_t *)k_pool, (uint8_t *)v_pool, k_scale, v_scale, S},
+                                   (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit append");
+  return AKV_OK;
+}
+
+akv_status akv_read_kv_q8(const akv_shape *shape, int32_t n, const int32_t *src, const int32_t *pos,
+                          const int32_t *dst, const void *k_pool, const void *v_pool,
+                          const uint8_t *k_scale, const uint8_t *v_scale, int32_t S, void *k_out,
+                          void *v_out, int32_t R, akv_stream_t stream) {
+  AKV_ENTRY("akv_read_kv_q8");
+  if (akv_status st = check_shape(shape)) return st;
+  if (n < 0 || S < 0 || R < 0) return fail(AKV_ERR_INVALID, "negative size");
+  if (n == 0 || R == 0) return AKV_OK;
+  if (!src || !k_out || !v_out) return fail(AKV_ERR_INVALID, "NULL argument");
+  if (akv_status st = check_pool8(S, k_pool, v_pool, k_scale, v_scale)) return st;
+  if (misaligned(k_out) || misaligned(v_out))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  RopeTheta th;
+  rope_theta(shape->rope_base, &th);
+  cudaError_t e = launch_read_q8(shape->dtype, shape->Hkv, n, src, pos, dst, R,
+                                 Kv8Pool{(uint8_t *)k_pool, (uint8_t *)v_pool, (uint8_t *)k_scale,
+                                         (uint8_t *)v_scale, S},
+                                 k_out, v_out, th, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit read");
+  return AKV_OK;
+}
+
+size_t akv_decode_q8_workspace(const akv_shape *shape, int32_t B, int32_t max_kv) {
+  if (!shape || shape->Hq <= 0 || shape->Hkv <= 0 || shape->Hq % shape->Hkv || B <= 0 || max_kv < 0 ||
+      max_kv > kMaxList)
+    return 0;
+  return decode_q8_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, max_kv);
+}
+
+akv_status akv_decode_attention_q8(const akv_shape *shape, int32_t B, const void *q,
+                                   const int32_t *q_pos, const void *k_new, const void *v_new,
+                                   const int32_t *new_slot, void *k_pool, void *v_pool,
+                                   uint8_t *k_scale, uint8_t *v_scale, int32_t S,
+                                   const int32_t *kv_indptr, const int32_t *kv_indices,
+                                   const int32_t *kv_pos, int32_t max_kv, void *out,
+                                   void *workspace, size_t workspace_bytes, akv_stream_t stream) {
+  AKV_ENTRY("akv_decode_attention_q8");
+  if (akv_status st = check_shape(shape)) return st;
+  if (B < 0 || max_kv < 0 || S < 0) return fail(AKV_ERR_INVALID, "negative size");
+  if (B > 65535 || shape->Hq > 65535)
+    return fail(AKV_ERR_UNSUPPORTED, "8-bit decode supports B <= 65535 and Hq <= 65535");
+  if (max_kv > kMaxList)
+    return fail(AKV_ERR_UNSUPPORTED, "8-bit decode supports max_kv <= %d", kMaxList);
+  if (B == 0) return AKV_OK;
+  if (!q || !q_pos || !kv_indptr || !out || (max_kv > 0 && (!kv_indices || !kv_pos)))
+    return fail(AKV_ERR_INVALID, "NULL argument");
+  if ((new_slot == nullptr) != (k_new == nullptr) || (new_slot == nullptr) != (v_new == nullptr))
+    return fail(AKV_ERR_INVALID, "k_new, v_new and new_slot are given together or not at all");
+  if (max_kv > 0 && S == 0) return fail(AKV_ERR_INVALID, "lists over an empty pool (S = 0)");
+  if (akv_status st = check_pool8(S, k_pool, v_pool, k_scale, v_scale)) return st;
+  if (misaligned(q) || misaligned(k_new) || misaligned(v_new) || misaligned(out))
+    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  const size_t need = decode_q8_workspace_bytes(shape->dtype, B, shape->Hq, shape->Hkv, max_kv);
+  if (akv_status st = check_scratch("8-bit decode", workspace, workspace_bytes, need)) return st;
+  RopeTheta th;
+  rope_theta(shape->rope_base, &th);
+  cudaError_t e = launch_decode_q8(shape->dtype, B, shape->Hq, shape->Hkv, q, q_pos, k_new, v_new,
+                                   new_slot,
+                                   Kv8Pool{(uint8_t *)k_pool, (uint8_t *)v_pool, k_scale, v_scale, S},
+                                   kv_indptr, kv_indices, kv_pos, max_kv, out, workspace, th,
+                                   (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit decode");
+  return AKV_OK;
+}
+
+// ------------------------------------------------------------------------
 // Decoder layers around the segment attention
 // ------------------------------------------------------------------------
 

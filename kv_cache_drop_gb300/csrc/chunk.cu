@@ -21,7 +21,11 @@ struct ChunkParts {
   float2 *ml;
   float *o;
   int ns, chunk;
-  __device__ __forceinline__ bool direct(int lim) const { return ns == 1 || lim <= chunk; }
+  bool joined;       // every row's splits are merged with those of another list
+  bool keep_status;  // an earlier kernel of the call has cleared the status word
+  __device__ __forceinline__ bool direct(int lim) const {
+    return !joined && (ns == 1 || lim <= chunk);
+  }
 };
 constexpr int kMaxSplit = 1024;  // the merge keeps one weight per split in shared memory
 
@@ -56,7 +60,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   F32Smem &sm = *reinterpret_cast<F32Smem *>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  clear_status(status);
+  if (!part.keep_status) clear_status(status);
   const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
   const int64_t r0 = (int64_t)(blockIdx.x / part.ns) * kFRows;
   const ChunkReq rq = chunk_req(a, b);
@@ -189,9 +193,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
   }
 }
 
-// The splits that hold row t's visible entries; 0 where there is nothing to
-// merge (written by its one split, or no request's row).
-__device__ __forceinline__ int merge_used(const ChunkBatch &a, const ChunkParts &part, int t) {
+// Entries that row t sees of its request's list; -1 where no request holds it.
+__device__ __forceinline__ int row_limit(const ChunkBatch &a, int t) {
   int lo = 0, hi = a.B;  // the request that holds row t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -199,9 +202,13 @@ __device__ __forceinline__ int merge_used(const ChunkBatch &a, const ChunkParts 
   }
   const ChunkReq rq = chunk_req(a, lo);
   const int i = t - rq.q0;
-  if (i < 0 || i >= rq.m) return 0;
-  const int lim = rq.limit(i);
-  return part.direct(lim) ? 0 : (lim + part.chunk - 1) / part.chunk;
+  return i < 0 || i >= rq.m ? -1 : rq.limit(i);
+}
+// The splits that hold row t's visible entries; 0 where there is nothing to
+// merge (written by its one split, or no request's row).
+__device__ __forceinline__ int merge_used(const ChunkBatch &a, const ChunkParts &part, int t) {
+  const int lim = row_limit(a, t);
+  return lim < 0 || part.direct(lim) ? 0 : (lim + part.chunk - 1) / part.chunk;
 }
 
 // Joins the splits of a row by their log-sum-exp; launched as a programmatic
@@ -314,6 +321,144 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // ---------------------------------------------------------------------------
+// A shared prefix.  The attention kernels run twice, over the groups' prefix
+// lists with the rows of all of a group's requests as one chunk that sees the
+// whole list, and over the requests' own lists; each leaves every row's splits
+// as partials, and the kernels below join a row's splits of both.
+// ---------------------------------------------------------------------------
+struct PrefixParts {
+  ChunkBatch batch;
+  ChunkParts part;
+  // splits that hold what row t sees; -1 where no list is the row's
+  __device__ __forceinline__ int used(int t) const {
+    const int lim = batch.B > 0 ? row_limit(batch, t) : -1;
+    return lim < 0 ? -1 : (lim + part.chunk - 1) / part.chunk;
+  }
+};
+
+// Up to kWarpMerge splits of both lists: a warp per (row, head), two columns
+// and one split's weight per lane.
+template <typename T>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    prefix_merge_warp_kernel(const PrefixParts pre, const PrefixParts own, T *out, float *lse,
+                             uint32_t *status) {
+  const int Hq = own.batch.Hq;
+  const int64_t w = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, t = (int)(w / Hq);
+  if (status) clear_status(status);
+  int na = -1, nb = -1;
+  if (t < own.batch.n_rows) {
+    na = pre.used(t);
+    nb = own.used(t);
+  }
+  // every warp waits, so that this grid never ends before the one it follows
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (na < 0 && nb < 0) return;  // no request's row
+  na = max(na, 0);
+  nb = max(nb, 0);
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < na) ml = __ldcg(pre.part.ml + w * pre.part.ns + lane);
+  else if (lane - na < nb) ml = __ldcg(own.part.ml + w * own.part.ns + lane - na);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+  float L = ml.y * f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float x0 = 0.f, x1 = 0.f;
+  const float2 *pa = reinterpret_cast<const float2 *>(pre.part.o + w * pre.part.ns * kD) + lane;
+  const float2 *pb = reinterpret_cast<const float2 *>(own.part.o + w * own.part.ns * kD) + lane;
+#pragma unroll 4
+  for (int s = 0; s < na + nb; ++s) {
+    const float2 v = __ldcg(s < na ? pa + s * (kD / 2) : pb + (s - na) * (kD / 2));
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+    x0 = fmaf(v.x, fs, x0);
+    x1 = fmaf(v.y, fs, x1);
+  }
+  const bool none = na + nb == 0;
+  x0 = none ? 0.f : x0 / L;
+  x1 = none ? 0.f : x1 / L;
+  if constexpr (sizeof(T) == 4) reinterpret_cast<float2 *>(out + w * kD)[lane] = make_float2(x0, x1);
+  else reinterpret_cast<__nv_bfloat162 *>(out + w * kD)[lane] = __floats2bfloat162_rn(x0, x1);
+  if (lse && lane == 0) lse[w] = none ? -INFINITY : M * kLn2 + logf(L);
+}
+
+// More splits: a CTA per (row, head), eight groups of 16 threads each summing
+// every eighth split's row, 16 bytes per load.
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads)
+    prefix_merge_kernel(const PrefixParts pre, const PrefixParts own, T *out, float *lse,
+                        uint32_t *status) {
+  __shared__ float wgt[2 * kMaxSplit];
+  __shared__ float4 red[8][kD / 4];
+  __shared__ float tot[kMergeThreads / 32], top[kMergeThreads / 32];
+  const int64_t w = blockIdx.x;
+  const int t = (int)(w / own.batch.Hq);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (status) clear_status(status);
+  int na = pre.used(t), nb = own.used(t);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (na < 0 && nb < 0) return;
+  na = max(na, 0);
+  nb = max(nb, 0);
+  const int n = na + nb;
+  const float2 *ma = pre.part.ml + w * pre.part.ns, *mb = own.part.ml + w * own.part.ns - na;
+  float M = -INFINITY;
+  for (int s = threadIdx.x; s < n; s += kMergeThreads) {
+    const float m = __ldcg(&(s < na ? ma : mb)[s].x);
+    wgt[s] = m;
+    M = fmaxf(M, m);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) top[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int s = threadIdx.x; s < n; s += kMergeThreads) {
+    const float f = exp2f(wgt[s] - ref);
+    wgt[s] = f;
+    L = fmaf(__ldcg(&(s < na ? ma : mb)[s].y), f, L);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) tot[warp] = L;
+  __syncthreads();
+  L = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+  const int cg = threadIdx.x & 15, sg = threadIdx.x >> 4;
+  const float4 *oa = reinterpret_cast<const float4 *>(pre.part.o + w * pre.part.ns * kD) + cg;
+  const float4 *ob = reinterpret_cast<const float4 *>(own.part.o + (w * own.part.ns - na) * kD) + cg;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = sg; s < n; s += 8) {
+    const float4 v = __ldcg((s < na ? oa : ob) + s * (kD / 4));
+    const float f = wgt[s];
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  red[sg][cg] = acc;
+  __syncthreads();
+  if (threadIdx.x < kD / 4) {
+    float y[4] = {};
+    for (int g = 0; g < 8; ++g) {
+      const float4 v = red[g][threadIdx.x];
+      y[0] += v.x;
+      y[1] += v.y;
+      y[2] += v.z;
+      y[3] += v.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = n == 0 ? 0.f : y[e] / L;
+    store4<T>(out + w * kD + 4 * threadIdx.x, y);
+  }
+  if (lse && threadIdx.x == 0) lse[w] = n == 0 ? -INFINITY : M * kLn2 + logf(L);
+}
+
+// ---------------------------------------------------------------------------
 // bf16, few rows (decode steps, short verification chunks): up to 16
 // packed rows per KV head.  CTA = key split x request, a warp per KV head (up
 // to eight heads a CTA), so that a key's heads are read together.  Keys and
@@ -333,7 +478,7 @@ __global__ void __launch_bounds__(kSHeads * 32, 2)
   constexpr int kSt = kSSt;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  clear_status(status);
+  if (!part.keep_status) clear_status(status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int split = blockIdx.x, b = blockIdx.y, g = blockIdx.z * kSHeads + warp;
@@ -645,7 +790,7 @@ __global__ void __launch_bounds__(tc_threads(kTiles), kTiles == 1 ? 2 : 1)
   TcSmem<kTiles> &sm = *reinterpret_cast<TcSmem<kTiles> *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  clear_status(status);
+  if (!part.keep_status) clear_status(status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the last row tiles see the most: they come first
   const int split = blockIdx.x % part.ns, g = blockIdx.y, b = blockIdx.z;
@@ -1299,11 +1444,11 @@ cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkPar
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
-                         cudaStream_t s) {
-  const int64_t items = (int64_t)a.n_rows * a.Hq;
-  const bool warps = part.ns <= kWarpMerge;
+// a merge over `items` (row, head) pairs as a programmatic dependent of the
+// kernel launched before it
+template <typename... P, typename... A>
+cudaError_t launch_join(int64_t items, bool warps, void (*warp_kernel)(P...),
+                        void (*cta_kernel)(P...), cudaStream_t s, const A &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(warps ? (items + kMergeWarps - 1) / kMergeWarps : items));
   cfg.blockDim = dim3(warps ? kMergeWarps * 32 : kMergeThreads);
@@ -1313,8 +1458,54 @@ cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const Chunk
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, warps ? chunk_merge_warp_kernel<T> : chunk_merge_kernel<T>, a,
-                            (T *)out, lse, part);
+  return cudaLaunchKernelEx(&cfg, warps ? warp_kernel : cta_kernel, args...);
+}
+
+template <typename T>
+cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+                         cudaStream_t s) {
+  return launch_join((int64_t)a.n_rows * a.Hq, part.ns <= kWarpMerge, chunk_merge_warp_kernel<T>,
+                     chunk_merge_kernel<T>, s, a, (T *)out, lse, part);
+}
+
+template <typename T>
+cudaError_t launch_prefix_merge(const PrefixParts &pre, const PrefixParts &own, void *out, float *lse,
+                                uint32_t *status, cudaStream_t s) {
+  return launch_join((int64_t)own.batch.n_rows * own.batch.Hq,
+                     pre.part.ns + own.part.ns <= kWarpMerge, prefix_merge_warp_kernel<T>,
+                     prefix_merge_kernel<T>, s, pre, own, (T *)out, lse, status);
+}
+
+cudaError_t launch_kind(const ChunkPlan &p, const ChunkBatch &a, void *out, float *lse,
+                        const ChunkParts &part, uint32_t *status, cudaStream_t s) {
+  if (p.kind == kTcKind) return launch_tc<1>(a, out, lse, part, p.tiles, status, s);
+  if (p.kind == kTcKind + 1) return launch_tc<2>(a, out, lse, part, p.tiles, status, s);
+  if (p.kind == kSmallKind) return launch_small(a, out, lse, part, status, s);
+  return launch_f32(a, out, lse, part, p.tiles, status, s);
+}
+
+size_t parts_bytes(int n_rows, int Hq, int ns) {
+  const size_t parts = (size_t)n_rows * Hq * ns;
+  return up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
+}
+ChunkParts parts_at(char *at, int n_rows, int Hq, const ChunkPlan &p) {
+  return ChunkParts{(float2 *)at, (float *)(at + up256((size_t)n_rows * Hq * p.ns * sizeof(float2))),
+                    p.ns, p.chunk, false, false};
+}
+
+// the two passes of a prefix call: over the groups, over the requests
+struct PrefixPlan {
+  ChunkPlan pre, own;
+};
+PrefixPlan prefix_plan(int dtype, int Hq, int Hkv, int n_groups, int max_rows, int max_prefix,
+                       int B, int n_rows, int max_q, int max_kv) {
+  const ChunkPlan none{0, 1, 128, 0};
+  PrefixPlan p{none, none};
+  if (n_groups > 0 && max_rows > 0 && max_prefix > 0)
+    p.pre = chunk_plan(dtype, n_groups, Hq, Hkv, n_rows, max_rows, max_prefix);
+  if (B > 0 && max_q > 0 && max_kv > 0)
+    p.own = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
+  return p;
 }
 
 }  // namespace
@@ -1326,9 +1517,7 @@ int64_t chunk_grid_x(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, i
 
 size_t chunk_workspace_bytes(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, int max_kv) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
-  if (p.ns == 1) return kTcStatusBytes;
-  const size_t parts = (size_t)n_rows * Hq * p.ns;
-  return kTcStatusBytes + up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
+  return kTcStatusBytes + (p.ns == 1 ? 0 : parts_bytes(n_rows, Hq, p.ns));
 }
 
 cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
@@ -1336,18 +1525,62 @@ cudaError_t launch_chunk(int dtype, int B, int Hq, int Hkv, int n_rows, int S,
                          const void *v, const int32_t *kv_indptr, const int32_t *kv_indices,
                          int max_kv, void *out, float *lse, void *ws, cudaStream_t s) {
   const ChunkPlan p = chunk_plan(dtype, B, Hq, Hkv, n_rows, max_q, max_kv);
-  const ChunkBatch a{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q, k, v};
-  char *const w = (char *)ws + kTcStatusBytes;
-  const ChunkParts part{(float2 *)w, (float *)(w + up256((size_t)n_rows * Hq * p.ns * sizeof(float2))),
-                        p.ns, p.chunk};
-  cudaError_t e;
-  if (p.kind == kTcKind) e = launch_tc<1>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
-  else if (p.kind == kTcKind + 1) e = launch_tc<2>(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
-  else if (p.kind == kSmallKind) e = launch_small(a, out, lse, part, (uint32_t *)ws, s);
-  else e = launch_f32(a, out, lse, part, p.tiles, (uint32_t *)ws, s);
+  const ChunkBatch a{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q, k, v,
+                     false};
+  const ChunkParts part = parts_at((char *)ws + kTcStatusBytes, n_rows, Hq, p);
+  const cudaError_t e = launch_kind(p, a, out, lse, part, (uint32_t *)ws, s);
   if (e != cudaSuccess || p.ns == 1) return e;
   return dtype == AKV_BF16 ? launch_merge<__nv_bfloat16>(a, out, lse, part, s)
                            : launch_merge<float>(a, out, lse, part, s);
+}
+
+int64_t prefix_grid_x(int dtype, int Hq, int Hkv, int n_groups, int max_rows, int max_prefix, int B,
+                      int n_rows, int max_q, int max_kv) {
+  const PrefixPlan p = prefix_plan(dtype, Hq, Hkv, n_groups, max_rows, max_prefix, B, n_rows, max_q,
+                                   max_kv);
+  return std::max(p.pre.tiles * p.pre.ns, p.own.tiles * p.own.ns);
+}
+
+size_t prefix_workspace_bytes(int dtype, int Hq, int Hkv, int n_groups, int max_rows, int max_prefix,
+                              int B, int n_rows, int max_q, int max_kv) {
+  const PrefixPlan p = prefix_plan(dtype, Hq, Hkv, n_groups, max_rows, max_prefix, B, n_rows, max_q,
+                                   max_kv);
+  return kTcStatusBytes + parts_bytes(n_rows, Hq, p.pre.ns) + parts_bytes(n_rows, Hq, p.own.ns);
+}
+
+cudaError_t launch_prefix(int dtype, int Hq, int Hkv, int S, int n_groups,
+                          const int32_t *group_indptr, int max_rows, const int32_t *prefix_indptr,
+                          const int32_t *prefix_indices, int max_prefix, int B,
+                          const int32_t *q_indptr, int n_rows, int max_q, const void *q,
+                          const void *k, const void *v, const int32_t *kv_indptr,
+                          const int32_t *kv_indices, int max_kv, void *out, float *lse, void *ws,
+                          cudaStream_t s) {
+  const PrefixPlan p = prefix_plan(dtype, Hq, Hkv, n_groups, max_rows, max_prefix, B, n_rows, max_q,
+                                   max_kv);
+  char *const w = (char *)ws + kTcStatusBytes;
+  PrefixParts pre{ChunkBatch{n_groups, Hq, Hkv, n_rows, S, max_rows, max_prefix, group_indptr,
+                             prefix_indptr, prefix_indices, q, k, v, true},
+                  parts_at(w, n_rows, Hq, p.pre)};
+  PrefixParts own{ChunkBatch{B, Hq, Hkv, n_rows, S, max_q, max_kv, q_indptr, kv_indptr, kv_indices, q,
+                             k, v, false},
+                  parts_at(w + parts_bytes(n_rows, Hq, p.pre.ns), n_rows, Hq, p.own)};
+  pre.part.joined = own.part.joined = true;
+  uint32_t *const status = (uint32_t *)ws;
+  bool cleared = false;
+  if (p.pre.tiles > 0) {
+    const cudaError_t e = launch_kind(p.pre, pre.batch, out, lse, pre.part, status, s);
+    if (e != cudaSuccess) return e;
+    cleared = true;
+  }
+  if (p.own.tiles > 0) {
+    own.part.keep_status = cleared;
+    const cudaError_t e = launch_kind(p.own, own.batch, out, lse, own.part, status, s);
+    if (e != cudaSuccess) return e;
+    cleared = true;
+  }
+  uint32_t *const clear = cleared ? nullptr : status;
+  return dtype == AKV_BF16 ? launch_prefix_merge<__nv_bfloat16>(pre, own, out, lse, clear, s)
+                           : launch_prefix_merge<float>(pre, own, out, lse, clear, s);
 }
 
 }  // namespace akv

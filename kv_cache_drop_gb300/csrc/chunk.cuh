@@ -5,7 +5,8 @@
 // Rows.  The query rows of KV head g are packed (token, head of the group):
 // packed row r of request b is token i = r / grp of its chunk and query head
 // g * grp + r % grp, so that one K/V tile serves every row that reads it.
-// Row i of a chunk of m tokens sees the list entries j < n - m + i + 1.
+// Row i of a chunk of m tokens sees the list entries j < n - m + i + 1, or, of a
+// shared prefix, all n.
 #pragma once
 
 #include "common.cuh"
@@ -17,13 +18,15 @@ struct ChunkBatch {
   int B, Hq, Hkv, n_rows, S, max_q, max_kv;
   const int32_t *q_indptr, *kv_indptr, *kv_indices;
   const void *q, *k, *v;
+  bool whole;  // every row sees its whole list
 };
 
 struct ChunkReq {
   int q0, m;    // first row of the chunk in q, its tokens
   int beg, n;   // first list entry, entries
+  int first;    // entries that token 0 sees, each later one a further one (n - m + 1 or n)
   __device__ __forceinline__ int limit(int i) const {  // entries that token i sees
-    return min(n, max(0, n - m + i + 1));
+    return min(n, max(0, first + i));
   }
 };
 
@@ -36,6 +39,7 @@ __device__ __forceinline__ ChunkReq chunk_req(const ChunkBatch &a, int b) {
   r.m = max(0, min(min(a.q_indptr[b + 1], a.n_rows) - r.q0, a.max_q));
   r.beg = a.kv_indptr[b];
   r.n = min(max(a.kv_indptr[b + 1] - r.beg, 0), a.max_kv);
+  r.first = a.whole ? r.n : r.n - r.m + 1;
   return r;
 }
 

@@ -1,0 +1,144 @@
+// Rows of an 8-bit cache written and read back (paper review page section 3.3:
+// append stores a token's key and value; a repos turns a stored key to another
+// position).  Keys are kept before RoPE, so that a repos only rewrites positions:
+// a key that was stored rotated would be rounded to 8 bits again at every turn.
+#include "kv8.cuh"
+
+#include <algorithm>
+
+namespace akv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanes = 4;             // lanes per head row
+constexpr int kEach = kD / kLanes;    // values per lane
+constexpr int kRows = 32 / kLanes;    // head rows per pass of a warp
+
+// Bound by HBM: a row is read once (128 or 256 bytes) and written once (64 and
+// a byte).  Four lanes take a head row, 16 values each: the maximum is two
+// shuffles and a lane's codes are one 16-byte store.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    kv8_append_kernel(int rows, int Hkv, const T *__restrict__ k, int64_t ks,
+                      const T *__restrict__ v, int64_t vs, const int32_t *__restrict__ slot,
+                      const Kv8Pool pool) {
+  constexpr int E = Chunk<T>::kElems;
+  const int r = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  const bool value = blockIdx.y != 0;
+  const int i = r / Hkv, h = r - i * Hkv;
+  const int at = r < rows ? __ldg(slot + i) : -1;
+  const bool real = (unsigned)at < (unsigned)pool.S;  // else padding: nothing read or written
+  const uint4 *src = reinterpret_cast<const uint4 *>(
+      (value ? v + i * vs : k + i * ks) + (int64_t)h * kD + c * kEach);
+  float x[kEach];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kEach / E; ++j)
+    chunk_to_f32<T>(real ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u), x + j * E);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) top = max(top, kv8_size(x[e]));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  if (!real) return;
+  const uint32_t scale = kv8_scale(top);
+  const float inv = kv8_inverse(scale);
+  const int64_t to = (int64_t)at * Hkv + h;
+  reinterpret_cast<uint4 *>((value ? pool.v : pool.k) + to * kD)[c] =
+      make_uint4(kv8_codes(x, inv), kv8_codes(x + 4, inv), kv8_codes(x + 8, inv),
+                 kv8_codes(x + 12, inv));
+  if (c == 0) (value ? pool.v_scale : pool.k_scale)[to] = (uint8_t)scale;
+}
+
+// A warp per entry: its 2 Hkv head rows, eight at a time; lane f forms the angle
+// of frequency f once and the lanes fetch theirs by shuffle.  Lane c of a row
+// holds values 8 c .. 8 c + 7 and the 32 + of these: the two sides of its
+// rotation pairs.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    kv8_read_kernel(int n, int Hkv, const int32_t *__restrict__ src,
+                    const int32_t *__restrict__ pos, const int32_t *__restrict__ dst, int R,
+                    const Kv8Pool pool, T *k_out, T *v_out, const __grid_constant__ RopeTheta th) {
+  __shared__ ThetaSmem ts;
+  const int lane = threadIdx.x & 31, c = lane % kLanes, r = lane / kLanes;
+  const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  stage_theta(th, ts);
+  __syncthreads();
+  if (i >= n) return;
+  const int from = __ldg(src + i), to = dst ? __ldg(dst + i) : (int)i;
+  if ((unsigned)from >= (unsigned)pool.S || (unsigned)to >= (unsigned)R) return;
+  float co[8], si[8];
+  if (pos) {
+    float cf, sf;
+    rope_cs(th, ts, lane, __ldg(pos + i), &cf, &sf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      co[e] = __shfl_sync(0xffffffffu, cf, 8 * c + e);
+      si[e] = __shfl_sync(0xffffffffu, sf, 8 * c + e);
+    }
+  }
+  for (int x = r; x < 2 * Hkv; x += kRows) {
+    const bool value = x >= Hkv;
+    const int h = value ? x - Hkv : x;
+    const int64_t at = (int64_t)from * Hkv + h;
+    const uint2 *row = reinterpret_cast<const uint2 *>((value ? pool.v : pool.k) + at * kD);
+    const uint2 a = __ldg(row + c), b = __ldg(row + c + kLanes);
+    const float power = kv8_power(__ldg((value ? pool.v_scale : pool.k_scale) + at));
+    float y0[8], y1[8];
+    kv8_floats(a.x, power, y0);
+    kv8_floats(a.y, power, y0 + 4);
+    kv8_floats(b.x, power, y1);
+    kv8_floats(b.y, power, y1 + 4);
+    if (pos && !value) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = y0[e], w = y1[e];
+        y0[e] = u * co[e] - w * si[e];
+        y1[e] = u * si[e] + w * co[e];
+      }
+    }
+    constexpr int E = Chunk<T>::kElems;
+    uint4 *out = reinterpret_cast<uint4 *>((value ? v_out : k_out) + ((int64_t)to * Hkv + h) * kD);
+#pragma unroll
+    for (int j = 0; j < 8 / E; ++j) {
+      out[c * (8 / E) + j] = f32_to_chunk<T>(y0 + j * E);
+      out[(c + kLanes) * (8 / E) + j] = f32_to_chunk<T>(y1 + j * E);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t append(int Hkv, int n, const void *k, int64_t ks, const void *v, int64_t vs,
+                   const int32_t *slot, const Kv8Pool &pool, cudaStream_t s) {
+  const int rows = n * Hkv, per = kThreads / kLanes;
+  kv8_append_kernel<T><<<dim3((unsigned)(((int64_t)rows + per - 1) / per), 2), kThreads, 0, s>>>(
+      rows, Hkv, (const T *)k, ks, (const T *)v, vs, slot, pool);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t read(int Hkv, int n, const int32_t *src, const int32_t *pos, const int32_t *dst, int R,
+                 const Kv8Pool &pool, void *k_out, void *v_out, const RopeTheta &th,
+                 cudaStream_t s) {
+  const int per = kThreads / 32;
+  kv8_read_kernel<T><<<(unsigned)(((int64_t)n + per - 1) / per), kThreads, 0, s>>>(
+      n, Hkv, src, pos, dst, R, pool, (T *)k_out, (T *)v_out, th);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_q8(int dtype, int Hkv, int n, const void *k, int64_t ks, const void *v,
+                             int64_t vs, const int32_t *slot, const Kv8Pool &pool, cudaStream_t s) {
+  return dtype == AKV_BF16 ? append<__nv_bfloat16>(Hkv, n, k, ks, v, vs, slot, pool, s)
+                           : append<float>(Hkv, n, k, ks, v, vs, slot, pool, s);
+}
+
+cudaError_t launch_read_q8(int dtype, int Hkv, int n, const int32_t *src, const int32_t *pos,
+                           const int32_t *dst, int R, const Kv8Pool &pool, void *k_out, void *v_out,
+                           const RopeTheta &th, cudaStream_t s) {
+  return dtype == AKV_BF16
+             ? read<__nv_bfloat16>(Hkv, n, src, pos, dst, R, pool, k_out, v_out, th, s)
+             : read<float>(Hkv, n, src, pos, dst, R, pool, k_out, v_out, th, s);
+}
+
+}  // namespace akv
