@@ -639,8 +639,8 @@ akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t 
  * Keys are kept before RoPE and lists carry positions (as for
  * akv_decode_attention_rope): a repos rewrites positions only, where stored
  * rotated keys would be rounded to 8 bits again at every turn.
- * k_pool, v_pool, rows of q, k, v and outputs must start at multiples of 16
- * bytes (AKV_ERR_INVALID); the pools may be NULL where S is 0.
+ * The pools, their scales, rows of q, k, v and outputs must start at multiples
+ * of 16 bytes (AKV_ERR_INVALID); the pools may be NULL where S is 0.
  *
  * akv_append_kv_q8: token i < n of k and v (device, raw, at i * {k,v}_stride
  * elements, its heads contiguous, so that they may be column blocks of one

@@ -1496,13 +1496,13 @@ akv_status akv_prefix_attention(const akv_shape *shape, int32_t n_groups,
 // ------------------------------------------------------------------------
 
 namespace {
-// the pools of an 8-bit cache: rows of codes at multiples of 16 bytes
+// the pools of an 8-bit cache
 akv_status check_pool8(int32_t S, const void *k_pool, const void *v_pool, const uint8_t *k_scale,
                        const uint8_t *v_scale) {
   if (S > 0 && (!k_pool || !v_pool || !k_scale || !v_scale))
     return fail(AKV_ERR_INVALID, "NULL argument");
-  if (misaligned(k_pool) || misaligned(v_pool))
-    return fail(AKV_ERR_INVALID, "rows must start at multiples of 16 bytes");
+  if (misaligned(k_pool) || misaligned(v_pool) || misaligned(k_scale) || misaligned(v_scale))
+    return fail(AKV_ERR_INVALID, "pools and their scales must start at multiples of 16 bytes");
   return AKV_OK;
 }
 }  // namespace

@@ -38,7 +38,8 @@ def _prefix(akv, **change):  # noqa: F811
 def test_append_refusals(akv):  # noqa: F811
     for change in (dict(n=-1), dict(S=-1), dict(k=None), dict(v=None), dict(slot=None), dict(kp=None),
                    dict(vp=None), dict(k_scale=None), dict(v_scale=None), dict(ks=120), dict(vs=127), dict(ks=132),
-                   dict(k=P + 8), dict(v=P + 2), dict(kp=P + 8), dict(vp=P + 4), dict(shape=akv.shape(7, 2))):
+                   dict(k=P + 8), dict(v=P + 2), dict(kp=P + 8), dict(vp=P + 4), dict(k_scale=P + 2),
+                   dict(v_scale=P + 8), dict(shape=akv.shape(7, 2))):
         assert _append(akv, **change) == INVALID, change
         assert akv.lib().akv_last_error()
     assert _append(akv, shape=akv.shape(8, 2, 128)) == UNSUPPORTED
