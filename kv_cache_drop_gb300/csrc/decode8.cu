@@ -7,6 +7,7 @@
 #include "kv8.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace akv {
 namespace {
@@ -23,10 +24,13 @@ struct Decode8 {
   Kv8Pool pool;
   const int32_t *indptr, *indices, *kvpos;
   int max_kv;
-  // split-KV partials [B][Hq][ns]: (maximum in log2 units, sum), sums of weighted values
+  // partials: (maximum in log2 units, sum), sums of weighted values; fp32
+  // [B][Hq][ctas], bf16 [range + request][sub][Hq]
   float2 *ml;
   float *o;
-  int ns, chunk, per;  // partials, entries of a split, partials of a split
+  int ctas;   // CTAs along a list (fp32), along all lists (bf16)
+  int chunk;  // fp32: entries of each
+  int sub;    // bf16: groups of warps that share out a CTA's entries
 };
 
 // A request's entries, held to the bound the workspace was sized for.
@@ -218,21 +222,24 @@ __global__ void __launch_bounds__(kSThreads)
 #pragma unroll
   for (int x = 0; x < kSHeads / 2; ++x)
     if (odd + 2 * x < heads)
-      a.o[(((int64_t)b * a.Hq + h0 + odd + 2 * x) * a.ns + split) * kD + d] = o[x];
+      a.o[(((int64_t)b * a.Hq + h0 + odd + 2 * x) * a.ctas + split) * kD + d] = o[x];
 #pragma unroll
   for (int x = 0; x < kSHeads / 4; ++x) {
     float s = l[x];
 #pragma unroll
     for (int y = 16; y; y >>= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
     if (lane == 0 && warp + 4 * x < heads)
-      a.ml[((int64_t)b * a.Hq + h0 + warp + 4 * x) * a.ns + split] = make_float2(m[x] * kScale, s);
+      a.ml[((int64_t)b * a.Hq + h0 + warp + 4 * x) * a.ctas + split] = make_float2(m[x] * kScale, s);
   }
 }
 
 // ---------------------------------------------------------------------------
-// bf16: mma.sync, a warp per (KV head, 16 entries at a time).  CTA = key split x up
-// to eight KV heads x request; with fewer heads the warps share out the tiles
-// (`sub` of them at a time), each with a partial of its own.
+// bf16: mma.sync.  The entries of all lists, one list behind the other, are cut
+// into equal ranges, one for each CTA that the GPU holds at a time, so that lists
+// of any lengths leave no SM idle; a range may end inside a list and hold several
+// lists, and leaves a partial for each list that it touches.  A CTA takes up to
+// eight KV heads, a warp each, 16 entries at a time; with fewer heads kSub groups of
+// warps take 16 entries each.
 //   S = Q K^T      m16n8k16: rows 0 .. 7 are the query heads' high fp16 parts, rows
 //                  8 .. 15 their low parts, so that a score is two accumulators
 //                  and no row is padding; B is eight rotated keys.
@@ -249,23 +256,34 @@ __global__ void __launch_bounds__(kSThreads)
 // a score passes m by 60 or a weight fp16's range raises m to the maximum and
 // sets f so that the largest weight is near 2^8.
 //
-// Rows travel by cp.async, several tiles ahead, and so do list entries, scales
-// and positions (a plain load returns only after the copies queued before it).
+// An entry's row of all the CTA's heads is copied by neighbouring lanes
+// (cp.async), several tiles ahead, and so are list entries, scales and positions
+// (a plain load returns only after the copies queued before it).
 // ---------------------------------------------------------------------------
 constexpr int kMWarps = 8, kMThreads = 32 * kMWarps, kMKeys = 16, kMStages = 4;
-constexpr int kMTile = kMKeys * kD;      // bytes of a K (or V) tile
-constexpr int kMRing = 2 * kMStages;     // of list entries and positions
-constexpr int kMTable = kMKeys * kD * 2; // cos and sin of a tile, fp16
+constexpr int kMTile = kMKeys * kD;       // bytes of a K (or V) tile of a head
+constexpr int kMRing = 2 * kMStages;      // of list entries and positions
+constexpr int kMTable = kMKeys * kD * 2;  // cos and sin of a tile, fp16
+constexpr int kMLeast = 4;                // tiles of a CTA, unless there are fewer
+constexpr int kMScale = 12;               // bytes that hold a row's scales of eight heads from any byte on
+template <int kSub>
 struct __align__(16) MmaSmem {
-  uint8_t kv[kMWarps][kMStages][2][kMTile];
-  uint32_t scale[kMWarps][kMStages][32];  // the words that hold 16 K and 16 V scales
-  float power[kMWarps][32];               // these scales of the current tile
-  int idx[kMWarps][kMRing][kMKeys];
-  float cs[kD / 2], sn[kD / 2];           // of the query
-  ThetaSmem ts;
-  double thd[kD / 2];
-  // then pos [kMRing][16 sub], the tables [2][sub][kMTable]
+  uint8_t kv[kMStages][2][kMWarps][kMTile];
+  uint8_t table[2][kSub][kMTable];
+  uint8_t scale[kMStages][2][kMKeys * kSub][kMScale];
+  int idx[kMRing][kMKeys * kSub], pos[kMRing][kMKeys * kSub];
+  float power[kMWarps][32];  // the current tile's 16 K and 16 V scales
+  float cs[kD / 2], sn[kD / 2];  // of the query
 };
+
+// Frequencies in turns: theta / 2 pi = hi 2^-32 + lo 2^-64, so that a position times
+// it modulo 1 is exact to 2^-32 turns for any position, in two integer products.
+struct Turns {
+  int32_t hi[kD / 2], lo[kD / 2];
+};
+__device__ __forceinline__ uint32_t turn_of(int hi, int lo, int pos) {
+  return (uint32_t)pos * (uint32_t)hi + (uint32_t)__mulhi(pos, lo);
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -297,10 +315,22 @@ __device__ __forceinline__ void mma_f16(float *c, const uint32_t *a, uint32_t b0
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_first(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
 }
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
 __device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
@@ -312,342 +342,417 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t code_at(int key, int col) {
   return (uint32_t)(key * kD + ((col ^ ((key >> 1) & 3)) << 4));
 }
-// cos/sin of positions past 2^18; rare, so out of line
-__device__ __noinline__ float2 cs_wide(double theta, int pos) {
-  float2 r;
-  rope_cs(theta, (double)pos, &r.x, &r.y);
-  return r;
-}
 
-// kTiles: eight query heads each, one or two
-template <int kTiles>
+// The ranges of a call: `ctas` equal parts of its entries, but none of less than
+// kMLeast tiles.
+struct Ranges {
+  int64_t base, total, parts;  // first entry, entries, ranges
+  __device__ __forceinline__ Ranges(const Decode8 &a, int step) {
+    base = a.indptr[0];
+    total = max(0, a.indptr[a.B] - (int)base);
+    parts = min((int64_t)a.ctas, max((int64_t)1, (total + step * kMLeast - 1) / (step * kMLeast)));
+  }
+  __device__ __forceinline__ int64_t first(int64_t i) const { return base + i * total / parts; }
+  // the range that holds entry e
+  __device__ __forceinline__ int range_of(int64_t e) const {
+    return (int)(((e - base + 1) * parts - 1) / total);
+  }
+};
+
+// kTiles: eight query heads each, one or two; kSub: groups of nh warps
+template <int kTiles, int kSub>
 __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
-    decode8_mma_kernel(const Decode8 a, const __grid_constant__ RopeTheta th, int nh, int sub) {
+    decode8_mma_kernel(const Decode8 a, const __grid_constant__ Turns turns, int nh) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  MmaSmem &sm = *reinterpret_cast<MmaSmem *>(smem_raw);
-  int *const pos_ring = reinterpret_cast<int *>(smem_raw + sizeof(MmaSmem));
-  uint8_t *const tables = smem_raw + sizeof(MmaSmem) + kMRing * kMKeys * sub * 4;
+  MmaSmem<kSub> &sm = *reinterpret_cast<MmaSmem<kSub> *>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  constexpr int kHeads = 8 * kTiles;
+  constexpr int kHeads = 8 * kTiles, kStep = kMKeys * kSub;
   const int blocks = (a.grp + kHeads - 1) / kHeads;
-  const int split = blockIdx.x, hb = blockIdx.y % blocks, b = blockIdx.z;
+  const int hb = blockIdx.y % blocks, g0 = blockIdx.y / blocks * nh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  const int part = warp / nh, g = (blockIdx.y / blocks) * nh + warp % nh;
-  const bool active = part < sub && g < a.Hkv;
+  const int part = warp / nh, hw = warp - part * nh, g = g0 + hw;
+  const bool active = part < kSub && g < a.Hkv;
   const int h0 = g * a.grp + hb * kHeads, heads = min(kHeads, a.grp - hb * kHeads);
-  int beg;
-  const int n = list_of(a, b, &beg);
-  const int c0 = split * a.chunk;
-  if (c0 >= n) return;  // the merge reads only splits that hold entries
-  const int nk = min(n - c0, a.chunk);
-  const int step = kMKeys * sub, n_tiles = (nk + step - 1) / step;
-  const int32_t *const list = a.indices + (int64_t)beg + c0, *const pos = a.kvpos + (int64_t)beg + c0;
-
-  stage_theta(th, sm.ts);
-  if (threadIdx.x < kD / 2) {
-    sm.thd[threadIdx.x] = th.th[threadIdx.x];
-    rope_cs_lane(th, threadIdx.x, a.qpos[b], &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
-  }
-  for (int x = threadIdx.x; x < 2 * step; x += kMThreads) pos_ring[x] = x < nk ? __ldg(pos + x) : 0;
-  if (a.new_slot && c0 + nk == n && active && part == 0) {
-    append_row<__nv_bfloat16>(a, b, g, false);
-    append_row<__nv_bfloat16>(a, b, g, true);
+  const Ranges ranges(a, kStep);
+  if (blockIdx.x >= ranges.parts) return;
+  int64_t e0 = ranges.first(blockIdx.x);
+  const int64_t e_end = ranges.first(blockIdx.x + 1);
+  int b = 0;  // the last request whose list begins at e0 or before
+  for (int hi = a.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (__ldg(a.indptr + mid) <= e0) b = mid; else hi = mid;
   }
 
-  // first entry of this warp's tile t is 16 (t sub + part)
-  const uint32_t kv = smem_u32(sm.kv[warp]);
-  const int own = active ? nk - kMKeys * part : 0;  // entries from its first on
-  auto fetch = [&](int t) {
-    const int x = t * step + lane;
-    if (lane < kMKeys && x < own)
-      copy4(smem_u32(&sm.idx[warp][t % kMRing][lane]), list + kMKeys * part + x, 4);
-  };
+  // This thread's 16-byte pieces of a step's rows: entry of the step, byte of the
+  // row, place in a stage.
+  const int cols = 4 * nh;
+  int piece_key[2], piece_off[2];
+  uint32_t piece_at[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = threadIdx.x + i * kMThreads, key = p / cols, col = p - key * cols;
+    const bool there = key < kStep && g0 + (col >> 2) < a.Hkv;
+    piece_key[i] = there ? key : 1 << 30;
+    piece_off[i] = g0 * kD + col * 16;
+    piece_at[i] = ((key >> 4) * nh + (col >> 2)) * kMTile + code_at(key & 15, col & 3);
+  }
+  const uint32_t row_bytes = (uint32_t)a.Hkv * kD;
   const int64_t scales = (int64_t)a.pool.S * a.Hkv;
-  auto row_of = [&](int slot) { return (int64_t)((unsigned)slot < (unsigned)a.pool.S ? slot : 0) * a.Hkv + g; };
-  auto issue = [&](int t) {
-    const int left = own - t * step;
-    if (left > 0) {
-      const int *entry = sm.idx[warp][t % kMRing];
-      const uint32_t at = kv + t % kMStages * 2 * kMTile;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = (lane >> 2) + 8 * i, col = lane & 3;
-        const bool valid = key < left;
-        const int64_t off = row_of(valid ? entry[key] : 0) * kD + col * 16;
-        copy16(at + code_at(key, col), a.pool.k + off, valid);
-        copy16(at + kMTile + code_at(key, col), a.pool.v + off, valid);
-      }
-      const int key = lane & 15;
-      const int64_t word = row_of(key < left ? entry[key] : 0) & ~(int64_t)3;
-      copy4(smem_u32(&sm.scale[warp][t % kMStages][lane]),
-            (lane < 16 ? a.pool.k_scale : a.pool.v_scale) + word,
-            (int)min(scales - word, (int64_t)4));
-      fetch(t + kMStages);
-    }
-    const int u = t + 2;  // the positions of the table to come
-    for (int x = threadIdx.x; x < step; x += kMThreads)
-      if (u * step + x < nk) copy4(smem_u32(pos_ring + u % kMRing * step + x), pos + u * step + x, 4);
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
-  };
-  // cos and sin of tile t's positions for this thread's frequencies f, f + 1
-  const int tf = 2 * (threadIdx.x % 16);
-  const uint32_t table_col = (tf >> 4) * 4 + ((tf >> 2) & 3), table_word = ((tf >> 1) & 1) * 4;
-  auto table = [&](int t, int s) {
-    const int key = threadIdx.x / 16, p = pos_ring[t % kMRing * step + s * kMKeys + key];
-    float c0f, s0f, c1f, s1f;
-    if (p < -262144 || p > 262144) {
-      const float2 u = cs_wide(sm.thd[tf], p), w = cs_wide(sm.thd[tf + 1], p);
-      c0f = u.x, s0f = u.y, c1f = w.x, s1f = w.y;
-    } else {
-      __sincosf(rope_angle(sm.ts.hi[tf], sm.ts.lo[tf], p), &s0f, &c0f);
-      __sincosf(rope_angle(sm.ts.hi[tf + 1], sm.ts.lo[tf + 1], p), &s1f, &c1f);
-    }
-    uint8_t *row = tables + ((t & 1) * sub + s) * kMTable + key * 128 +
-                   ((table_col ^ ((key & 1) << 2)) << 4) + table_word;
-    *reinterpret_cast<uint32_t *>(row) = pack_f16(c0f, c1f);
-    *reinterpret_cast<uint32_t *>(row + 8) = pack_f16(s0f, s1f);
-  };
-#pragma unroll
-  for (int t = 0; t < kMStages; ++t) fetch(t);
-  asm volatile("cp.async.wait_all;\n" ::: "memory");
-  __syncthreads();  // frequencies, positions, the appended row
-#pragma unroll
-  for (int t = 0; t < kMStages - 1; ++t) issue(t);
-  for (int s = 0; s < sub; ++s) table(0, s);
+  const bool even = (a.Hkv & 3) == 0;  // every row's scales begin at a multiple of 4
+  auto slot_in = [&](int slot) { return (unsigned)slot < (unsigned)a.pool.S ? (uint32_t)slot : 0u; };
+  // this thread's frequencies of the table, f and f + 1
+  const int tf = 2 * (threadIdx.x % 16), tkey = threadIdx.x / 16;
+  const int t_hi[2] = {turns.hi[tf], turns.hi[tf + 1]}, t_lo[2] = {turns.lo[tf], turns.lo[tf + 1]};
+  const uint32_t table_at = tkey * 128 +
+                            ((((tf >> 4) * 4 + ((tf >> 2) & 3)) ^ ((tkey & 1) << 2)) << 4) +
+                            ((tf >> 1) & 1) * 4;
 
-  // Q: rotated, 1/sqrt(D) log2(e) folded in, scaled by a power of two to 16 .. 32,
-  // split into fp16 parts.  k index 2 tig (+1) of step c is dimension 16 c + 4 tig
-  // (+1), 2 tig + 8 (+1) the two after these, as a 4-byte piece of a row of codes
-  // holds them.
-  uint32_t qa[kTiles][4][4];
-  float r[kTiles];  // the row's power of two
-#pragma unroll
-  for (int ht = 0; ht < kTiles; ++ht) {
-    const bool ok = active && 8 * ht + gid < heads;
-    const __nv_bfloat16 *src =
-        (const __nv_bfloat16 *)a.q + ((int64_t)b * a.Hq + (ok ? h0 + 8 * ht + gid : 0)) * kD;
-    float x[4][4];
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[c][e] = ok ? __bfloat162float(src[16 * c + 4 * tig + e]) * kScale : 0.f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int f = 16 * c + 4 * tig + e;
-        const float u = x[c][e], w = x[c + 2][e];
-        x[c][e] = u * sm.cs[f] - w * sm.sn[f];
-        x[c + 2][e] = u * sm.sn[f] + w * sm.cs[f];
-        top = max(top, max(__float_as_uint(x[c][e]) & 0x7fffffffu,
-                           __float_as_uint(x[c + 2][e]) & 0x7fffffffu));
-      }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // exponent of r: that of the largest component less 4, its inverse in range too
-    const int e = min(max((int)(top >> 23) - 4, 4), 250);
-    r[ht] = __uint_as_float((uint32_t)e << 23);
-    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float hi[4], lo[4];
-#pragma unroll
-      for (int e2 = 0; e2 < 4; ++e2) {
-        const float y = x[c][e2] * inv;
-        hi[e2] = __half2float(__float2half_rn(y));
-        lo[e2] = y - hi[e2];
-      }
-      qa[ht][c][0] = pack_f16(hi[0], hi[1]);
-      qa[ht][c][1] = pack_f16(lo[0], lo[1]);
-      qa[ht][c][2] = pack_f16(hi[2], hi[3]);
-      qa[ht][c][3] = pack_f16(lo[2], lo[3]);
-    }
-  }
-  float o[kTiles][4][4], m[kTiles], l[kTiles], f[kTiles];
-#pragma unroll
-  for (int ht = 0; ht < kTiles; ++ht) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[ht][c][0] = o[ht][c][1] = o[ht][c][2] = o[ht][c][3] = 0.f;
-    m[ht] = -INFINITY;
-    l[ht] = 0.f;
-    f[ht] = 1.f;
-  }
-  __syncthreads();  // table 0
+  for (; e0 < e_end; ++b) {
+    const int beg = __ldg(a.indptr + b), end = __ldg(a.indptr + b + 1);
+    const int64_t e1 = min(e_end, (int64_t)end);
+    const int c0 = (int)(e0 - beg), nk = min((int)(e1 - beg), a.max_kv) - c0;
+    if (b + 1 >= a.B) e0 = e_end; else e0 = max(e0, e1);
+    if (nk <= 0) continue;
+    const int n = min(end - beg, a.max_kv);
+    const int n_tiles = (nk + kStep - 1) / kStep;
+    const int32_t *const list = a.indices + (int64_t)beg + c0, *const pos = a.kvpos + (int64_t)beg + c0;
 
-  for (int it = 0; it < n_tiles; ++it) {
-    issue(it + kMStages - 1);
-    if (it + 1 < n_tiles)
-      for (int s = 0; s < sub; ++s) table(it + 1, s);
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(kMStages - 1) : "memory");
-    __syncwarp();
-    const int left = own - it * step;
-    if (left > 0) {
-      const uint32_t kt = kv + it % kMStages * 2 * kMTile, vt = kt + kMTile;
-      {
-        const int slot = sm.idx[warp][it % kMRing][lane & 15];
-        const uint32_t shift = ((uint32_t)row_of((lane & 15) < left ? slot : 0) & 3) * 8;
-        sm.power[warp][lane] = kv8_power((sm.scale[warp][it % kMStages][lane] >> shift) & 255u);
-      }
-      float s[kTiles][2][4];
+    if (threadIdx.x < kD / 2) {
+      const int f = threadIdx.x;
+      const float t = (float)(int)turn_of(turns.hi[f], turns.lo[f], a.qpos[b]) * 4.656612873e-10f;
+      sincospif(t, &sm.sn[f], &sm.cs[f]);
+    }
+    for (int x = threadIdx.x; x < kMStages * kStep; x += kMThreads) {
+      (&sm.idx[0][0])[x] = x < nk ? __ldg(list + x) : 0;
+      (&sm.pos[0][0])[x] = x < nk ? __ldg(pos + x) : 0;
+    }
+    if (a.new_slot && c0 + nk == n && active && part == 0) {
+      append_row<__nv_bfloat16>(a, b, g, false);
+      append_row<__nv_bfloat16>(a, b, g, true);
+    }
+
+    // rows and scales of tile t, list entries and positions of tile t + kMStages
+    auto issue = [&](int t) {
+      const int left = nk - t * kStep;
+      if (left > 0) {
+        const int *entry = sm.idx[t % kMRing];
+        const uint32_t at = smem_u32(sm.kv[t % kMStages]);
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        uint32_t kc[4], kb[4][2];
-        load_matrices(kt + code_at(8 * nb + (lane & 7), lane >> 3), kc);
-        const int key = 8 * nb + gid;
-        const uint8_t *row = tables + ((it & 1) * sub + part) * kMTable + key * 128;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 t4 =
-              *reinterpret_cast<const uint4 *>(row + (((c * 4 + tig) ^ ((key & 1) << 2)) << 4));
-          const uint32_t cs[2] = {t4.x, t4.y}, sn[2] = {t4.z, t4.w};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const __half2 x1 = half2_of(kv8_pair((uint16_t)(kc[c] >> (16 * e))));
-            const __half2 x2 = half2_of(kv8_pair((uint16_t)(kc[c + 2] >> (16 * e))));
-            const __half2 cc = half2_of(cs[e]), ss = half2_of(sn[e]);
-            kb[c][e] = bits_of(__hfma2(x1, cc, __hneg2(__hmul2(x2, ss))));
-            kb[c + 2][e] = bits_of(__hfma2(x1, ss, __hmul2(x2, cc)));
+        for (int i = 0; i < 2; ++i)
+          if (piece_key[i] < kStep) {
+            const bool valid = piece_key[i] < left;
+            const uint64_t off =
+                (uint64_t)slot_in(valid ? entry[piece_key[i]] : 0) * row_bytes + piece_off[i];
+            copy16(at + piece_at[i], a.pool.k + off, valid);
+            copy16(at + piece_at[i] + kMWarps * kMTile, a.pool.v + off, valid);
+          }
+        if (threadIdx.x < 2 * kStep) {
+          const int key = threadIdx.x % kStep, which = threadIdx.x / kStep;
+          if (key < left) {
+            const int64_t first = (int64_t)slot_in(entry[key]) * a.Hkv + g0, word = first & ~(int64_t)3;
+            const int words = ((int)(first & 3) + nh + 3) >> 2;
+            const uint8_t *src = (which ? a.pool.v_scale : a.pool.k_scale) + word;
+            const uint32_t to = smem_u32(sm.scale[t % kMStages][which][key]);
+            for (int w = 0; w < words; ++w)
+              if (word + 4 * w < scales)
+                copy4(to + 4 * w, src + 4 * w, (int)min(scales - word - 4 * w, (int64_t)4));
           }
         }
-#pragma unroll
-        for (int ht = 0; ht < kTiles; ++ht) {
-          s[ht][nb][0] = s[ht][nb][1] = s[ht][nb][2] = s[ht][nb][3] = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mma_f16(s[ht][nb], qa[ht][c], kb[c][0], kb[c][1]);
+        const int x = (t + kMStages) * kStep + threadIdx.x;
+        if (threadIdx.x < kStep && x < nk) {
+          copy4(smem_u32(&sm.idx[(t + kMStages) % kMRing][threadIdx.x]), list + x, 4);
+          copy4(smem_u32(&sm.pos[(t + kMStages) % kMRing][threadIdx.x]), pos + x, 4);
         }
       }
-      __syncwarp();  // the powers
-      float2 kp[2], vp[2];
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    // cos and sin of tile t's positions for this thread's frequencies
+    auto table = [&](int t) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-        kp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][8 * nb + 2 * tig]);
-        vp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][16 + 8 * nb + 2 * tig]);
+      for (int s = 0; s < kSub; ++s) {
+        const int p = sm.pos[t % kMRing][s * kMKeys + tkey];
+        float c[2], sn[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // the turn, half of one added, as a number in [1, 2): angles in +-pi
+          const uint32_t u = turn_of(t_hi[e], t_lo[e], p) + 0x80000000u;
+          const float x = fmaf(__uint_as_float(u >> 9 | 0x3f800000u), 6.2831853f, -9.4247780f);
+          c[e] = __cosf(x);
+          sn[e] = __sinf(x);
+        }
+        uint8_t *row = sm.table[t & 1][s] + table_at;
+        *reinterpret_cast<uint32_t *>(row) = pack_f16(c[0], c[1]);
+        *reinterpret_cast<uint32_t *>(row + 8) = pack_f16(sn[0], sn[1]);
       }
-      uint32_t pb[kTiles][2];
+    };
+    __syncthreads();  // list entries, positions, the query's angles, the appended row
 #pragma unroll
-      for (int ht = 0; ht < kTiles; ++ht) {
-        float u[4], w[4];
+    for (int t = 0; t < kMStages - 1; ++t) issue(t);
+    table(0);
+
+    // Q: rotated, 1/sqrt(D) log2(e) folded in, scaled by a power of two to 16 .. 32,
+    // split into fp16 parts.  k index 2 tig (+1) of step c is dimension 16 c + 4 tig
+    // (+1), 2 tig + 8 (+1) the two after these, as a 4-byte piece of a row of codes
+    // holds them.
+    uint32_t qa[kTiles][4][4];
+    float r[kTiles];  // the row's power of two
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          u[2 * nb] = (s[ht][nb][0] + s[ht][nb][2]) * (kp[nb].x * r[ht]);
-          u[2 * nb + 1] = (s[ht][nb][1] + s[ht][nb][3]) * (kp[nb].y * r[ht]);
-        }
-        if (left < kMKeys) {
+    for (int ht = 0; ht < kTiles; ++ht) {
+      const bool ok = active && 8 * ht + gid < heads;
+      const __nv_bfloat16 *src =
+          (const __nv_bfloat16 *)a.q + ((int64_t)b * a.Hq + (ok ? h0 + 8 * ht + gid : 0)) * kD;
+      float x[4][4];
+      uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((e >> 1) * 8 + 2 * tig + (e & 1) >= left) u[e] = -INFINITY;
-        }
-        const float v[4] = {vp[0].x, vp[0].y, vp[1].x, vp[1].y};
-        float p[4], most = 0.f, far = -INFINITY;
+      for (int c = 0; c < 4; ++c) {
+        const uint2 w = ok ? __ldg(reinterpret_cast<const uint2 *>(src + 16 * c + 4 * tig)) : make_uint2(0u, 0u);
+        x[c][0] = __uint_as_float(w.x << 16) * kScale;
+        x[c][1] = __uint_as_float(w.x & 0xffff0000u) * kScale;
+        x[c][2] = __uint_as_float(w.y << 16) * kScale;
+        x[c][3] = __uint_as_float(w.y & 0xffff0000u) * kScale;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = u[e] - m[ht];
-          p[e] = ex2(x);
-          w[e] = p[e] * (v[e] * f[ht]);
-          far = fmaxf(far, x);
-          most = fmaxf(most, w[e]);
+          const int f = 16 * c + 4 * tig + e;
+          const float u = x[c][e], w = x[c + 2][e];
+          x[c][e] = u * sm.cs[f] - w * sm.sn[f];
+          x[c + 2][e] = u * sm.sn[f] + w * sm.cs[f];
+          top = max(top, max(__float_as_uint(x[c][e]) & 0x7fffffffu,
+                             __float_as_uint(x[c + 2][e]) & 0x7fffffffu));
         }
-        if (__any_sync(0xffffffffu, it == 0 || far > 60.f || most > 32768.f)) {
-          float mx = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mx = fmaxf(mx, m[ht]);
-          const float ref = mx == -INFINITY ? 0.f : mx, alpha = ex2(m[ht] - ref);
-          m[ht] = mx;
-          most = 0.f;
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // exponent of r: that of the largest component less 4, its inverse in range too
+      const int e = min(max((int)(top >> 23) - 4, 4), 250);
+      r[ht] = __uint_as_float((uint32_t)e << 23);
+      const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(u[e] - ref);
-            most = fmaxf(most, p[e] * v[e]);
-          }
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          // 2^8 over the largest weight's power of two, at most 2^100 and, once
-          // there are sums, 2^60 times what it was
-          const int e8 = min(262 - (int)(__float_as_uint(most) >> 23), 227);
-          float f_new = __uint_as_float((uint32_t)e8 << 23);
-          if (it > 0) f_new = fminf(f_new, f[ht] * 1.1529215e18f);
-          const float ratio = it > 0 ? alpha * (f_new / f[ht]) : 0.f;
-          f[ht] = f_new;
-          l[ht] *= alpha;
-          const float ra = __shfl_sync(0xffffffffu, ratio, 8 * tig);
-          const float rb = __shfl_sync(0xffffffffu, ratio, 8 * tig + 4);
+      for (int c = 0; c < 4; ++c) {
+        float hi[4], lo[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            o[ht][c][0] *= ra;
-            o[ht][c][1] *= rb;
-            o[ht][c][2] *= ra;
-            o[ht][c][3] *= rb;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = p[e] * (v[e] * f_new);
+        for (int d = 0; d < 4; ++d) {
+          const float y = x[c][d] * inv;
+          hi[d] = __half2float(__float2half_rn(y));
+          lo[d] = y - hi[d];
         }
-        l[ht] += (p[0] + p[1]) + (p[2] + p[3]);
-        pb[ht][0] = pack_f16(w[0], w[1]);
-        pb[ht][1] = pack_f16(w[2], w[3]);
-      }
-      // V: a transposed matrix's register holds dimensions d, d + 1 of two keys
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t vc[4];
-        load_matrices_t(vt + code_at((lane >> 3 & 1) * 8 + (lane & 7), 2 * cc + (lane >> 4)), vc);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t x0 = __byte_perm(vc[2 * c], 0, 0x3120), x1 = __byte_perm(vc[2 * c + 1], 0, 0x3120);
-          const uint32_t va[4] = {kv8_pair((uint16_t)x0), kv8_pair((uint16_t)(x0 >> 16)),
-                                  kv8_pair((uint16_t)x1), kv8_pair((uint16_t)(x1 >> 16))};
-#pragma unroll
-          for (int ht = 0; ht < kTiles; ++ht) mma_f16(o[ht][2 * cc + c], va, pb[ht][0], pb[ht][1]);
-        }
+        qa[ht][c][0] = pack_f16(hi[0], hi[1]);
+        qa[ht][c][1] = pack_f16(lo[0], lo[1]);
+        qa[ht][c][2] = pack_f16(hi[2], hi[3]);
+        qa[ht][c][3] = pack_f16(lo[2], lo[3]);
       }
     }
-    __syncthreads();  // the next table; this one's and the tiles' readers are done
-  }
-  asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-  if (!active) return;
+    float o[kTiles][4][4], m[kTiles], l[kTiles], f[kTiles];
 #pragma unroll
-  for (int ht = 0; ht < kTiles; ++ht) {
-    l[ht] += __shfl_xor_sync(0xffffffffu, l[ht], 1);
-    l[ht] += __shfl_xor_sync(0xffffffffu, l[ht], 2);
-    const float inv = 1.f / f[ht];
-    const int64_t base = ((int64_t)b * a.Hq + h0 + 8 * ht) * a.ns + split * sub + part;
-    if (tig == 0 && 8 * ht + gid < heads) a.ml[base + (int64_t)gid * a.ns] = make_float2(m[ht], l[ht]);
+    for (int ht = 0; ht < kTiles; ++ht) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float y = __shfl_sync(0xffffffffu, inv, 8 * tig + 4 * e);
-      if (8 * ht + 2 * tig + e >= heads) continue;
-      float *to = a.o + (base + (int64_t)(2 * tig + e) * a.ns) * kD + 2 * gid;
+      for (int c = 0; c < 4; ++c) o[ht][c][0] = o[ht][c][1] = o[ht][c][2] = o[ht][c][3] = 0.f;
+      m[ht] = -INFINITY;
+      l[ht] = 0.f;
+      f[ht] = 1.f;
+    }
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kMStages - 2) : "memory");
+    __syncthreads();  // tile 0 and its table
+
+    for (int it = 0; it < n_tiles; ++it) {
+      issue(it + kMStages - 1);
+      if (it + 1 < n_tiles) table(it + 1);
+      const int left = nk - it * kStep - kMKeys * part;
+      if (active && left > 0) {
+        const uint32_t kt = smem_u32(sm.kv[it % kMStages][0][warp]), vt = kt + kMWarps * kMTile;
+        {
+          const int key = part * kMKeys + (lane & 15);
+          const bool listed = (lane & 15) < left;
+          uint32_t off = hw;
+          if (!even) off += (slot_in(listed ? sm.idx[it % kMRing][key] : 0) * a.Hkv + g0) & 3;
+          sm.power[warp][lane] =
+              listed ? kv8_power(sm.scale[it % kMStages][lane >> 4][key][off]) : 0.f;
+        }
+        float s[kTiles][2][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<float2 *>(to + 16 * c) = make_float2(o[ht][c][e] * y, o[ht][c][2 + e] * y);
+        for (int nb = 0; nb < 2; ++nb) {
+          uint32_t kc[4], kb[4][2];
+          load_matrices(kt + code_at(8 * nb + (lane & 7), lane >> 3), kc);
+          const int key = 8 * nb + gid;
+          const uint8_t *row = sm.table[it & 1][kSub == 1 ? 0 : part] + key * 128;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4 t4 =
+                *reinterpret_cast<const uint4 *>(row + (((c * 4 + tig) ^ ((key & 1) << 2)) << 4));
+            const uint32_t cs[2] = {t4.x, t4.y}, sn[2] = {t4.z, t4.w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const __half2 x1 = half2_of(kv8_pair((uint16_t)(kc[c] >> (16 * e))));
+              const __half2 x2 = half2_of(kv8_pair((uint16_t)(kc[c + 2] >> (16 * e))));
+              const __half2 cc = half2_of(cs[e]), ss = half2_of(sn[e]);
+              kb[c][e] = bits_of(__hfma2(x1, cc, __hneg2(__hmul2(x2, ss))));
+              kb[c + 2][e] = bits_of(__hfma2(x1, ss, __hmul2(x2, cc)));
+            }
+          }
+#pragma unroll
+          for (int ht = 0; ht < kTiles; ++ht) {
+            mma_f16_first(s[ht][nb], qa[ht][0], kb[0][0], kb[0][1]);
+#pragma unroll
+            for (int c = 1; c < 4; ++c) mma_f16(s[ht][nb], qa[ht][c], kb[c][0], kb[c][1]);
+          }
+        }
+        __syncwarp();  // the powers
+        float2 kp[2], vp[2];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          kp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][8 * nb + 2 * tig]);
+          vp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][16 + 8 * nb + 2 * tig]);
+        }
+        uint32_t pb[kTiles][2];
+#pragma unroll
+        for (int ht = 0; ht < kTiles; ++ht) {
+          float2 u[2], p[2], w[2];
+          const float2 r2 = make_float2(r[ht], r[ht]), m2 = make_float2(-m[ht], -m[ht]);
+          const float2 f2 = make_float2(f[ht], f[ht]);
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            const float *x = s[ht][nb];
+            u[nb] = __fmul2_rn(__fadd2_rn(make_float2(x[0], x[1]), make_float2(x[2], x[3])),
+                               __fmul2_rn(kp[nb], r2));
+          }
+          if (left < kMKeys) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              if (8 * nb + 2 * tig >= left) u[nb].x = -INFINITY;
+              if (8 * nb + 2 * tig + 1 >= left) u[nb].y = -INFINITY;
+            }
+          }
+          float2 x[2];
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            x[nb] = __fadd2_rn(u[nb], m2);
+            p[nb] = make_float2(ex2(x[nb].x), ex2(x[nb].y));
+            w[nb] = __fmul2_rn(p[nb], __fmul2_rn(vp[nb], f2));
+          }
+          const float far = fmaxf(max3(x[0].x, x[0].y, x[1].x), x[1].y);
+          const float most = fmaxf(max3(w[0].x, w[0].y, w[1].x), w[1].y);
+          if (__any_sync(0xffffffffu, it == 0 || far > 60.f || most > 32768.f)) {
+            float mx = fmaxf(max3(u[0].x, u[0].y, u[1].x), u[1].y);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx = fmaxf(mx, m[ht]);
+            const float ref = mx == -INFINITY ? 0.f : mx, alpha = ex2(m[ht] - ref);
+            m[ht] = mx;
+            float big = 0.f;
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              p[nb] = make_float2(ex2(u[nb].x - ref), ex2(u[nb].y - ref));
+              big = max3(big, p[nb].x * vp[nb].x, p[nb].y * vp[nb].y);
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^8 over the largest weight's power of two, at most 2^100 and, once
+            // there are sums, 2^60 times what it was
+            const int e8 = min(262 - (int)(__float_as_uint(big) >> 23), 227);
+            float f_new = __uint_as_float((uint32_t)e8 << 23);
+            if (it > 0) f_new = fminf(f_new, f[ht] * 1.1529215e18f);
+            const float ratio = it > 0 ? alpha * (f_new / f[ht]) : 0.f;
+            f[ht] = f_new;
+            l[ht] *= alpha;
+            const float ra = __shfl_sync(0xffffffffu, ratio, 8 * tig);
+            const float rb = __shfl_sync(0xffffffffu, ratio, 8 * tig + 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              o[ht][c][0] *= ra;
+              o[ht][c][1] *= rb;
+              o[ht][c][2] *= ra;
+              o[ht][c][3] *= rb;
+            }
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+              w[nb] = make_float2(p[nb].x * (vp[nb].x * f_new), p[nb].y * (vp[nb].y * f_new));
+          }
+          const float2 sum = __fadd2_rn(p[0], p[1]);
+          l[ht] += sum.x + sum.y;
+          pb[ht][0] = pack_f16(w[0].x, w[0].y);
+          pb[ht][1] = pack_f16(w[1].x, w[1].y);
+        }
+        // V: a transposed matrix's register holds dimensions d, d + 1 of two keys
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t vc[4];
+          load_matrices_t(vt + code_at((lane >> 3 & 1) * 8 + (lane & 7), 2 * cc + (lane >> 4)), vc);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t x0 = __byte_perm(vc[2 * c], 0, 0x3120), x1 = __byte_perm(vc[2 * c + 1], 0, 0x3120);
+            const uint32_t va[4] = {kv8_pair((uint16_t)x0), kv8_pair((uint16_t)(x0 >> 16)),
+                                    kv8_pair((uint16_t)x1), kv8_pair((uint16_t)(x1 >> 16))};
+#pragma unroll
+            for (int ht = 0; ht < kTiles; ++ht) mma_f16(o[ht][2 * cc + c], va, pb[ht][0], pb[ht][1]);
+          }
+        }
+      }
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kMStages - 2) : "memory");
+      __syncthreads();  // the next tile and its table; this one's readers are done
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    if (active) {
+#pragma unroll
+      for (int ht = 0; ht < kTiles; ++ht) {
+        l[ht] += __shfl_xor_sync(0xffffffffu, l[ht], 1);
+        l[ht] += __shfl_xor_sync(0xffffffffu, l[ht], 2);
+        const float inv = 1.f / f[ht];
+        // range + request never repeats: along the entries one of the two grows
+        const int64_t base = ((int64_t)(blockIdx.x + b) * kSub + part) * a.Hq + h0 + 8 * ht;
+        if (tig == 0 && 8 * ht + gid < heads) a.ml[base + gid] = make_float2(m[ht], l[ht]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y = __shfl_sync(0xffffffffu, inv, 8 * tig + 4 * e);
+          if (8 * ht + 2 * tig + e >= heads) continue;
+          float *to = a.o + (base + 2 * tig + e) * kD + 2 * gid;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float2 *>(to + 16 * c) = make_float2(o[ht][c][e] * y, o[ht][c][2 + e] * y);
+        }
+      }
     }
   }
 }
 
-// Joins the splits by their log-sum-exp: CTA = (query head, request), eight
-// groups of 16 threads each summing every eighth split's row.  Launched as a
+// Joins a row's partials by their log-sum-exp: CTA = (query head, request), eight
+// groups of 16 threads each summing every eighth partial's row.  Launched as a
 // programmatic dependent of the attention kernel.  A request without entries
 // gets zeros.
-constexpr int kMergeThreads = 128, kMaxSplit = 1024;
+constexpr int kMergeThreads = 128, kMaxParts = 2560;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Decode8 a, T *out) {
-  __shared__ float wgt[kMaxSplit];
+  __shared__ float wgt[kMaxParts];
   __shared__ float4 red[8][kD / 4];
   __shared__ float tot[4], top[4];
   const int h = blockIdx.x, b = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int beg;
   const int n = list_of(a, b, &beg);
-  const int used = (n + a.chunk - 1) / a.chunk * a.per;
+  // partials of this row: the first, how many, how far apart
+  int64_t at, apart;
+  int used = 0;
+  if constexpr (sizeof(T) == 4) {
+    used = (n + a.chunk - 1) / a.chunk;
+    at = ((int64_t)b * a.Hq + h) * a.ctas;
+    apart = 1;
+  } else {
+    const Ranges ranges(a, kMKeys * a.sub);
+    int first = 0;
+    if (n > 0) {
+      first = ranges.range_of(beg);
+      used = (ranges.range_of((int64_t)beg + n - 1) - first + 1) * a.sub;
+    }
+    at = (int64_t)(first + b) * a.sub * a.Hq + h;
+    apart = a.Hq;
+  }
   const int64_t w = (int64_t)b * a.Hq + h;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const float2 *ml = a.ml + w * a.ns;
+  const float2 *ml = a.ml + at;
   float M = -INFINITY;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float m = __ldcg(&ml[s].x);
+    const float m = __ldcg(&ml[s * apart].x);
     wgt[s] = m;
     M = fmaxf(M, m);
   }
@@ -661,7 +766,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Deco
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
     const float f = exp2f(wgt[s] - ref);
     wgt[s] = f;
-    L = fmaf(__ldcg(&ml[s].y), f, L);
+    L = fmaf(__ldcg(&ml[s * apart].y), f, L);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -672,7 +777,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Deco
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = sg; s < used; s += 8) {
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o + (w * a.ns + s) * kD) + cg);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o + (at + s * apart) * kD) + cg);
     const float f = wgt[s];
     acc.x = fmaf(v.x, f, acc.x);
     acc.y = fmaf(v.y, f, acc.y);
@@ -700,39 +805,38 @@ int sm_count() {
   return sms;
 }
 
-// Key splits from the host's bounds alone, so that a captured call replays for
-// any lengths within them.
+// The cut of the work, from the host's bounds alone, so that a captured call
+// replays for any lengths within them.
 struct Decode8Plan {
-  int splits, chunk, per;  // CTAs along a list, entries of each, partials of each
-  int nh, blocks;          // KV heads per CTA (mma.sync), query head blocks of a KV head
+  int ctas, chunk, sub;
+  int nh, blocks;  // KV heads per CTA (bf16), query head blocks of a KV head
+  size_t parts;    // partials of a query head, over the batch
 };
 Decode8Plan plan_of(int dtype, int B, int Hq, int Hkv, int max_kv) {
   Decode8Plan p;
-  const int grp = Hq / Hkv;
-  int64_t ctas, want;
-  int c, least;
+  const int grp = Hq / Hkv, sms = sm_count();
   if (dtype == AKV_BF16) {
     const int tiles = grp <= 8 ? 1 : 2;
     p.blocks = (grp + 8 * tiles - 1) / (8 * tiles);
     p.nh = std::min(Hkv, kMWarps);
-    p.per = kMWarps / p.nh;
-    ctas = (int64_t)B * ((Hkv + p.nh - 1) / p.nh) * p.blocks;
-    want = 4LL * 2 * sm_count();
-    c = 2048 * p.per;
-    least = kMKeys * p.per * 8;
+    p.sub = kMWarps / p.nh >= 8 ? 8 : kMWarps / p.nh >= 4 ? 4 : kMWarps / p.nh >= 2 ? 2 : 1;
+    p.chunk = 0;
+    // as many as the SMs hold at a time; no more than the merge's table has room for
+    const int ny = (Hkv + p.nh - 1) / p.nh * p.blocks, per_sm = tiles == 1 ? 2 : 1;
+    p.ctas = std::min(std::max(1, per_sm * sms / ny), kMaxParts / p.sub);
+    p.parts = ((size_t)p.ctas + B) * p.sub;
   } else {
     p.blocks = (grp + kSHeads - 1) / kSHeads;
-    p.nh = p.per = 1;
-    ctas = (int64_t)B * Hkv * p.blocks;
-    want = 4LL * 4 * sm_count();
-    c = 4096;
-    least = kSKeys;
+    p.nh = p.sub = 1;
+    const auto splits = [&](int x) { return std::max<int64_t>(1, ((int64_t)max_kv + x - 1) / x); };
+    const int64_t rows = (int64_t)B * Hkv * p.blocks;
+    int c = 4096;
+    while (c > kSKeys && rows * splits(c) < 4LL * 4 * sms) c /= 2;
+    while (splits(c) > kMaxParts) c *= 2;
+    p.ctas = (int)splits(c);
+    p.chunk = c;
+    p.parts = (size_t)p.ctas * B;
   }
-  const auto splits = [&](int x) { return std::max<int64_t>(1, ((int64_t)max_kv + x - 1) / x); };
-  while (c / 2 >= least && ctas * splits(c) < want) c /= 2;
-  while (splits(c) * p.per > kMaxSplit) c *= 2;
-  p.splits = (int)splits(c);
-  p.chunk = c;
   return p;
 }
 
@@ -757,26 +861,38 @@ cudaError_t launch_simt(const Decode8 &a, const Decode8Plan &p, const RopeTheta 
   const cudaError_t e = cudaFuncSetAttribute(decode8_simt_kernel<float>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode8_simt_kernel<float><<<dim3(p.splits, a.Hkv * p.blocks, a.B), kSThreads, smem, s>>>(a, th);
+  decode8_simt_kernel<float><<<dim3(p.ctas, a.Hkv * p.blocks, a.B), kSThreads, smem, s>>>(a, th);
   return cudaGetLastError();
 }
 
-template <int kTiles>
-cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const RopeTheta &th, cudaStream_t s) {
-  const int smem = (int)sizeof(MmaSmem) + p.per * (kMRing * kMKeys * 4 + 2 * kMTable);
-  const cudaError_t e = cudaFuncSetAttribute(decode8_mma_kernel<kTiles>,
+template <int kTiles, int kSub>
+cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const Turns &turns, cudaStream_t s) {
+  const int smem = (int)sizeof(MmaSmem<kSub>);
+  const cudaError_t e = cudaFuncSetAttribute(decode8_mma_kernel<kTiles, kSub>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode8_mma_kernel<kTiles><<<dim3(p.splits, (a.Hkv + p.nh - 1) / p.nh * p.blocks, a.B), kMThreads, smem,
-                               s>>>(a, th, p.nh, p.per);
+  decode8_mma_kernel<kTiles, kSub>
+      <<<dim3(p.ctas, (a.Hkv + p.nh - 1) / p.nh * p.blocks), kMThreads, smem, s>>>(a, turns, p.nh);
   return cudaGetLastError();
+}
+template <int kTiles>
+cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const RopeTheta &th, cudaStream_t s) {
+  Turns turns;
+  for (int f = 0; f < kD / 2; ++f) {
+    const double t = th.th[f] / 6.283185307179586476925286766559 * 4294967296.0, hi = std::rint(t);
+    turns.hi[f] = (int32_t)(uint32_t)(int64_t)hi;
+    turns.lo[f] = (int32_t)std::min(std::rint((t - hi) * 4294967296.0), 2147483647.0);
+  }
+  return p.sub == 8   ? launch_mma<kTiles, 8>(a, p, turns, s)
+         : p.sub == 4 ? launch_mma<kTiles, 4>(a, p, turns, s)
+         : p.sub == 2 ? launch_mma<kTiles, 2>(a, p, turns, s)
+                      : launch_mma<kTiles, 1>(a, p, turns, s);
 }
 
 }  // namespace
 
 size_t decode_q8_workspace_bytes(int dtype, int B, int Hq, int Hkv, int max_kv) {
-  const Decode8Plan p = plan_of(dtype, B, Hq, Hkv, max_kv);
-  const size_t parts = (size_t)B * Hq * p.splits * p.per;
+  const size_t parts = plan_of(dtype, B, Hq, Hkv, max_kv).parts * Hq;
   return up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
 }
 
@@ -786,10 +902,9 @@ cudaError_t launch_decode_q8(int dtype, int B, int Hq, int Hkv, const void *q, c
                              const int32_t *kvpos, int max_kv, void *out, void *ws,
                              const RopeTheta &th, cudaStream_t s) {
   const Decode8Plan p = plan_of(dtype, B, Hq, Hkv, max_kv);
-  const int ns = p.splits * p.per;
   const Decode8 a{B, Hq, Hkv, Hq / Hkv, q, qpos, k_new, v_new, new_slot, pool, indptr, indices, kvpos,
-                  max_kv, (float2 *)ws,
-                  (float *)((char *)ws + up256((size_t)B * Hq * ns * sizeof(float2))), ns, p.chunk, p.per};
+                  max_kv, (float2 *)ws, (float *)((char *)ws + up256(p.parts * Hq * sizeof(float2))),
+                  p.ctas, p.chunk, p.sub};
   const cudaError_t e = dtype != AKV_BF16 ? launch_simt(a, p, th, s)
                         : a.grp <= 8      ? launch_mma<1>(a, p, th, s)
                                           : launch_mma<2>(a, p, th, s);
