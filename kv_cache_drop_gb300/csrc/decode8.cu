@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace akv {
 namespace {
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kSThreads)
 // into equal ranges, one for each CTA that the GPU holds at a time, so that lists
 // of any lengths leave no SM idle; a range may end inside a list and hold several
 // lists, and leaves a partial for each list that it touches.  A CTA takes up to
-// eight KV heads, a warp each, 16 entries at a time; with fewer heads kSub groups of
-// warps take 16 entries each.
+// eight KV heads, a warp each, 32 entries at a time; with fewer heads kSub groups of
+// warps take 32 entries each.
 //   S = Q K^T      m16n8k16: rows 0 .. 7 are the query heads' high fp16 parts, rows
 //                  8 .. 15 their low parts, so that a score is two accumulators
 //                  and no row is padding; B is eight rotated keys.
@@ -260,19 +261,22 @@ __global__ void __launch_bounds__(kSThreads)
 // (cp.async), several tiles ahead, and so are list entries, scales and positions
 // (a plain load returns only after the copies queued before it).
 // ---------------------------------------------------------------------------
-constexpr int kMWarps = 8, kMThreads = 32 * kMWarps, kMKeys = 16, kMStages = 4;
+constexpr int kMWarps = 8, kMThreads = 32 * kMWarps, kMKeys = 32;
+// tiles of a warp, and of list entries and positions: what leaves room for two
+// CTAs per SM (one with eight groups)
+constexpr int stages_of(int sub) { return sub == 1 ? 3 : 2; }
+constexpr int ring_of(int sub) { return sub == 1 ? 8 : 4; }
 constexpr int kMTile = kMKeys * kD;       // bytes of a K (or V) tile of a head
-constexpr int kMRing = 2 * kMStages;      // of list entries and positions
 constexpr int kMTable = kMKeys * kD * 2;  // cos and sin of a tile, fp16
-constexpr int kMLeast = 4;                // tiles of a CTA, unless there are fewer
-constexpr int kMScale = 12;               // bytes that hold a row's scales of eight heads from any byte on
+constexpr int kMLeast = 2;                // tiles of a CTA, unless there are fewer
+constexpr int kMScale = 16;               // bytes that hold a row's scales of eight heads from any byte on
 template <int kSub>
 struct __align__(16) MmaSmem {
-  uint8_t kv[kMStages][2][kMWarps][kMTile];
+  uint8_t kv[stages_of(kSub)][2][kMWarps][kMTile];
   uint8_t table[2][kSub][kMTable];
-  uint8_t scale[kMStages][2][kMKeys * kSub][kMScale];
-  int idx[kMRing][kMKeys * kSub], pos[kMRing][kMKeys * kSub];
-  float power[kMWarps][32];  // the current tile's 16 K and 16 V scales
+  uint8_t scale[stages_of(kSub)][2][kMKeys * kSub][kMScale];
+  int idx[ring_of(kSub)][kMKeys * kSub], pos[ring_of(kSub)][kMKeys * kSub];
+  float power[kMWarps][2][kMKeys];  // the current tile's scales of K and of V
   float cs[kD / 2], sn[kD / 2];  // of the query
 };
 
@@ -295,6 +299,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t *r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -337,7 +344,7 @@ __device__ __forceinline__ uint32_t bits_of(__half2 x) { return *reinterpret_cas
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return bits_of(__floats2half2_rn(lo, hi));
 }
-// byte offset of (key, 16-byte column) in a [16][64] tile of codes: eight keys at
+// byte offset of (key, 16-byte column) in a [32][64] tile of codes: eight keys at
 // one column fall in different banks
 __device__ __forceinline__ uint32_t code_at(int key, int col) {
   return (uint32_t)(key * kD + ((col ^ ((key >> 1) & 3)) << 4));
@@ -361,12 +368,13 @@ struct Ranges {
 
 // kTiles: eight query heads each, one or two; kSub: groups of nh warps
 template <int kTiles, int kSub>
-__global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
     decode8_mma_kernel(const Decode8 a, const __grid_constant__ Turns turns, int nh) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   MmaSmem<kSub> &sm = *reinterpret_cast<MmaSmem<kSub> *>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   constexpr int kHeads = 8 * kTiles, kStep = kMKeys * kSub;
+  constexpr int kMStages = stages_of(kSub), kMRing = ring_of(kSub);
   const int blocks = (a.grp + kHeads - 1) / kHeads;
   const int hb = blockIdx.y % blocks, g0 = blockIdx.y / blocks * nh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -384,22 +392,17 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
     if (__ldg(a.indptr + mid) <= e0) b = mid; else hi = mid;
   }
 
-  // This thread's 16-byte pieces of a step's rows: entry of the step, byte of the
-  // row, place in a stage.
-  const int cols = 4 * nh;
-  int piece_key[2], piece_off[2];
-  uint32_t piece_at[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = threadIdx.x + i * kMThreads, key = p / cols, col = p - key * cols;
-    const bool there = key < kStep && g0 + (col >> 2) < a.Hkv;
-    piece_key[i] = there ? key : 1 << 30;
-    piece_off[i] = g0 * kD + col * 16;
-    piece_at[i] = ((key >> 4) * nh + (col >> 2)) * kMTile + code_at(key & 15, col & 3);
-  }
+  // This thread copies a 16-byte column of four rows of a step, a quarter of the
+  // step apart, of K and of V.
+  constexpr int kQuarter = kStep / 4;
+  const int col = threadIdx.x % (4 * nh), row0 = threadIdx.x / (4 * nh);
+  const bool copies = row0 < kQuarter && g0 + (col >> 2) < a.Hkv;
+  const uint8_t *const k_col = a.pool.k + g0 * kD + col * 16, *const v_col = a.pool.v + g0 * kD + col * 16;
+  const uint32_t col_at = smem_u32(sm.kv) + ((row0 / kMKeys) * nh + (col >> 2)) * kMTile +
+                          code_at(row0 % kMKeys, col & 3);
   const uint32_t row_bytes = (uint32_t)a.Hkv * kD;
   const int64_t scales = (int64_t)a.pool.S * a.Hkv;
-  const bool even = (a.Hkv & 3) == 0;  // every row's scales begin at a multiple of 4
+  const int odd = a.Hkv & 3;  // not 0: a row's scales may begin at any byte
   auto slot_in = [&](int slot) { return (unsigned)slot < (unsigned)a.pool.S ? (uint32_t)slot : 0u; };
   // this thread's frequencies of the table, f and f + 1
   const int tf = 2 * (threadIdx.x % 16), tkey = threadIdx.x / 16;
@@ -407,6 +410,13 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
   const uint32_t table_at = tkey * 128 +
                             ((((tf >> 4) * 4 + ((tf >> 2) & 3)) ^ ((tkey & 1) << 2)) << 4) +
                             ((tf >> 1) & 1) * 4;
+
+  // this lane's part of the tiles: matrix rows of K and (columns 0, 16 of 64; ^ 32:
+  // 32, 48) of V, cos and sin of dimensions 4 tig .. (^ 64: 16 + 4 tig ..)
+  const uint32_t tile_at = smem_u32(sm.kv[0][0][warp]);
+  const uint32_t k_at = code_at(lane & 7, lane >> 3);
+  const uint32_t v_at = code_at((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4);
+  const uint32_t cs_at = gid * 128 + ((tig ^ ((gid & 1) << 2)) << 4);
 
   for (; e0 < e_end; ++b) {
     const int beg = __ldg(a.indptr + b), end = __ldg(a.indptr + b + 1);
@@ -437,32 +447,46 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
       const int left = nk - t * kStep;
       if (left > 0) {
         const int *entry = sm.idx[t % kMRing];
-        const uint32_t at = smem_u32(sm.kv[t % kMStages]);
+        const uint32_t stage = t % kMStages;
+        if (copies) {
+          const uint32_t to = col_at + stage * (2 * kMWarps * kMTile);
+          auto rows = [&](auto whole) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (piece_key[i] < kStep) {
-            const bool valid = piece_key[i] < left;
-            const uint64_t off =
-                (uint64_t)slot_in(valid ? entry[piece_key[i]] : 0) * row_bytes + piece_off[i];
-            copy16(at + piece_at[i], a.pool.k + off, valid);
-            copy16(at + piece_at[i] + kMWarps * kMTile, a.pool.v + off, valid);
-          }
-        if (threadIdx.x < 2 * kStep) {
-          const int key = threadIdx.x % kStep, which = threadIdx.x / kStep;
-          if (key < left) {
-            const int64_t first = (int64_t)slot_in(entry[key]) * a.Hkv + g0, word = first & ~(int64_t)3;
-            const int words = ((int)(first & 3) + nh + 3) >> 2;
-            const uint8_t *src = (which ? a.pool.v_scale : a.pool.k_scale) + word;
-            const uint32_t to = smem_u32(sm.scale[t % kMStages][which][key]);
-            for (int w = 0; w < words; ++w)
-              if (word + 4 * w < scales)
-                copy4(to + 4 * w, src + 4 * w, (int)min(scales - word - 4 * w, (int64_t)4));
-          }
+            for (int i = 0; i < 4; ++i) {
+              const int key = row0 + i * kQuarter;
+              const bool listed = decltype(whole)::value || key < left;
+              const uint64_t off = (uint64_t)(listed ? slot_in(entry[key]) : 0u) * row_bytes;
+              const uint32_t at =
+                  to + (i * kQuarter % kMKeys) * kD + (i * kQuarter / kMKeys) * nh * kMTile;
+              copy16(at, k_col + off, listed);
+              copy16(at + kMWarps * kMTile, v_col + off, listed);
+            }
+          };
+          if (left >= kStep) rows(std::true_type());
+          else rows(std::false_type());
         }
-        const int x = (t + kMStages) * kStep + threadIdx.x;
-        if (threadIdx.x < kStep && x < nk) {
-          copy4(smem_u32(&sm.idx[(t + kMStages) % kMRing][threadIdx.x]), list + x, 4);
-          copy4(smem_u32(&sm.pos[(t + kMStages) % kMRing][threadIdx.x]), pos + x, 4);
+        // a warp's 32 threads have one of the four arrays
+#pragma unroll
+        for (int z = 0; z < 4 * kStep; z += kMThreads) {
+          const int what = (z + threadIdx.x) / kStep, key = (z + threadIdx.x) % kStep;
+          if (what < 2 && key < left) {
+            const int64_t first = (int64_t)slot_in(entry[key]) * a.Hkv + g0;
+            const uint8_t *const src = what ? a.pool.v_scale : a.pool.k_scale;
+            const uint32_t to = smem_u32(sm.scale[stage][what][key]);
+            if ((a.Hkv & 7) == 0) copy8(to, src + first);
+            else if (!odd) copy4(to, src + first, 4);
+            else {
+              const int64_t word = first & ~(int64_t)3;
+              for (int w = 0; w < (((int)(first & 3) + nh + 3) >> 2); ++w)
+                if (word + 4 * w < scales)
+                  copy4(to + 4 * w, src + word + 4 * w, (int)min(scales - word - 4 * w, (int64_t)4));
+            }
+          } else if (what >= 2 && what < 4) {
+            const int x = (t + kMStages) * kStep + key;
+            if (x < nk)
+              copy4(smem_u32(&(what == 2 ? sm.idx : sm.pos)[(t + kMStages) % kMRing][key]),
+                    (what == 2 ? list : pos) + x, 4);
+          }
         }
       }
       asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -470,8 +494,8 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
     // cos and sin of tile t's positions for this thread's frequencies
     auto table = [&](int t) {
 #pragma unroll
-      for (int s = 0; s < kSub; ++s) {
-        const int p = sm.pos[t % kMRing][s * kMKeys + tkey];
+      for (int s = 0; s < 2 * kSub; ++s) {
+        const int p = sm.pos[t % kMRing][s * 16 + tkey];
         float c[2], sn[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -481,7 +505,7 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
           c[e] = __cosf(x);
           sn[e] = __sinf(x);
         }
-        uint8_t *row = sm.table[t & 1][s] + table_at;
+        uint8_t *row = sm.table[t & 1][s >> 1] + (s & 1) * (kMTable / 2) + table_at;
         *reinterpret_cast<uint32_t *>(row) = pack_f16(c[0], c[1]);
         *reinterpret_cast<uint32_t *>(row + 8) = pack_f16(sn[0], sn[1]);
       }
@@ -558,29 +582,28 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
 
     for (int it = 0; it < n_tiles; ++it) {
       issue(it + kMStages - 1);
-      if (it + 1 < n_tiles) table(it + 1);
+      table(it + 1);  // past the end: of whatever the ring holds
       const int left = nk - it * kStep - kMKeys * part;
       if (active && left > 0) {
-        const uint32_t kt = smem_u32(sm.kv[it % kMStages][0][warp]), vt = kt + kMWarps * kMTile;
+        const uint32_t kt = tile_at + it % kMStages * (2 * kMWarps * kMTile), vt = kt + kMWarps * kMTile;
         {
-          const int key = part * kMKeys + (lane & 15);
-          const bool listed = (lane & 15) < left;
+          const int key = part * kMKeys + lane;
+          const bool listed = lane < left;
           uint32_t off = hw;
-          if (!even) off += (slot_in(listed ? sm.idx[it % kMRing][key] : 0) * a.Hkv + g0) & 3;
-          sm.power[warp][lane] =
-              listed ? kv8_power(sm.scale[it % kMStages][lane >> 4][key][off]) : 0.f;
+          if (odd) off += (slot_in(listed ? sm.idx[it % kMRing][key] : 0) * a.Hkv + g0) & 3;
+          const uint8_t(*scale)[kStep][kMScale] = sm.scale[it % kMStages];
+          sm.power[warp][0][lane] = listed ? kv8_power(scale[0][key][off]) : 0.f;
+          sm.power[warp][1][lane] = listed ? kv8_power(scale[1][key][off]) : 0.f;
         }
-        float s[kTiles][2][4];
+        float s[kTiles][4][4];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+        for (int nb = 0; nb < 4; ++nb) {
           uint32_t kc[4], kb[4][2];
-          load_matrices(kt + code_at(8 * nb + (lane & 7), lane >> 3), kc);
-          const int key = 8 * nb + gid;
-          const uint8_t *row = sm.table[it & 1][kSub == 1 ? 0 : part] + key * 128;
+          load_matrices(kt + k_at + 8 * nb * kD, kc);
+          const uint8_t *row = sm.table[it & 1][kSub == 1 ? 0 : part] + 8 * nb * 128;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const uint4 t4 =
-                *reinterpret_cast<const uint4 *>(row + (((c * 4 + tig) ^ ((key & 1) << 2)) << 4));
+            const uint4 t4 = *reinterpret_cast<const uint4 *>(row + (c ? cs_at ^ 64 : cs_at));
             const uint32_t cs[2] = {t4.x, t4.y}, sn[2] = {t4.z, t4.w};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -599,52 +622,52 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
           }
         }
         __syncwarp();  // the powers
-        float2 kp[2], vp[2];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          kp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][8 * nb + 2 * tig]);
-          vp[nb] = *reinterpret_cast<const float2 *>(&sm.power[warp][16 + 8 * nb + 2 * tig]);
-        }
-        uint32_t pb[kTiles][2];
+        uint32_t pb[kTiles][4];
 #pragma unroll
         for (int ht = 0; ht < kTiles; ++ht) {
-          float2 u[2], p[2], w[2];
+          float2 u[4], p[4], w[4];
           const float2 r2 = make_float2(r[ht], r[ht]), m2 = make_float2(-m[ht], -m[ht]);
           const float2 f2 = make_float2(f[ht], f[ht]);
+          auto vp = [&](int nb) {
+            return *reinterpret_cast<const float2 *>(&sm.power[warp][1][8 * nb + 2 * tig]);
+          };
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
+          for (int nb = 0; nb < 4; ++nb) {
             const float *x = s[ht][nb];
+            const float2 kp = *reinterpret_cast<const float2 *>(&sm.power[warp][0][8 * nb + 2 * tig]);
             u[nb] = __fmul2_rn(__fadd2_rn(make_float2(x[0], x[1]), make_float2(x[2], x[3])),
-                               __fmul2_rn(kp[nb], r2));
+                               __fmul2_rn(kp, r2));
           }
           if (left < kMKeys) {
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
+            for (int nb = 0; nb < 4; ++nb) {
               if (8 * nb + 2 * tig >= left) u[nb].x = -INFINITY;
               if (8 * nb + 2 * tig + 1 >= left) u[nb].y = -INFINITY;
             }
           }
-          float2 x[2];
+          float far = -INFINITY, most = 0.f;
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            x[nb] = __fadd2_rn(u[nb], m2);
-            p[nb] = make_float2(ex2(x[nb].x), ex2(x[nb].y));
-            w[nb] = __fmul2_rn(p[nb], __fmul2_rn(vp[nb], f2));
+          for (int nb = 0; nb < 4; ++nb) {
+            const float2 x = __fadd2_rn(u[nb], m2);
+            p[nb] = make_float2(ex2(x.x), ex2(x.y));
+            w[nb] = __fmul2_rn(p[nb], __fmul2_rn(vp(nb), f2));
+            far = max3(far, x.x, x.y);
+            most = max3(most, w[nb].x, w[nb].y);
           }
-          const float far = fmaxf(max3(x[0].x, x[0].y, x[1].x), x[1].y);
-          const float most = fmaxf(max3(w[0].x, w[0].y, w[1].x), w[1].y);
           if (__any_sync(0xffffffffu, it == 0 || far > 60.f || most > 32768.f)) {
-            float mx = fmaxf(max3(u[0].x, u[0].y, u[1].x), u[1].y);
+            float mx = m[ht];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) mx = max3(mx, u[nb].x, u[nb].y);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mx = fmaxf(mx, m[ht]);
             const float ref = mx == -INFINITY ? 0.f : mx, alpha = ex2(m[ht] - ref);
             m[ht] = mx;
             float big = 0.f;
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
+            for (int nb = 0; nb < 4; ++nb) {
               p[nb] = make_float2(ex2(u[nb].x - ref), ex2(u[nb].y - ref));
-              big = max3(big, p[nb].x * vp[nb].x, p[nb].y * vp[nb].y);
+              w[nb] = __fmul2_rn(p[nb], vp(nb));
+              big = max3(big, w[nb].x, w[nb].y);
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -666,28 +689,31 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 ? 2 : 1)
               o[ht][c][3] *= rb;
             }
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-              w[nb] = make_float2(p[nb].x * (vp[nb].x * f_new), p[nb].y * (vp[nb].y * f_new));
+            for (int nb = 0; nb < 4; ++nb)
+              w[nb] = __fmul2_rn(p[nb], __fmul2_rn(vp(nb), make_float2(f_new, f_new)));
           }
-          const float2 sum = __fadd2_rn(p[0], p[1]);
+          const float2 sum = __fadd2_rn(__fadd2_rn(p[0], p[1]), __fadd2_rn(p[2], p[3]));
           l[ht] += sum.x + sum.y;
-          pb[ht][0] = pack_f16(w[0].x, w[0].y);
-          pb[ht][1] = pack_f16(w[1].x, w[1].y);
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) pb[ht][nb] = pack_f16(w[nb].x, w[nb].y);
         }
         // V: a transposed matrix's register holds dimensions d, d + 1 of two keys
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t vc[4];
-          load_matrices_t(vt + code_at((lane >> 3 & 1) * 8 + (lane & 7), 2 * cc + (lane >> 4)), vc);
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t x0 = __byte_perm(vc[2 * c], 0, 0x3120), x1 = __byte_perm(vc[2 * c + 1], 0, 0x3120);
-            const uint32_t va[4] = {kv8_pair((uint16_t)x0), kv8_pair((uint16_t)(x0 >> 16)),
-                                    kv8_pair((uint16_t)x1), kv8_pair((uint16_t)(x1 >> 16))};
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t vc[4];
+            load_matrices_t(vt + (cc ? v_at ^ 32 : v_at) + 16 * kk * kD, vc);
 #pragma unroll
-            for (int ht = 0; ht < kTiles; ++ht) mma_f16(o[ht][2 * cc + c], va, pb[ht][0], pb[ht][1]);
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t x0 = __byte_perm(vc[2 * c], 0, 0x3120), x1 = __byte_perm(vc[2 * c + 1], 0, 0x3120);
+              const uint32_t va[4] = {kv8_pair((uint16_t)x0), kv8_pair((uint16_t)(x0 >> 16)),
+                                      kv8_pair((uint16_t)x1), kv8_pair((uint16_t)(x1 >> 16))};
+#pragma unroll
+              for (int ht = 0; ht < kTiles; ++ht)
+                mma_f16(o[ht][2 * cc + c], va, pb[ht][2 * kk], pb[ht][2 * kk + 1]);
+            }
           }
-        }
       }
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kMStages - 2) : "memory");
       __syncthreads();  // the next tile and its table; this one's readers are done
@@ -822,7 +848,7 @@ Decode8Plan plan_of(int dtype, int B, int Hq, int Hkv, int max_kv) {
     p.sub = kMWarps / p.nh >= 8 ? 8 : kMWarps / p.nh >= 4 ? 4 : kMWarps / p.nh >= 2 ? 2 : 1;
     p.chunk = 0;
     // as many as the SMs hold at a time; no more than the merge's table has room for
-    const int ny = (Hkv + p.nh - 1) / p.nh * p.blocks, per_sm = tiles == 1 ? 2 : 1;
+    const int ny = (Hkv + p.nh - 1) / p.nh * p.blocks, per_sm = tiles == 1 && p.sub < 8 ? 2 : 1;
     p.ctas = std::min(std::max(1, per_sm * sms / ny), kMaxParts / p.sub);
     p.parts = ((size_t)p.ctas + B) * p.sub;
   } else {
