@@ -22,7 +22,7 @@ struct ChunkParts {
   float *o;
   int ns, chunk;
   bool joined;       // every row's splits are merged with those of another list
-  bool keep_status;  // an earlier kernel of the call has cleared the status word
+  bool keep_status;  // an earlier kernel of the call, which may still run, cleared the status word
   __device__ __forceinline__ bool direct(int lim) const {
     return !joined && (ns == 1 || lim <= chunk);
   }
@@ -351,8 +351,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     na = pre.used(t);
     nb = own.used(t);
   }
-  // every warp waits, so that this grid never ends before the one it follows
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (na < 0 && nb < 0) return;  // no request's row
   na = max(na, 0);
   nb = max(nb, 0);
@@ -398,7 +396,6 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (status) clear_status(status);
   int na = pre.used(t), nb = own.used(t);
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (na < 0 && nb < 0) return;
   na = max(na, 0);
   nb = max(nb, 0);
@@ -1402,26 +1399,40 @@ ChunkPlan chunk_plan(int dtype, int B, int Hq, int Hkv, int n_rows, int max_q, i
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// `beside`: may start while the kernel launched before it runs (no word of that
+// one's is read), once all of that one's CTAs have
+template <typename... P, typename... A>
+cudaError_t launch_attention(void (*kernel)(P...), dim3 grid, int threads, int smem, bool beside,
+                             cudaStream_t s, const A &...args) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_f32(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                        int64_t tiles, uint32_t *status, cudaStream_t s) {
   const int smem = (int)sizeof(F32Smem);
-  cudaError_t e =
-      cudaFuncSetAttribute(chunk_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  chunk_f32_kernel<<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kFThreads, smem, s>>>(
-      a, (float *)out, lse, part, status);
-  return cudaGetLastError();
+  return launch_attention(chunk_f32_kernel, dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), kFThreads,
+                          smem, part.keep_status, s, a, (float *)out, lse, part, status);
 }
 
 cudaError_t launch_small(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
                          uint32_t *status, cudaStream_t s) {
   const int warps = std::min(a.Hkv, kSHeads), smem = warps * kSSt * 2 * (kSTile + kSKeys * 4);
-  cudaError_t e = cudaFuncSetAttribute(chunk_small_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  chunk_small_kernel<<<dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads), warps * 32, smem, s>>>(
-      a, (__nv_bfloat16 *)out, lse, part, status);
-  return cudaGetLastError();
+  return launch_attention(chunk_small_kernel, dim3(part.ns, a.B, (a.Hkv + kSHeads - 1) / kSHeads),
+                          warps * 32, smem, part.keep_status, s, a, (__nv_bfloat16 *)out, lse, part,
+                          status);
 }
 
 template <int kTiles>
@@ -1436,19 +1447,16 @@ cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkPar
   }();
   if (!regs_ok) return cudaErrorInvalidConfiguration;
   const int smem = (int)sizeof(TcSmem<kTiles>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<kTiles>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  chunk_tc_kernel<kTiles><<<dim3((unsigned)(tiles * part.ns), a.Hkv, a.B), tc_threads(kTiles), smem, s>>>(
-      a, (__nv_bfloat16 *)out, lse, part, status);
-  return cudaGetLastError();
+  return launch_attention(chunk_tc_kernel<kTiles>, dim3((unsigned)(tiles * part.ns), a.Hkv, a.B),
+                          tc_threads(kTiles), smem, part.keep_status, s, a, (__nv_bfloat16 *)out, lse,
+                          part, status);
 }
 
-// a merge over `items` (row, head) pairs as a programmatic dependent of the
-// kernel launched before it
-template <typename... P, typename... A>
-cudaError_t launch_join(int64_t items, bool warps, void (*warp_kernel)(P...),
-                        void (*cta_kernel)(P...), cudaStream_t s, const A &...args) {
+template <typename T>
+cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
+                         cudaStream_t s) {
+  const int64_t items = (int64_t)a.n_rows * a.Hq;
+  const bool warps = part.ns <= kWarpMerge;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(warps ? (items + kMergeWarps - 1) / kMergeWarps : items));
   cfg.blockDim = dim3(warps ? kMergeWarps * 32 : kMergeThreads);
@@ -1458,22 +1466,22 @@ cudaError_t launch_join(int64_t items, bool warps, void (*warp_kernel)(P...),
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, warps ? warp_kernel : cta_kernel, args...);
-}
-
-template <typename T>
-cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const ChunkParts &part,
-                         cudaStream_t s) {
-  return launch_join((int64_t)a.n_rows * a.Hq, part.ns <= kWarpMerge, chunk_merge_warp_kernel<T>,
-                     chunk_merge_kernel<T>, s, a, (T *)out, lse, part);
+  return cudaLaunchKernelEx(&cfg, warps ? chunk_merge_warp_kernel<T> : chunk_merge_kernel<T>, a,
+                            (T *)out, lse, part);
 }
 
 template <typename T>
 cudaError_t launch_prefix_merge(const PrefixParts &pre, const PrefixParts &own, void *out, float *lse,
                                 uint32_t *status, cudaStream_t s) {
-  return launch_join((int64_t)own.batch.n_rows * own.batch.Hq,
-                     pre.part.ns + own.part.ns <= kWarpMerge, prefix_merge_warp_kernel<T>,
-                     prefix_merge_kernel<T>, s, pre, own, (T *)out, lse, status);
+  // not as a programmatic dependent: it follows both passes, which may end in
+  // either order
+  const int64_t items = (int64_t)own.batch.n_rows * own.batch.Hq;
+  if (pre.part.ns + own.part.ns <= kWarpMerge)
+    prefix_merge_warp_kernel<T><<<(unsigned)((items + kMergeWarps - 1) / kMergeWarps),
+                                  kMergeWarps * 32, 0, s>>>(pre, own, (T *)out, lse, status);
+  else
+    prefix_merge_kernel<T><<<(unsigned)items, kMergeThreads, 0, s>>>(pre, own, (T *)out, lse, status);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kind(const ChunkPlan &p, const ChunkBatch &a, void *out, float *lse,
@@ -1573,7 +1581,7 @@ cudaError_t launch_prefix(int dtype, int Hq, int Hkv, int S, int n_groups,
     cleared = true;
   }
   if (p.own.tiles > 0) {
-    own.part.keep_status = cleared;
+    own.part.keep_status = cleared;  // and it runs beside the first pass
     const cudaError_t e = launch_kind(p.own, own.batch, out, lse, own.part, status, s);
     if (e != cudaSuccess) return e;
     cleared = true;

@@ -7,7 +7,6 @@
 #include "kv8.cuh"
 
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 namespace akv {
@@ -280,15 +279,6 @@ struct __align__(16) MmaSmem {
   float cs[kD / 2], sn[kD / 2];  // of the query
 };
 
-// Frequencies in turns: theta / 2 pi = hi 2^-32 + lo 2^-64, so that a position times
-// it modulo 1 is exact to 2^-32 turns for any position, in two integer products.
-struct Turns {
-  int32_t hi[kD / 2], lo[kD / 2];
-};
-__device__ __forceinline__ uint32_t turn_of(int hi, int lo, int pos) {
-  return (uint32_t)pos * (uint32_t)hi + (uint32_t)__mulhi(pos, lo);
-}
-
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
@@ -430,8 +420,7 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
 
     if (threadIdx.x < kD / 2) {
       const int f = threadIdx.x;
-      const float t = (float)(int)turn_of(turns.hi[f], turns.lo[f], a.qpos[b]) * 4.656612873e-10f;
-      sincospif(t, &sm.sn[f], &sm.cs[f]);
+      turn_cs(turns.hi[f], turns.lo[f], a.qpos[b], &sm.cs[f], &sm.sn[f]);
     }
     for (int x = threadIdx.x; x < kMStages * kStep; x += kMThreads) {
       (&sm.idx[0][0])[x] = x < nk ? __ldg(list + x) : 0;
@@ -903,12 +892,7 @@ cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const Turns &turn
 }
 template <int kTiles>
 cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const RopeTheta &th, cudaStream_t s) {
-  Turns turns;
-  for (int f = 0; f < kD / 2; ++f) {
-    const double t = th.th[f] / 6.283185307179586476925286766559 * 4294967296.0, hi = std::rint(t);
-    turns.hi[f] = (int32_t)(uint32_t)(int64_t)hi;
-    turns.lo[f] = (int32_t)std::min(std::rint((t - hi) * 4294967296.0), 2147483647.0);
-  }
+  const Turns turns = turns_of(th);
   return p.sub == 8   ? launch_mma<kTiles, 8>(a, p, turns, s)
          : p.sub == 4 ? launch_mma<kTiles, 4>(a, p, turns, s)
          : p.sub == 2 ? launch_mma<kTiles, 2>(a, p, turns, s)

@@ -4,8 +4,6 @@
 // a key that was stored rotated would be rounded to 8 bits again at every turn.
 #include "kv8.cuh"
 
-#include <algorithm>
-
 namespace akv {
 namespace {
 
@@ -49,59 +47,73 @@ __global__ void __launch_bounds__(kThreads)
   if (c == 0) (value ? pool.v_scale : pool.k_scale)[to] = (uint8_t)scale;
 }
 
-// A warp per entry: its 2 Hkv head rows, eight at a time; lane f forms the angle
-// of frequency f once and the lanes fetch theirs by shuffle.  Lane c of a row
-// holds values 8 c .. 8 c + 7 and the 32 + of these: the two sides of its
-// rotation pairs.
+// A warp per entry: its 2 Hkv head rows, eight at a time, two such passes in
+// flight; lane f forms the angle of frequency f once and the lanes fetch theirs by
+// shuffle.  Lane c of a row holds values 8 c .. 8 c + 7 and the 32 + of these: the
+// two sides of its rotation pairs.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     kv8_read_kernel(int n, int Hkv, const int32_t *__restrict__ src,
                     const int32_t *__restrict__ pos, const int32_t *__restrict__ dst, int R,
-                    const Kv8Pool pool, T *k_out, T *v_out, const __grid_constant__ RopeTheta th) {
-  __shared__ ThetaSmem ts;
+                    const Kv8Pool pool, T *k_out, T *v_out, const __grid_constant__ Turns turns) {
+  constexpr int E = Chunk<T>::kElems;
   const int lane = threadIdx.x & 31, c = lane % kLanes, r = lane / kLanes;
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  stage_theta(th, ts);
-  __syncthreads();
   if (i >= n) return;
   const int from = __ldg(src + i), to = dst ? __ldg(dst + i) : (int)i;
+  const int p = pos ? __ldg(pos + i) : 0;
   if ((unsigned)from >= (unsigned)pool.S || (unsigned)to >= (unsigned)R) return;
+  uint2 w[2][2];
+  uint32_t power[2];
+  auto fetch = [&](int x, int u) {
+    if (x >= 2 * Hkv) return;
+    const bool value = x >= Hkv;
+    const int64_t at = (int64_t)from * Hkv + (value ? x - Hkv : x);
+    const uint2 *row = reinterpret_cast<const uint2 *>((value ? pool.v : pool.k) + at * kD);
+    w[u][0] = __ldg(row + c);
+    w[u][1] = __ldg(row + c + kLanes);
+    power[u] = __ldg((value ? pool.v_scale : pool.k_scale) + at);
+  };
+  fetch(r, 0);
+  fetch(r + kRows, 1);
   float co[8], si[8];
   if (pos) {
     float cf, sf;
-    rope_cs(th, ts, lane, __ldg(pos + i), &cf, &sf);
+    turn_cs(turns.hi[lane], turns.lo[lane], p, &cf, &sf);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       co[e] = __shfl_sync(0xffffffffu, cf, 8 * c + e);
       si[e] = __shfl_sync(0xffffffffu, sf, 8 * c + e);
     }
   }
-  for (int x = r; x < 2 * Hkv; x += kRows) {
-    const bool value = x >= Hkv;
-    const int h = value ? x - Hkv : x;
-    const int64_t at = (int64_t)from * Hkv + h;
-    const uint2 *row = reinterpret_cast<const uint2 *>((value ? pool.v : pool.k) + at * kD);
-    const uint2 a = __ldg(row + c), b = __ldg(row + c + kLanes);
-    const float power = kv8_power(__ldg((value ? pool.v_scale : pool.k_scale) + at));
-    float y0[8], y1[8];
-    kv8_floats(a.x, power, y0);
-    kv8_floats(a.y, power, y0 + 4);
-    kv8_floats(b.x, power, y1);
-    kv8_floats(b.y, power, y1 + 4);
-    if (pos && !value) {
+  for (int x0 = r; x0 < 2 * Hkv; x0 += 2 * kRows) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = y0[e], w = y1[e];
-        y0[e] = u * co[e] - w * si[e];
-        y1[e] = u * si[e] + w * co[e];
+    for (int u = 0; u < 2; ++u) {
+      const int x = x0 + u * kRows;
+      if (x >= 2 * Hkv) break;
+      const bool value = x >= Hkv;
+      const float f = kv8_power(power[u]);
+      float y0[8], y1[8];
+      kv8_floats(w[u][0].x, f, y0);
+      kv8_floats(w[u][0].y, f, y0 + 4);
+      kv8_floats(w[u][1].x, f, y1);
+      kv8_floats(w[u][1].y, f, y1 + 4);
+      fetch(x + 2 * kRows, u);
+      if (pos && !value) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = y0[e], z = y1[e];
+          y0[e] = y * co[e] - z * si[e];
+          y1[e] = y * si[e] + z * co[e];
+        }
       }
-    }
-    constexpr int E = Chunk<T>::kElems;
-    uint4 *out = reinterpret_cast<uint4 *>((value ? v_out : k_out) + ((int64_t)to * Hkv + h) * kD);
+      uint4 *out = reinterpret_cast<uint4 *>((value ? v_out : k_out) +
+                                             ((int64_t)to * Hkv + (value ? x - Hkv : x)) * kD);
 #pragma unroll
-    for (int j = 0; j < 8 / E; ++j) {
-      out[c * (8 / E) + j] = f32_to_chunk<T>(y0 + j * E);
-      out[(c + kLanes) * (8 / E) + j] = f32_to_chunk<T>(y1 + j * E);
+      for (int j = 0; j < 8 / E; ++j) {
+        out[c * (8 / E) + j] = f32_to_chunk<T>(y0 + j * E);
+        out[(c + kLanes) * (8 / E) + j] = f32_to_chunk<T>(y1 + j * E);
+      }
     }
   }
 }
@@ -121,7 +133,7 @@ cudaError_t read(int Hkv, int n, const int32_t *src, const int32_t *pos, const i
                  cudaStream_t s) {
   const int per = kThreads / 32;
   kv8_read_kernel<T><<<(unsigned)(((int64_t)n + per - 1) / per), kThreads, 0, s>>>(
-      n, Hkv, src, pos, dst, R, pool, (T *)k_out, (T *)v_out, th);
+      n, Hkv, src, pos, dst, R, pool, (T *)k_out, (T *)v_out, turns_of(th));
   return cudaGetLastError();
 }
 

@@ -12,6 +12,9 @@
 
 #include "common.cuh"
 
+#include <algorithm>
+#include <cmath>
+
 namespace akv {
 
 // |x| as bits, 0 where x is not finite: ordered as |x| is
@@ -60,6 +63,29 @@ __device__ __forceinline__ void kv8_floats(uint32_t codes, float power, float *x
   x[1] = u.y * power;
   x[2] = w.x * power;
   x[3] = w.y * power;
+}
+
+// Frequencies in turns: theta / 2 pi = hi 2^-32 + lo 2^-64, so that a position times
+// it modulo 1 is exact to 2^-32 turns for any position, in two integer products.
+struct Turns {
+  int32_t hi[kD / 2], lo[kD / 2];
+};
+__device__ __forceinline__ uint32_t turn_of(int hi, int lo, int pos) {
+  return (uint32_t)pos * (uint32_t)hi + (uint32_t)__mulhi(pos, lo);
+}
+
+// cos and sin, the angle good to 1e-7
+__device__ __forceinline__ void turn_cs(int hi, int lo, int pos, float *c, float *s) {
+  sincospif((float)(int)turn_of(hi, lo, pos) * 4.656612873e-10f, s, c);
+}
+inline Turns turns_of(const RopeTheta &th) {
+  Turns turns;
+  for (int f = 0; f < kD / 2; ++f) {
+    const double t = th.th[f] / 6.283185307179586476925286766559 * 4294967296.0, hi = std::rint(t);
+    turns.hi[f] = (int32_t)(uint32_t)(int64_t)hi;
+    turns.lo[f] = (int32_t)std::min(std::rint((t - hi) * 4294967296.0), 2147483647.0);
+  }
+  return turns;
 }
 
 }  // namespace akv
