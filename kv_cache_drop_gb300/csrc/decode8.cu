@@ -81,12 +81,12 @@ struct SimtSmem {
   float p[kSHeads][kSKeys];
   float v[kSKeys][kD];
   float alpha[kSHeads];
-  ThetaSmem ts;
+  int turn_hi[kD / 2], turn_lo[kD / 2];
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kSThreads)
-    decode8_simt_kernel(const Decode8 a, const __grid_constant__ RopeTheta th) {
+    decode8_simt_kernel(const Decode8 a, const __grid_constant__ Turns turns) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   SimtSmem &sm = *reinterpret_cast<SimtSmem *>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -98,14 +98,17 @@ __global__ void __launch_bounds__(kSThreads)
   const int c0 = split * a.chunk, c1 = min(n, c0 + a.chunk);
   if (c0 >= n) return;  // the merge reads only splits that hold entries
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  stage_theta(th, sm.ts);
+  if (threadIdx.x < kD / 2) {
+    sm.turn_hi[threadIdx.x] = turns.hi[threadIdx.x];
+    sm.turn_lo[threadIdx.x] = turns.lo[threadIdx.x];
+  }
   // every head block writes the same bytes
   if (a.new_slot && c1 == n && warp < 2) append_row<T>(a, b, g, warp == 1);
   __syncthreads();
   for (int x = threadIdx.x; x < heads * (kD / 2); x += kSThreads) {
     const int h = x / (kD / 2), f = x % (kD / 2);
     float c, s;
-    rope_cs(th, sm.ts, f, a.qpos[b], &c, &s);
+    turn_cs(sm.turn_hi[f], sm.turn_lo[f], a.qpos[b], &c, &s);
     const T *row = (const T *)a.q + ((int64_t)b * a.Hq + h0 + h) * kD;
     const float x1 = to_float<T>(row[f]), x2 = to_float<T>(row[f + kD / 2]);
     sm.q[h][f] = x1 * c - x2 * s;
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kSThreads)
 #pragma unroll
       for (int f = 0; f < kD / 2; ++f) {
         float c, s;
-        rope_cs(th, sm.ts, f, pos, &c, &s);
+        turn_cs(turns.hi[f], turns.lo[f], pos, &c, &s);
         const float x1 = x[f], x2 = x[f + kD / 2];
         x[f] = x1 * c - x2 * s;
         x[f + kD / 2] = x1 * s + x2 * c;
@@ -876,7 +879,7 @@ cudaError_t launch_simt(const Decode8 &a, const Decode8Plan &p, const RopeTheta 
   const cudaError_t e = cudaFuncSetAttribute(decode8_simt_kernel<float>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode8_simt_kernel<float><<<dim3(p.ctas, a.Hkv * p.blocks, a.B), kSThreads, smem, s>>>(a, th);
+  decode8_simt_kernel<float><<<dim3(p.ctas, a.Hkv * p.blocks, a.B), kSThreads, smem, s>>>(a, turns_of(th));
   return cudaGetLastError();
 }
 

@@ -47,73 +47,78 @@ __global__ void __launch_bounds__(kThreads)
   if (c == 0) (value ? pool.v_scale : pool.k_scale)[to] = (uint8_t)scale;
 }
 
-// A warp per entry: its 2 Hkv head rows, eight at a time, two such passes in
+// A warp per entry: its 2 Hkv head rows, four at a time, kFlight such passes in
 // flight; lane f forms the angle of frequency f once and the lanes fetch theirs by
-// shuffle.  Lane c of a row holds values 8 c .. 8 c + 7 and the 32 + of these: the
-// two sides of its rotation pairs.
+// shuffle.  Eight lanes take a head row: lane c holds values 4 c .. 4 c + 3 and the
+// 32 + of these, the two sides of its rotation pairs, so that few registers leave
+// many warps to cover the chain from list entry to row (four lanes a row, with
+// 72 registers: 22 us on the device for 26,081 entries of 8 heads; XX now).
+constexpr int kReadLanes = 8, kReadRows = 32 / kReadLanes, kFlight = 4;
+__device__ __forceinline__ void store4(float *to, const float *y) {
+  *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *to, const float *y) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+  *reinterpret_cast<uint2 *>(to) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                              *reinterpret_cast<const uint32_t *>(&b));
+}
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     kv8_read_kernel(int n, int Hkv, const int32_t *__restrict__ src,
                     const int32_t *__restrict__ pos, const int32_t *__restrict__ dst, int R,
                     const Kv8Pool pool, T *k_out, T *v_out, const __grid_constant__ Turns turns) {
-  constexpr int E = Chunk<T>::kElems;
-  const int lane = threadIdx.x & 31, c = lane % kLanes, r = lane / kLanes;
+  const int lane = threadIdx.x & 31, c = lane % kReadLanes, r = lane / kReadLanes;
   const int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (i >= n) return;
   const int from = __ldg(src + i), to = dst ? __ldg(dst + i) : (int)i;
   const int p = pos ? __ldg(pos + i) : 0;
   if ((unsigned)from >= (unsigned)pool.S || (unsigned)to >= (unsigned)R) return;
-  uint2 w[2][2];
-  uint32_t power[2];
+  const int64_t row0 = (int64_t)from * Hkv;
+  T *const k_to = k_out + (int64_t)to * Hkv * kD, *const v_to = v_out + (int64_t)to * Hkv * kD;
+  uint32_t w[kFlight][2], power[kFlight];
   auto fetch = [&](int x, int u) {
     if (x >= 2 * Hkv) return;
     const bool value = x >= Hkv;
-    const int64_t at = (int64_t)from * Hkv + (value ? x - Hkv : x);
-    const uint2 *row = reinterpret_cast<const uint2 *>((value ? pool.v : pool.k) + at * kD);
+    const int64_t at = row0 + (value ? x - Hkv : x);
+    const uint32_t *row = reinterpret_cast<const uint32_t *>((value ? pool.v : pool.k) + at * kD);
     w[u][0] = __ldg(row + c);
-    w[u][1] = __ldg(row + c + kLanes);
+    w[u][1] = __ldg(row + c + kReadLanes);
     power[u] = __ldg((value ? pool.v_scale : pool.k_scale) + at);
   };
-  fetch(r, 0);
-  fetch(r + kRows, 1);
-  float co[8], si[8];
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u) fetch(r + u * kReadRows, u);
+  float co[4], si[4];
   if (pos) {
     float cf, sf;
     turn_cs(turns.hi[lane], turns.lo[lane], p, &cf, &sf);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      co[e] = __shfl_sync(0xffffffffu, cf, 8 * c + e);
-      si[e] = __shfl_sync(0xffffffffu, sf, 8 * c + e);
+    for (int e = 0; e < 4; ++e) {
+      co[e] = __shfl_sync(0xffffffffu, cf, 4 * c + e);
+      si[e] = __shfl_sync(0xffffffffu, sf, 4 * c + e);
     }
   }
-  for (int x0 = r; x0 < 2 * Hkv; x0 += 2 * kRows) {
+  for (int x0 = r; x0 < 2 * Hkv; x0 += kFlight * kReadRows) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int x = x0 + u * kRows;
+    for (int u = 0; u < kFlight; ++u) {
+      const int x = x0 + u * kReadRows;
       if (x >= 2 * Hkv) break;
       const bool value = x >= Hkv;
       const float f = kv8_power(power[u]);
-      float y0[8], y1[8];
-      kv8_floats(w[u][0].x, f, y0);
-      kv8_floats(w[u][0].y, f, y0 + 4);
-      kv8_floats(w[u][1].x, f, y1);
-      kv8_floats(w[u][1].y, f, y1 + 4);
-      fetch(x + 2 * kRows, u);
+      float y0[4], y1[4];
+      kv8_floats(w[u][0], f, y0);
+      kv8_floats(w[u][1], f, y1);
+      fetch(x + kFlight * kReadRows, u);
       if (pos && !value) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const float y = y0[e], z = y1[e];
           y0[e] = y * co[e] - z * si[e];
           y1[e] = y * si[e] + z * co[e];
         }
       }
-      uint4 *out = reinterpret_cast<uint4 *>((value ? v_out : k_out) +
-                                             ((int64_t)to * Hkv + (value ? x - Hkv : x)) * kD);
-#pragma unroll
-      for (int j = 0; j < 8 / E; ++j) {
-        out[c * (8 / E) + j] = f32_to_chunk<T>(y0 + j * E);
-        out[(c + kLanes) * (8 / E) + j] = f32_to_chunk<T>(y1 + j * E);
-      }
+      T *const out = (value ? v_to + (x - Hkv) * kD : k_to + x * kD) + 4 * c;
+      store4(out, y0);
+      store4(out + kD / 2, y1);
     }
   }
 }
