@@ -344,9 +344,10 @@ struct PrefixParts {
   }
 };
 
-// Up to kWarpMerge splits of both lists: CTA = row, a warp per head (every eighth),
+// Up to kPrefixWarp splits of both lists: CTA = row, a warp per head (every eighth),
 // two columns and one split's weight per lane.  (A warp per row and head looked
 // every row's lists up again: 22.7 us for 1,518 rows of 24 heads, XX now.)
+constexpr int kPrefixWarp = 8;
 template <typename T>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_merge_warp_kernel(const PrefixParts pre, const PrefixParts own, T *out, float *lse,
@@ -1493,7 +1494,7 @@ template <typename T>
 cudaError_t launch_prefix_merge(const PrefixParts &pre, const PrefixParts &own, void *out, float *lse,
                                 uint32_t *status, cudaStream_t s) {
   const int n_rows = own.batch.n_rows;
-  if (pre.part.ns + own.part.ns <= kWarpMerge)
+  if (pre.part.ns + own.part.ns <= kPrefixWarp)
     return launch_join(prefix_merge_warp_kernel<T>, n_rows, kMergeWarps * 32, s, pre, own, (T *)out,
                        lse, status);
   return launch_join(prefix_merge_kernel<T>, (int64_t)n_rows * own.batch.Hq, kMergeThreads, s, pre, own,

@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
             const uint8_t *const src = what ? a.pool.v_scale : a.pool.k_scale;
             const uint32_t to = smem_u32(sm.scale[stage][what][key]);
             if ((a.Hkv & 7) == 0) copy8(to, src + first);
-            else if (!odd) copy4(to, src + first, 4);
-            else {
+            else if (a.Hkv == 4) copy4(to, src + first, 4);
+            else {  // as many words as the CTA's heads lie in, up to the last row's end
               const int64_t word = first & ~(int64_t)3;
               for (int w = 0; w < (((int)(first & 3) + nh + 3) >> 2); ++w)
                 if (word + 4 * w < scales)
@@ -573,10 +573,11 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
     __syncthreads();  // tile 0 and its table
 
     for (int it = 0; it < n_tiles; ++it) {
-      issue(it + kMStages - 1);
       table(it + 1);  // past the end: of whatever the ring holds
       const int left = nk - it * kStep - kMKeys * part;
-      if (active && left > 0) {
+      if (!(active && left > 0)) {
+        issue(it + kMStages - 1);
+      } else {
         const uint32_t kt = tile_at + it % kMStages * (2 * kMWarps * kMTile), vt = kt + kMWarps * kMTile;
         {
           const int key = part * kMKeys + lane;
@@ -689,6 +690,7 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) pb[ht][nb] = pack_f16(w[nb].x, w[nb].y);
         }
+        issue(it + kMStages - 1);  // while the weights' products wait for nothing else
         // V: a transposed matrix's register holds dimensions d, d + 1 of two keys
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)

@@ -21,13 +21,14 @@ __global__ void __launch_bounds__(kThreads)
                       const T *__restrict__ v, int64_t vs, const int32_t *__restrict__ slot,
                       const Kv8Pool pool) {
   constexpr int E = Chunk<T>::kElems;
-  const int r = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  const uint32_t r = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;  // may pass 2^31 - 1
+  const int c = threadIdx.x % kLanes;
   const bool value = blockIdx.y != 0;
-  const int i = r / Hkv, h = r - i * Hkv;
-  const int at = r < rows ? __ldg(slot + i) : -1;
+  const int i = (int)(r / (uint32_t)Hkv), h = (int)(r - (uint32_t)i * (uint32_t)Hkv);
+  const int at = r < (uint32_t)rows ? __ldg(slot + i) : -1;
   const bool real = (unsigned)at < (unsigned)pool.S;  // else padding: nothing read or written
   const uint4 *src = reinterpret_cast<const uint4 *>(
-      (value ? v + i * vs : k + i * ks) + (int64_t)h * kD + c * kEach);
+      (value ? v + (int64_t)i * vs : k + (int64_t)i * ks) + (int64_t)h * kD + c * kEach);
   float x[kEach];
   uint32_t top = 0;
 #pragma unroll

@@ -438,3 +438,28 @@ def test_binding_refuses():
     with pytest.raises(akv.AkvError) as e:
         bt.run(d, ws=bt.workspace()[:-256] if bt.workspace().numel() > 256 else bt.workspace()[:1])
     assert "WORKSPACE" in str(e.value)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(12, 12), (40, 20), (12, 6), (14, 7), (30, 10), (22, 11), (100, 4)])
+def test_decode_head_counts_that_split_scale_words(Hq, Hkv):
+    """KV heads whose scales do not fill whole words, that take several CTAs, the
+    last of them with fewer heads; a pool whose last rows' words end with it."""
+    bt = Batch(50 + Hkv, [700, 33, 1, 129], Hq, Hkv, "bf16", new=True, S=870)
+    bt.idx[5], bt.idx[700] = bt.S - 1, bt.S - 1  # the pool's last row, twice
+    bt.slot[:] = [bt.idx[p - 1] for p in bt.ptr[1:]]
+    if bt.S - 1 in bt.slot:
+        bt.new = False
+    d = bt.device()
+    bt.check(bt.run(d))
+    assert all(np.array_equal(a, b) for a, b in zip(_host_pool(d["pool"]), bt.after()))
+
+
+def test_decode_many_requests():
+    """700 short lists, every fifth empty: ranges that hold several requests."""
+    rng = np.random.default_rng(5)
+    n = [0 if b % 5 == 2 else int(rng.integers(1, 90)) for b in range(700)]
+    for Hq, Hkv in ((16, 8), (4, 1)):
+        bt = Batch(60, n, Hq, Hkv, "bf16", new=True)
+        d = bt.device()
+        bt.check(bt.run(d))
+        assert all(np.array_equal(a, b) for a, b in zip(_host_pool(d["pool"]), bt.after()))
