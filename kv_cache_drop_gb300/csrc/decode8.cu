@@ -736,16 +736,17 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
   }
 }
 
-// Joins a row's partials by their log-sum-exp: CTA = (query head, request), eight
-// groups of 16 threads each summing every eighth partial's row.  Launched as a
+// Joins a row's partials by their log-sum-exp: CTA = (query head, request), 16
+// groups of 16 threads each summing every 16th partial's row, eight loads in
+// flight (one request may have 304 partials).  Launched as a
 // programmatic dependent of the attention kernel.  A request without entries
 // gets zeros.
-constexpr int kMergeThreads = 128, kMaxParts = 2560;
+constexpr int kMergeThreads = 256, kMergeGroups = kMergeThreads / 16, kMaxParts = 2560;
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Decode8 a, T *out) {
-  __shared__ float wgt[kMaxParts];
-  __shared__ float4 red[8][kD / 4];
-  __shared__ float tot[4], top[4];
+  __shared__ float2 part[kMaxParts];  // (maximum, then weight; sum)
+  __shared__ float4 red[kMergeGroups][kD / 4];
+  __shared__ float tot[kMergeThreads / 32], top[kMergeThreads / 32];
   const int h = blockIdx.x, b = blockIdx.y;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int beg;
@@ -772,33 +773,35 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Deco
   const float2 *ml = a.ml + at;
   float M = -INFINITY;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float m = __ldcg(&ml[s * apart].x);
-    wgt[s] = m;
-    M = fmaxf(M, m);
+    part[s] = __ldcg(ml + s * apart);
+    M = fmaxf(M, part[s].x);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) top[warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+#pragma unroll
+  for (int x = 0; x < kMergeThreads / 32; ++x) M = fmaxf(M, top[x]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   for (int s = threadIdx.x; s < used; s += kMergeThreads) {
-    const float f = exp2f(wgt[s] - ref);
-    wgt[s] = f;
-    L = fmaf(__ldcg(&ml[s * apart].y), f, L);
+    const float f = exp2f(part[s].x - ref);
+    part[s].x = f;
+    L = fmaf(part[s].y, f, L);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   if (lane == 0) tot[warp] = L;
   __syncthreads();
-  L = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+  L = 0.f;
+#pragma unroll
+  for (int x = 0; x < kMergeThreads / 32; ++x) L += tot[x];
   const int cg = threadIdx.x & 15, sg = threadIdx.x >> 4;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = sg; s < used; s += 8) {
+#pragma unroll 8
+  for (int s = sg; s < used; s += kMergeGroups) {
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.o + (at + s * apart) * kD) + cg);
-    const float f = wgt[s];
+    const float f = part[s].x;
     acc.x = fmaf(v.x, f, acc.x);
     acc.y = fmaf(v.y, f, acc.y);
     acc.z = fmaf(v.z, f, acc.z);
@@ -810,7 +813,8 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const Deco
     const int col = threadIdx.x;
     float x = 0.f;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) x += reinterpret_cast<const float *>(&red[y][col >> 2])[col & 3];
+    for (int y = 0; y < kMergeGroups; ++y)
+      x += reinterpret_cast<const float *>(&red[y][col >> 2])[col & 3];
     x = used > 0 ? x / L : 0.f;
     T *to = out + w * kD + col;
     if constexpr (sizeof(T) == 4) *to = x;
