@@ -391,15 +391,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
 }
 
-// More splits: a CTA per (row, head), eight groups of 16 threads each summing
-// every eighth split's row, 16 bytes per load.
+// More splits: a CTA per (row, head), 16 groups of 16 threads each summing every
+// 16th split's row, 16 bytes per load, eight loads in flight.
+constexpr int kPrefixThreads = 256, kPrefixGroups = kPrefixThreads / 16;
 template <typename T>
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kPrefixThreads)
     prefix_merge_kernel(const PrefixParts pre, const PrefixParts own, T *out, float *lse,
                         uint32_t *status) {
-  __shared__ float wgt[2 * kMaxSplit];
-  __shared__ float4 red[8][kD / 4];
-  __shared__ float tot[kMergeThreads / 32], top[kMergeThreads / 32];
+  __shared__ float2 part[2 * kMaxSplit];  // (maximum, then weight; sum)
+  __shared__ float4 red[kPrefixGroups][kD / 4];
+  __shared__ float tot[kPrefixThreads / 32], top[kPrefixThreads / 32];
   const int64_t w = blockIdx.x;
   const int t = (int)(w / own.batch.Hq);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -412,36 +413,38 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int n = na + nb;
   const float2 *ma = pre.part.ml + w * pre.part.ns, *mb = own.part.ml + w * own.part.ns - na;
   float M = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += kMergeThreads) {
-    const float m = __ldcg(&(s < na ? ma : mb)[s].x);
-    wgt[s] = m;
-    M = fmaxf(M, m);
+  for (int s = threadIdx.x; s < n; s += kPrefixThreads) {
+    part[s] = __ldcg((s < na ? ma : mb) + s);
+    M = fmaxf(M, part[s].x);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) top[warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+#pragma unroll
+  for (int x = 0; x < kPrefixThreads / 32; ++x) M = fmaxf(M, top[x]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int s = threadIdx.x; s < n; s += kMergeThreads) {
-    const float f = exp2f(wgt[s] - ref);
-    wgt[s] = f;
-    L = fmaf(__ldcg(&(s < na ? ma : mb)[s].y), f, L);
+  for (int s = threadIdx.x; s < n; s += kPrefixThreads) {
+    const float f = exp2f(part[s].x - ref);
+    part[s].x = f;
+    L = fmaf(part[s].y, f, L);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   if (lane == 0) tot[warp] = L;
   __syncthreads();
-  L = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+  L = 0.f;
+#pragma unroll
+  for (int x = 0; x < kPrefixThreads / 32; ++x) L += tot[x];
   const int cg = threadIdx.x & 15, sg = threadIdx.x >> 4;
   const float4 *oa = reinterpret_cast<const float4 *>(pre.part.o + w * pre.part.ns * kD) + cg;
   const float4 *ob = reinterpret_cast<const float4 *>(own.part.o + (w * own.part.ns - na) * kD) + cg;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = sg; s < n; s += 8) {
+#pragma unroll 8
+  for (int s = sg; s < n; s += kPrefixGroups) {
     const float4 v = __ldcg((s < na ? oa : ob) + s * (kD / 4));
-    const float f = wgt[s];
+    const float f = part[s].x;
     acc.x = fmaf(v.x, f, acc.x);
     acc.y = fmaf(v.y, f, acc.y);
     acc.z = fmaf(v.z, f, acc.z);
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   __syncthreads();
   if (threadIdx.x < kD / 4) {
     float y[4] = {};
-    for (int g = 0; g < 8; ++g) {
+    for (int g = 0; g < kPrefixGroups; ++g) {
       const float4 v = red[g][threadIdx.x];
       y[0] += v.x;
       y[1] += v.y;
@@ -1497,7 +1500,7 @@ cudaError_t launch_prefix_merge(const PrefixParts &pre, const PrefixParts &own, 
   if (pre.part.ns + own.part.ns <= kPrefixWarp)
     return launch_join(prefix_merge_warp_kernel<T>, n_rows, kMergeWarps * 32, s, pre, own, (T *)out,
                        lse, status);
-  return launch_join(prefix_merge_kernel<T>, (int64_t)n_rows * own.batch.Hq, kMergeThreads, s, pre, own,
+  return launch_join(prefix_merge_kernel<T>, (int64_t)n_rows * own.batch.Hq, kPrefixThreads, s, pre, own,
                      (T *)out, lse, status);
 }
 
