@@ -73,7 +73,10 @@ __device__ __forceinline__ void append_row(const Decode8 &a, int b, int g, bool 
 // CUDA cores: CTA = key split x KV head (up to 16 of its query heads) x request,
 // 128 entries at a time: a thread rotates one key in fp32 registers and takes
 // its products with the query heads; a warp per head forms the weights; a thread
-// per (dimension, every second head) sums the values from shared memory.
+// per (dimension, every second head) sums the values from shared memory.  fp32 is
+// the library's parity type, and the tensor cores take none.  3 requests of 500 to
+// 4,000 entries, 16 / 4 heads: 17 us on the device, 20.5 for the call (37 with
+// sincosf for the angles), bound by the chain within a CTA of one tile.
 // ---------------------------------------------------------------------------
 constexpr int kSThreads = 128, kSKeys = 128, kSHeads = 16;
 struct SimtSmem {
@@ -262,6 +265,12 @@ __global__ void __launch_bounds__(kSThreads)
 // An entry's row of all the CTA's heads is copied by neighbouring lanes
 // (cp.async), several tiles ahead, and so are list entries, scales and positions
 // (a plain load returns only after the copies queued before it).
+//
+// 14 requests of 20,000 to 90,000 entries, 64 / 8 heads: 162 us the call, 4.7 TB/s
+// (the floor is 111), where decode_heads_kernel takes 292 over bf16 keys before
+// RoPE.  252 instructions per 16 entries and head; no pipe is full: with 16 warps per
+// SM the latency of a step's chain bounds it.  With 16 entries a step, or splits of
+// 512 entries instead of ranges, 219 and 256 us.
 // ---------------------------------------------------------------------------
 constexpr int kMWarps = 8, kMThreads = 32 * kMWarps, kMKeys = 32;
 // tiles of a warp, and of list entries and positions: what leaves room for two

@@ -1,5 +1,5 @@
 """Definitions in 64 bits of the 8-bit cache and of attention over it, for the
-tests (numpy; written apart from the kernels and from perf's plain forms)."""
+tests (numpy; written apart from the kernels and from the timed plain forms)."""
 import numpy as np
 
 BASE = 10000.0
