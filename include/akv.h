@@ -631,7 +631,7 @@ akv_status akv_evict_by_mass(int32_t B, const int32_t *kv_indptr, const int32_t 
  * A cache in 8 bits: half the bytes per entry, for the pool whose lists the
  * decode calls read.  Pools: k_pool, v_pool [S, Hkv, D] e4m3 values (one byte,
  * no infinity), k_scale, v_scale [S, Hkv] bytes, a power of two 2^(byte - 127)
- * for each head row (e8m0).  A row stands for value * 2^s with the smallest s
+ * for each head row (e8m0, 255 never).  A row stands for value * 2^s with the smallest s
  * in -127 .. 127 for which the row's largest finite |x| is at most 448 * 2^s
  * (-127 for a row of zeros); each value is rounded to the nearest, ties to
  * even: at most 2^-4 of it off, or 2^-10 * 2^s where that is more.  What is not
@@ -676,7 +676,10 @@ akv_status akv_read_kv_q8(const akv_shape *shape, int32_t n, const int32_t *src,
  * the list must end with new_slot[b] (its kv_pos entry is q_pos[b]) and no other
  * entry of the batch may name that slot.  A request whose new_slot is outside
  * [0, S) or whose list is empty appends nothing.
- * Any number of query heads per KV head.  Limits: B <= 65535, Hq <= 65535, max_kv
+ * Any number of query heads per KV head.  bf16: the query keeps ~22 bits, keys are
+ * rotated in fp16 (three roundings of 2^-11 relative to their pair) whatever their
+ * scale, weights times their value's scale are rounded to fp16 (2^-11, or 2^-32 of
+ * the largest); sums are fp32.  Limits: B <= 65535, Hq <= 65535, max_kv
  * <= 2^30 (AKV_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned,
  * akv_decode_q8_workspace() bytes (split-KV partials); it serves one call at a
  * time.  All index data stays on the device, so the call can be captured in a
