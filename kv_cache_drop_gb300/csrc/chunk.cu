@@ -1468,9 +1468,11 @@ cudaError_t launch_tc(const ChunkBatch &a, void *out, float *lse, const ChunkPar
                           part, status);
 }
 
-// a merge, as a programmatic dependent of the kernel launched before it
+// A merge.  `beside`: as a programmatic dependent of the kernel launched before
+// it, which must be a pass of the same call: the merge reads the call's index
+// data before it waits, and only what came before that pass has ended by then.
 template <typename... P, typename... A>
-cudaError_t launch_join(void (*kernel)(P...), int64_t ctas, int threads, cudaStream_t s,
+cudaError_t launch_join(void (*kernel)(P...), int64_t ctas, int threads, bool beside, cudaStream_t s,
                         const A &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
@@ -1480,7 +1482,7 @@ cudaError_t launch_join(void (*kernel)(P...), int64_t ctas, int threads, cudaStr
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1490,19 +1492,21 @@ cudaError_t launch_merge(const ChunkBatch &a, void *out, float *lse, const Chunk
   const int64_t items = (int64_t)a.n_rows * a.Hq;
   if (part.ns <= kWarpMerge)
     return launch_join(chunk_merge_warp_kernel<T>, (items + kMergeWarps - 1) / kMergeWarps,
-                       kMergeWarps * 32, s, a, (T *)out, lse, part);
-  return launch_join(chunk_merge_kernel<T>, items, kMergeThreads, s, a, (T *)out, lse, part);
+                       kMergeWarps * 32, true, s, a, (T *)out, lse, part);
+  return launch_join(chunk_merge_kernel<T>, items, kMergeThreads, true, s, a, (T *)out, lse, part);
 }
 
+// `status` is not NULL where no pass ran: the merge opens the call, and follows
+// the caller's last kernel in full
 template <typename T>
 cudaError_t launch_prefix_merge(const PrefixParts &pre, const PrefixParts &own, void *out, float *lse,
                                 uint32_t *status, cudaStream_t s) {
   const int n_rows = own.batch.n_rows;
   if (pre.part.ns + own.part.ns <= kPrefixWarp)
-    return launch_join(prefix_merge_warp_kernel<T>, n_rows, kMergeWarps * 32, s, pre, own, (T *)out,
-                       lse, status);
-  return launch_join(prefix_merge_kernel<T>, (int64_t)n_rows * own.batch.Hq, kPrefixThreads, s, pre, own,
-                     (T *)out, lse, status);
+    return launch_join(prefix_merge_warp_kernel<T>, n_rows, kMergeWarps * 32, !status, s, pre, own,
+                       (T *)out, lse, status);
+  return launch_join(prefix_merge_kernel<T>, (int64_t)n_rows * own.batch.Hq, kPrefixThreads, !status, s,
+                     pre, own, (T *)out, lse, status);
 }
 
 cudaError_t launch_kind(const ChunkPlan &p, const ChunkBatch &a, void *out, float *lse,
