@@ -15,8 +15,8 @@
 // plain TMA loads: the same kernel then serves runs of any number of GPUs.  The
 // K-block ring bounds the bytes in flight at one CTA per SM, and the L2-to-SM
 // stream bounds the kernel: M = 1,048,576, N = 4096, K = 1024 takes 5.76 ms,
-// 1,527 TFLOP/s, with the tensor pipe 65% busy.  Pairs of CTAs that multicast
-// halves of W to one another took 5.27 ms, but such a load is for runs on one GPU.
+// 1,527 TFLOP/s, with the tensor pipe 65% busy.  Pairs of CTAs that each
+// loaded half of W for both took 5.27 ms, but such a load is for runs on one GPU.
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
