@@ -681,10 +681,11 @@ akv_status akv_read_kv_q8(const akv_shape *shape, int32_t n, const int32_t *src,
  * scale, weights times their value's scale are rounded to fp16 (2^-11, or 2^-32 of
  * the largest); sums are fp32.  Limits: B <= 65535, Hq <= 65535, max_kv
  * <= 2^30 (AKV_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned,
- * akv_decode_q8_workspace() bytes (split-KV partials); it serves one call at a
- * time.  All index data stays on the device, so the call can be captured in a
- * CUDA graph and replayed with other lengths within max_kv; make the first call
- * outside a capture (it loads the kernels). */
+ * akv_decode_q8_workspace() bytes (split-KV partials), which serve any call with
+ * no more requests and no larger max_kv, one call at a time.  All index data stays
+ * on the device, so the call can be captured in a CUDA graph and replayed with
+ * other lengths within max_kv; make the first call outside a capture (it loads the
+ * kernels). */
 size_t akv_decode_q8_workspace(const akv_shape *shape, int32_t B, int32_t max_kv);
 akv_status akv_decode_attention_q8(const akv_shape *shape, int32_t B, const void *q,
                                    const int32_t *q_pos, const void *k_new, const void *v_new,

@@ -844,6 +844,7 @@ struct Decode8Plan {
   int ctas, chunk, sub;
   int nh, blocks;  // KV heads per CTA (bf16), query head blocks of a KV head
   size_t parts;    // partials of a query head, over the batch
+  size_t most;     // the most of any call with no larger B and max_kv
 };
 Decode8Plan plan_of(int dtype, int B, int Hq, int Hkv, int max_kv) {
   Decode8Plan p;
@@ -857,18 +858,24 @@ Decode8Plan plan_of(int dtype, int B, int Hq, int Hkv, int max_kv) {
     // as many as the SMs hold at a time; no more than the merge's table has room for
     const int ny = (Hkv + p.nh - 1) / p.nh * p.blocks, per_sm = tiles == 1 && p.sub < 8 ? 2 : 1;
     p.ctas = std::min(std::max(1, per_sm * sms / ny), kMaxParts / p.sub);
-    p.parts = ((size_t)p.ctas + B) * p.sub;
+    p.parts = p.most = ((size_t)p.ctas + B) * p.sub;
   } else {
     p.blocks = (grp + kSHeads - 1) / kSHeads;
     p.nh = p.sub = 1;
     const auto splits = [&](int x) { return std::max<int64_t>(1, ((int64_t)max_kv + x - 1) / x); };
     const int64_t rows = (int64_t)B * Hkv * p.blocks;
     int c = 4096;
-    while (c > kSKeys && rows * splits(c) < 4LL * 4 * sms) c /= 2;
+    const int64_t want = 4LL * 4 * sms;
+    while (c > kSKeys && rows * splits(c) < want) c /= 2;
     while (splits(c) > kMaxParts) c *= 2;
     p.ctas = (int)splits(c);
     p.chunk = c;
     p.parts = (size_t)p.ctas * B;
+    // A smaller batch or shorter lists may be cut finer.  Splits below the longest
+    // were chosen because twice their length left rows * splits below `want`, so
+    // that rows * splits is below 2 * want; none is shorter than kSKeys.
+    const int64_t fine = std::min(B * splits(kSKeys), (2 * want - 1) / (Hkv * p.blocks));
+    p.most = (size_t)std::max(fine, B * std::min<int64_t>(splits(4096), kMaxParts));
   }
   return p;
 }
@@ -920,7 +927,7 @@ cudaError_t launch_mma(const Decode8 &a, const Decode8Plan &p, const RopeTheta &
 }  // namespace
 
 size_t decode_q8_workspace_bytes(int dtype, int B, int Hq, int Hkv, int max_kv) {
-  const size_t parts = plan_of(dtype, B, Hq, Hkv, max_kv).parts * Hq;
+  const size_t parts = plan_of(dtype, B, Hq, Hkv, max_kv).most * Hq;
   return up256(parts * sizeof(float2)) + up256(parts * kD * sizeof(float));
 }
 
