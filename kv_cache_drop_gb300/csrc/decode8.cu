@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(kSThreads)
 //
 // Weights are 2^(score - m) with m any reference near the maximum; times the
 // value's scale and a power of two f they are rounded to fp16.  A tile in which
-// a score passes m by 60 or a weight fp16's range raises m to the maximum and
-// sets f so that the largest weight is near 2^8.
+// a score passes m by 60 or a weight fp16's range, or which has a scale that times f
+// might pass fp32's (a weight of 0 times infinity), raises m to the maximum and sets f
+// so that the largest weight is near 2^8 and no scale of the tile times f passes 2^127.
 //
 // An entry's row of all the CTA's heads is copied by neighbouring lanes
 // (cp.async), several tiles ahead, and so are list entries, scales and positions
@@ -280,6 +281,7 @@ constexpr int ring_of(int sub) { return sub == 1 ? 8 : 4; }
 constexpr int kMTile = kMKeys * kD;       // bytes of a K (or V) tile of a head
 constexpr int kMTable = kMKeys * kD * 2;  // cos and sin of a tile, fp16
 constexpr int kMLeast = 2;                // tiles of a CTA, unless there are fewer
+constexpr uint32_t kHighScale = (127u + 27) << 23;  // 2^27, which the largest f takes to 2^127
 constexpr int kMScale = 16;               // bytes that hold a row's scales of eight heads from any byte on
 template <int kSub>
 struct __align__(16) MmaSmem {
@@ -587,6 +589,7 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
       if (!(active && left > 0)) {
         issue(it + kMStages - 1);
       } else {
+        uint32_t value;  // bits of this lane's value scale, ordered as it is
         const uint32_t kt = tile_at + it % kMStages * (2 * kMWarps * kMTile), vt = kt + kMWarps * kMTile;
         {
           const int key = part * kMKeys + lane;
@@ -595,7 +598,9 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
           if (odd) off += (slot_in(listed ? sm.idx[it % kMRing][key] : 0) * a.Hkv + g0) & 3;
           const uint8_t(*scale)[kStep][kMScale] = sm.scale[it % kMStages];
           sm.power[warp][0][lane] = listed ? kv8_power(scale[0][key][off]) : 0.f;
-          sm.power[warp][1][lane] = listed ? kv8_power(scale[1][key][off]) : 0.f;
+          const float vp = listed ? kv8_power(scale[1][key][off]) : 0.f;
+          sm.power[warp][1][lane] = vp;
+          value = __float_as_uint(vp);
         }
         float s[kTiles][4][4];
 #pragma unroll
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
             far = max3(far, x.x, x.y);
             most = max3(most, w[nb].x, w[nb].y);
           }
-          if (__any_sync(0xffffffffu, it == 0 || far > 60.f || most > 32768.f)) {
+          if (__any_sync(0xffffffffu, it == 0 || far > 60.f || most > 32768.f || value >= kHighScale)) {
             float mx = m[ht];
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) mx = max3(mx, u[nb].x, u[nb].y);
@@ -673,9 +678,11 @@ __global__ void __launch_bounds__(kMThreads, kTiles == 1 && kSub < 8 ? 2 : 1)
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^8 over the largest weight's power of two, at most 2^100 and, once
-            // there are sums, 2^60 times what it was
-            const int e8 = min(262 - (int)(__float_as_uint(big) >> 23), 227);
+            const uint32_t scale = __reduce_max_sync(0xffffffffu, value);
+            // 2^8 over the largest weight's power of two, at most 2^100, 2^127 over
+            // the largest scale and, once there are sums, 2^60 times what it was
+            const int e8 = min(min(262 - (int)(__float_as_uint(big) >> 23), 227),
+                               381 - (int)(scale >> 23));
             float f_new = __uint_as_float((uint32_t)e8 << 23);
             if (it > 0) f_new = fminf(f_new, f[ht] * 1.1529215e18f);
             const float ratio = it > 0 ? alpha * (f_new / f[ht]) : 0.f;

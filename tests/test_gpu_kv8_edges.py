@@ -1,8 +1,11 @@
-"""The 8-bit cache where it can go wrong: a workspace sized for larger calls."""
+"""The 8-bit cache where it can go wrong: a workspace sized for larger calls, value
+rows of very different size."""
+import numpy as np
 import pytest
 
 import kv_cache_drop_gb300 as akv
-from test_gpu_kv8 import Batch
+from _kv8 import held, quantise
+from test_gpu_kv8 import Batch, _bits
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +33,52 @@ def test_a_workspace_serves_smaller_calls(dtype):
     few.check(few.run(e, max_kv=5376, ws=room[:need]))
     few.check(few.run(e, max_kv=5632, ws=room[:need]))
     assert bool((room[need:] == 77).all())
+
+
+# ----------------------------------------------------------------- values
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (64, 8), (80, 8), (9, 1)])
+@pytest.mark.parametrize("power", [20, 28, 60, 115])
+def test_a_large_value_row_without_weight(power, Hq, Hkv, dtype):
+    """Entries in threes of tiles: value rows of zeros, which have the smallest scale;
+    then more of these and among them rows of up to 448 * 2^power whose weight is
+    exp(-320); then ordinary rows, whose part is all of the output.
+
+    Every score is exact: positions are 0, the query and the keys have one component.
+    The output is sum w v / sum w over the rows of weight 1 and exp(-1), whose sums
+    are good to 2^-18 in fp32, with weights rounded to fp16 (2^-11 each) and, in
+    bf16, the output to 2^-8 of itself.  What the large rows put in is below
+    448 * 2^115 exp(-320) = 2^-338."""
+    n = 3 * 3 * 256
+    bt = Batch(73, [n, n // 3 + 5], Hq, Hkv, dtype)
+    bt.pos[:], bt.q_pos[:] = 0, 0
+    q = np.zeros((2, Hq, 64))
+    q[..., 0] = 64.0
+    bt.q = _bits(q, dtype)
+    kc, ks, vc, vs = bt.pool
+    rng = np.random.default_rng(power)
+    for b in range(2):
+        rows = bt.idx[bt.ptr[b]:bt.ptr[b + 1]]
+        j = np.arange(len(rows))
+        kind = j // 256 % 3  # zeros, large, ordinary
+        kind[(kind == 1) & (j % 7 != 3)] = 0
+        k = np.zeros((len(rows), Hkv, 64))
+        k[..., 0] = np.where(kind == 1, -40.0, np.where(kind == 2, -0.125, 0.0))[:, None]
+        v = rng.standard_normal((len(rows), Hkv, 64)) + 2
+        v[kind == 0] = 0
+        v[kind == 1] *= 2.0 ** power
+        kc[rows], ks[rows] = quantise(k)
+        vc[rows], vs[rows] = quantise(v)
+    got = bt.run(bt.device()).float().cpu().numpy().astype(np.float64)
+    V = held(vc, vs)
+    for b in range(2):
+        rows = bt.idx[bt.ptr[b]:bt.ptr[b + 1]]
+        s = 8 * held(kc, ks)[rows][..., 0]                      # [n, Hkv]
+        w = np.exp(s)
+        want = np.einsum("jg,jgd->gd", w, V[rows]) / w.sum(0)[:, None]
+        size = np.einsum("jg,jgd->gd", w, np.abs(V[rows])) / w.sum(0)[:, None]
+        want, size = np.repeat(want, Hq // Hkv, 0), np.repeat(size, Hq // Hkv, 0)
+        tol = (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -18) * size if dtype == "bf16"
+               else 2.0 ** -24 * np.abs(want) + 2.0 ** -18 * size)
+        assert np.all(np.abs(got[b] - want) <= tol), float(np.abs((got[b] - want) / tol).max())
