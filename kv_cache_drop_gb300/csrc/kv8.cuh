@@ -65,8 +65,9 @@ __device__ __forceinline__ void kv8_floats(uint32_t codes, float power, float *x
   x[3] = w.y * power;
 }
 
-// Frequencies in turns: theta / 2 pi = hi 2^-32 + lo 2^-64, so that a position times
-// it modulo 1 is exact to 2^-32 turns for any position, in two integer products.
+// Frequencies in turns: theta / 2 pi = hi 2^-32 + lo 2^-64 for the double theta, so
+// that a position times it modulo 1 is off by less than 1.3 * 2^-32 turns (the floor, and a
+// quarter for lo's rounding), in two integer products, for any position.
 struct Turns {
   int32_t hi[kD / 2], lo[kD / 2];
 };
@@ -74,16 +75,21 @@ __device__ __forceinline__ uint32_t turn_of(int hi, int lo, int pos) {
   return (uint32_t)pos * (uint32_t)hi + (uint32_t)__mulhi(pos, lo);
 }
 
-// cos and sin, the angle good to 1e-7
+// cos and sin: the angle is good to 2^-24 of itself and 1.9e-9 (theta's own rounding,
+// 2^-53 of it, is beside that 2.4e-7 where the angle is 2^31)
 __device__ __forceinline__ void turn_cs(int hi, int lo, int pos, float *c, float *s) {
   sincospif((float)(int)turn_of(hi, lo, pos) * 4.656612873e-10f, s, c);
 }
 inline Turns turns_of(const RopeTheta &th) {
+  // 2^32 / 2 pi in two doubles: one would leave 23 bits of lo where theta is 1, and the
+  // turn off by 90 of 2^-32 at position 2^31
+  const double c0 = 0x1.45f306dc9c883p-3 * 4294967296.0, c1 = -0x1.6b01ec5417056p-57 * 4294967296.0;
   Turns turns;
   for (int f = 0; f < kD / 2; ++f) {
-    const double t = th.th[f] / 6.283185307179586476925286766559 * 4294967296.0, hi = std::rint(t);
+    const double t = th.th[f] * c0, rest = std::fma(th.th[f], c1, std::fma(th.th[f], c0, -t));
+    const double hi = std::rint(t), lo = std::rint(((t - hi) + rest) * 4294967296.0);
     turns.hi[f] = (int32_t)(uint32_t)(int64_t)hi;
-    turns.lo[f] = (int32_t)std::min(std::rint((t - hi) * 4294967296.0), 2147483647.0);
+    turns.lo[f] = (int32_t)std::min(std::max(lo, -2147483648.0), 2147483647.0);
   }
   return turns;
 }

@@ -1,11 +1,14 @@
 """The 8-bit cache where it can go wrong: a workspace sized for larger calls, value
-rows of very different size."""
+rows of very different size, positions near the ends of int32."""
+import fractions
+import math
+
 import numpy as np
 import pytest
 
 import kv_cache_drop_gb300 as akv
 from _kv8 import held, quantise
-from test_gpu_kv8 import Batch, _bits
+from test_gpu_kv8 import Batch, _bits, _dev_pool
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +85,52 @@ def test_a_large_value_row_without_weight(power, Hq, Hkv, dtype):
         tol = (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -18) * size if dtype == "bf16"
                else 2.0 ** -24 * np.abs(want) + 2.0 ** -18 * size)
         assert np.all(np.abs(got[b] - want) <= tol), float(np.abs((got[b] - want) / tol).max())
+
+
+# -------------------------------------------------------------- positions
+
+# 2 pi to 70 digits
+TWO_PI = fractions.Fraction("6.283185307179586476925286766559005768394338798750211641949889184615632")
+
+
+def _turned(theta, pos):
+    """theta * pos modulo 2 pi, in -pi .. pi."""
+    x = fractions.Fraction(theta) * pos
+    x -= round(x / TWO_PI) * TWO_PI
+    return float(x)
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_angles_of_far_positions(base):
+    """Positions near both ends of int32 at which one frequency's angle is next to a
+    whole turn, so that its sine shows the angle's own error.
+
+    The frequency is a double.  Its turn is a product in integers, off by at most one
+    of 2^-32 turns for the floor and, for the frequency's rounding to 2^-64 turns,
+    2^31 * 2^-65 = a quarter of 2^-32 more: by less than 1.3 * 2 pi * 2^-32 < 1.91e-9.
+    The turn's conversion to fp32 and the sine and cosine are good to four roundings
+    of 2^-24 relative to them."""
+    torch = _torch()
+    n = 32
+    thetas = [math.pow(float(np.float32(base)), -2.0 * f / 64) for f in range(n)]
+    pos, rng = [], np.random.default_rng(5)
+    for f in range(n):
+        best = []
+        for sign in (-1, 1):
+            tries = [sign * (2 ** 31 - 2 - int(x)) for x in rng.integers(0, 2 ** 20, 4000)]
+            best.append(min(tries, key=lambda p: abs(math.remainder(thetas[f] * p, 2 * math.pi))))
+        pos += best
+    pos = np.array(pos, np.int64)
+    codes = np.zeros((2 * n, 1, 64), np.uint8)
+    codes[..., :32] = 0x38                                      # 1.0
+    scale = np.full((2 * n, 1), 127, np.uint8)
+    d = _dev_pool((codes, scale, codes, scale))
+    out = [torch.zeros(2 * n, 1, 64, device="cuda") for _ in range(2)]
+    akv.akv_read_kv_q8(akv.shape(1, 1, 64, "f32", base), 2 * n, akv.i32_device(np.arange(2 * n)),
+                       akv.i32_device(pos.astype(np.int32)), None, *d, *out)
+    got = out[0].cpu().numpy().astype(np.float64)[:, 0]
+    for i, p in enumerate(pos):
+        f = i // 2
+        a = _turned(thetas[f], int(p))
+        assert abs(got[i, f + 32] - math.sin(a)) <= 1.91e-9 + 2.0 ** -22 * abs(math.sin(a)), (f, int(p), a)
+        assert abs(got[i, f] - math.cos(a)) <= 1.91e-9 + 2.0 ** -22, (f, int(p), a)
