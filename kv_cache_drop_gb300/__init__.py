@@ -625,8 +625,13 @@ def _run_on(stream):
 
 def _list_bound(kv_indices, max_kv: int) -> int:
     """max_kv; 0 where no list has an entry, as an empty tensor has no address
-    to pass on."""
-    return max_kv if kv_indices.shape[0] else 0
+    to pass on.  None stays for the library to judge: right where max_kv is 0."""
+    return max_kv if kv_indices is None or kv_indices.shape[0] else 0
+
+
+def _like(kv_indices):
+    """The shape of what goes with the lists' entries (None: any)."""
+    return (None,) if kv_indices is None else tuple(kv_indices.shape)
 
 
 def _torch_dtype(shp: Shape):
@@ -699,11 +704,11 @@ def akv_prefix_attention(shp: Shape, n_groups: int, group_indptr, prefix_indptr,
     dt, D, n, S = _torch_dtype(shp), shp.D, q.shape[0], k_pool.shape[0]
     if n_groups == 0:
         max_prefix = 0
-    elif prefix_indices is not None:
+    else:
         max_prefix = _list_bound(prefix_indices, max_prefix)
     if B == 0:
         max_kv = 0
-    elif kv_indices is not None:
+    else:
         max_kv = _list_bound(kv_indices, max_kv)
     _check(lib().akv_prefix_attention(
         ctypes.byref(shp), n_groups, _typed("group_indptr", group_indptr, i32, dev, (n_groups + 1,)),
@@ -827,7 +832,7 @@ def akv_decode_attention_q8(shp: Shape, B: int, q, q_pos, k_new, v_new, new_slot
         _typed("new_slot", new_slot, i32, dev, (B,)), kp, vp, ks, vs, S,
         _typed("kv_indptr", kv_indptr, i32, dev, (B + 1,)),
         _typed("kv_indices", kv_indices, i32, dev, (None,)),
-        _typed("kv_pos", kv_pos, i32, dev, tuple(kv_indices.shape)), _list_bound(kv_indices, max_kv),
+        _typed("kv_pos", kv_pos, i32, dev, _like(kv_indices)), _list_bound(kv_indices, max_kv),
         _typed("out", out, dt, dev, heads), _typed("workspace", workspace, torch.uint8, dev),
         0 if workspace is None else workspace.numel(), st))
 

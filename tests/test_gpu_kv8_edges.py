@@ -1,5 +1,5 @@
 """The 8-bit cache where it can go wrong: a workspace sized for larger calls, value
-rows of very different size, positions near the ends of int32."""
+rows of very different size, positions near the ends of int32, lists left out."""
 import fractions
 import math
 
@@ -8,7 +8,7 @@ import pytest
 
 import kv_cache_drop_gb300 as akv
 from _kv8 import held, quantise
-from test_gpu_kv8 import Batch, _bits, _dev_pool
+from test_gpu_kv8 import Batch, _bits, _dev_pool, _wide
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,33 @@ def test_angles_of_far_positions(base):
         a = _turned(thetas[f], int(p))
         assert abs(got[i, f + 32] - math.sin(a)) <= 1.91e-9 + 2.0 ** -22 * abs(math.sin(a)), (f, int(p), a)
         assert abs(got[i, f] - math.cos(a)) <= 1.91e-9 + 2.0 ** -22, (f, int(p), a)
+
+
+# ------------------------------------------------------------ lists left out
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lists_and_pool_left_out(dtype):
+    """Where max_kv is 0 the lists may be None: every request gets zeros."""
+    torch = _torch()
+    bt = Batch(75, [3, 4], 16, 4, dtype)
+    d = bt.device()
+    out = torch.full_like(d["q"], 7.0)
+    ws = torch.empty(akv.akv_decode_q8_workspace(bt.shp, 2, 0), dtype=torch.uint8, device="cuda")
+    akv.akv_decode_attention_q8(bt.shp, 2, d["q"], d["q_pos"], None, None, None, *d["pool"], d["ptr"], None, None, 0,
+                                out, ws)
+    assert not out.any()
+    with pytest.raises(akv.AkvError):
+        akv.akv_decode_attention_q8(bt.shp, 2, d["q"], d["q_pos"], None, None, None, *d["pool"], d["ptr"], None,
+                                    None, 5, out, ws)
+    with pytest.raises(ValueError):
+        akv.akv_decode_attention_q8(bt.shp, 2, d["q"], d["q_pos"], None, None, None, *d["pool"], d["ptr"], d["idx"],
+                                    d["pos"][:-1], 4, out, ws)
+    assert np.array_equal(_wide(bt.q, dtype), d["q"].float().cpu().numpy())
+    # the chunk calls' lists as well
+    ptr = akv.i32_device([0, 1, 2])
+    lse = torch.zeros(2, 16, device="cuda")
+    pool = torch.zeros(3, 4, 64, dtype=d["q"].dtype, device="cuda")
+    ws = torch.empty(akv.akv_chunk_workspace(bt.shp, 2, 2, 1, 0), dtype=torch.uint8, device="cuda")
+    out.fill_(7.0)
+    akv.akv_chunk_attention(bt.shp, 2, ptr, d["q"], pool, pool, d["ptr"], None, 1, 0, out, lse, ws)
+    assert not out.any() and bool(torch.isneginf(lse).all())
