@@ -32,14 +32,15 @@ struct ChunkReq {
 
 // Rows and lengths are held to the bounds the call was given, so that no row
 // of q, out or a workspace outside them is touched (kv_indptr itself is
-// trusted, as by the decode calls).
+// trusted, as by the decode calls).  kLists: a.whole is false.
+template <bool kLists = false>
 __device__ __forceinline__ ChunkReq chunk_req(const ChunkBatch &a, int b) {
   ChunkReq r;
   r.q0 = max(0, a.q_indptr[b]);
   r.m = max(0, min(min(a.q_indptr[b + 1], a.n_rows) - r.q0, a.max_q));
   r.beg = a.kv_indptr[b];
   r.n = min(max(a.kv_indptr[b + 1] - r.beg, 0), a.max_kv);
-  r.first = a.whole ? r.n : r.n - r.m + 1;
+  r.first = !kLists && a.whole ? r.n : r.n - r.m + 1;
   return r;
 }
 

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kFThreads, 2)
   MassF32Smem &sm = *reinterpret_cast<MassF32Smem *>(smem_raw);
   const int part = blockIdx.x % parts, b = blockIdx.y;
   const int j0 = (int)(blockIdx.x / parts) * kFKeys;
-  const ChunkReq rq = chunk_req(a, b);
+  const ChunkReq rq = chunk_req<true>(a, b);
   if (j0 >= rq.n) return;
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kSHeads * 32, mass_ctas(kRT))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const int b = blockIdx.y, c0 = blockIdx.x * chunk;
-  const ChunkReq rq = chunk_req(a, b);
+  const ChunkReq rq = chunk_req<true>(a, b);
   if (c0 >= rq.n) return;
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   const int nk = min(rq.n - c0, chunk), n_tiles = (nk + kSKeys - 1) / kSKeys;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = blockIdx.x % parts, b = blockIdx.y;
   const int j0 = (int)(blockIdx.x / parts) * kMBlock;
-  const ChunkReq rq = chunk_req(a, b);
+  const ChunkReq rq = chunk_req<true>(a, b);
   if (j0 >= rq.n) return;
   const int grp = a.Hq / a.Hkv, rows = rq.m * grp;
   // row tiles from the first that sees an entry of this block on
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kMThreads, 1)
 __global__ void __launch_bounds__(256)
     mass_join_kernel(const ChunkBatch a, const MassArgs ma, int parts, const float *partial) {
   const int b = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
-  const ChunkReq rq = chunk_req(a, b);
+  const ChunkReq rq = chunk_req<true>(a, b);
   if (j >= rq.n) return;
   float x = 0.f;
 #pragma unroll 4
