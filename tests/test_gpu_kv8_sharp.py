@@ -100,3 +100,23 @@ def test_ranges_of_a_replayed_call():
             want = np.repeat(bt.V[bt.ptr[b]:bt.ptr[b + 1]].sum(0) / max(n, 1), Hq // Hkv, 0)
             assert np.all(np.abs(got[b] - want) <= 1.001 * 2.0 ** -8 * want), (bt.n, b)
     assert akv.akv_decode_q8_workspace(bts[0].shp, 3, 9041) == ws.numel()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lists_inside_longer_arrays(dtype):
+    """kv_indptr need not begin at 0 nor the arrays end with the last list: entries
+    before and behind name rows of NaN."""
+    import torch
+    bt = Batch(41, [900, 0, 33, 2100], 24, 3, dtype, new=True)
+    bt.pool = modest_pool(np.random.default_rng(2), bt.S, 3)
+    spare = np.setdiff1d(np.arange(bt.S), bt.idx)[:1]
+    bt.pool[0][spare], bt.pool[2][spare] = 127, 127
+    d = bt.device()
+    before = bt.run(d)
+    bt.check(before)
+    e = bt.device()
+    pad = lambda x, lo, hi: torch.cat([x.new_full((lo,), int(spare[0])), x, x.new_full((hi,), int(spare[0]))])  # noqa: E731
+    e["idx"], e["pos"], e["ptr"] = pad(e["idx"], 1237, 70), pad(e["pos"], 1237, 70), e["ptr"] + 1237
+    after = bt.run(e)
+    bt.check(after)
+    assert torch.equal(before, after)
