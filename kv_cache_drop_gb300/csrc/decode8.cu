@@ -267,11 +267,12 @@ __global__ void __launch_bounds__(kSThreads)
 // (cp.async), several tiles ahead, and so are list entries, scales and positions
 // (a plain load returns only after the copies queued before it).
 //
-// 14 requests of 20,000 to 90,000 entries, 64 / 8 heads: 162 us the call, 4.7 TB/s
+// 14 requests of 20,000 to 90,000 entries, 64 / 8 heads: 162.5 us the call, 4.7 TB/s
 // (the floor is 111); decode_heads_kernel over bf16 keys before RoPE takes 292 for
-// 766,000 entries, these are 720,000.  252 instructions per 16 entries and head; no pipe is full: with 16 warps per
-// SM the latency of a step's chain bounds it.  With 16 entries a step, or splits of
-// 512 entries instead of ranges, 219 and 256 us.
+// 766,000 entries, these are 720,000.  256 instructions per 16 entries and head; no
+// pipe is full: with 16 warps per SM the latency of a step's chain and its barrier
+// bound it.  With 16 entries a step, or splits of 512 entries instead of ranges, 219
+// and 256 us.
 // ---------------------------------------------------------------------------
 constexpr int kMWarps = 8, kMThreads = 32 * kMWarps, kMKeys = 32;
 // tiles of a warp, and of list entries and positions: what leaves room for two

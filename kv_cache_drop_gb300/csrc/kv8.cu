@@ -14,8 +14,8 @@ constexpr int kEach = kD / kLanes;    // values per lane
 // Bound by HBM: a row is read once (128 or 256 bytes) and written once (64 and
 // a byte).  Four lanes take a head row, 16 values each: the maximum is two
 // shuffles and a lane's codes are one 16-byte store.  16,384 tokens of 8 heads,
-// bf16: 11.2 us on the device, 4.5 TB/s, 14.5 for the call; a few tokens: the
-// host's call, 8.6.
+// bf16: 11.2 us on the device, 4.5 TB/s, 14 to 20 for the call by the host; a few
+// tokens: the host's call, 8.6.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     kv8_append_kernel(int rows, int Hkv, const T *__restrict__ k, int64_t ks,
@@ -50,12 +50,13 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // A warp per entry: its 2 Hkv head rows, four at a time, kFlight such passes in
-// flight (few registers, so that many warps are there too); lane f forms the angle of frequency f once and the lanes fetch theirs by
-// shuffle.  Eight lanes take a head row: lane c holds values 4 c .. 4 c + 3 and the
-// 32 + of these, the two sides of its rotation pairs.  26,081 entries of 8 heads to
-// bf16, rotated: 22 us on the device, 3.7 TB/s (26.6 us the call with one pass at a
-// time and sincosf, 22.7 now).  Bound by scattered rows on both sides: 24 or 40
-// warps per SM take the same time.
+// flight (few registers, so that many warps are there too); lane f forms the angle of
+// frequency f once and the lanes fetch theirs by shuffle.  Eight lanes take a head row:
+// lane c holds values 4 c .. 4 c + 3 and the 32 + of these, the two sides of its
+// rotation pairs.  26,081 entries of 8 heads to bf16, rotated: 22 us on the device, 3.7
+// TB/s (26.6 us the call with one pass at a time and sincosf, 22.6 now).  24 or 40 warps
+// per SM take the same time: the memory pipes are 65 % busy with 4-byte loads and
+// 8-byte stores, 449 instructions an entry, and DRAM is not what bounds it.
 constexpr int kReadLanes = 8, kReadRows = 32 / kReadLanes, kFlight = 4;
 __device__ __forceinline__ void store4(float *to, const float *y) {
   *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
